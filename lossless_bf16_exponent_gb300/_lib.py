@@ -27,6 +27,10 @@ EXPORTS = (
     "uzip_version",
 )
 NOALLOC_MAX_N = 1 << 25
+KV_EXPORTS = (
+    "uzkv_rotary", "uzkv_rotary_append", "uzkv_tree_attention_workspace_bytes", "uzkv_tree_attention",
+    "uzkv_attention_mass", "uzkv_evict",
+)
 
 
 class Info(ctypes.Structure):
@@ -36,6 +40,25 @@ class Info(ctypes.Structure):
         ("version", ctypes.c_uint32), ("flags", ctypes.c_uint32), ("exps", ctypes.c_uint8 * 16),
         ("format", ctypes.c_uint32), ("reserved", ctypes.c_uint32),
     ]
+
+
+class KvCache(ctypes.Structure):
+    """``uzkv_cache_t`` of ``include/uzip_kv.h``."""
+    _fields_ = [
+        ("d_k", ctypes.c_void_p), ("d_v", ctypes.c_void_p),
+        ("k_page_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64), ("k_token_stride", ctypes.c_int64),
+        ("v_page_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64), ("v_token_stride", ctypes.c_int64),
+        ("d_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("d_lengths", ctypes.c_void_p),
+        ("d_status", ctypes.c_void_p), ("pages", ctypes.c_uint32), ("kv_heads", ctypes.c_uint32),
+        ("page_tokens", ctypes.c_uint32), ("head_dim", ctypes.c_uint32), ("sequences", ctypes.c_uint32),
+        ("pages_per_sequence", ctypes.c_uint32), ("dtype", ctypes.c_uint32), ("reserved", ctypes.c_uint32),
+    ]
+
+
+class KvRows(ctypes.Structure):
+    """``uzkv_rows_t`` of ``include/uzip_kv.h``."""
+    _fields_ = [("d", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_t", ctypes.c_int64),
+                ("stride_h", ctypes.c_int64)]
 
 
 class UzipError(RuntimeError):
@@ -91,6 +114,16 @@ def load(path: str | None = None):
               "uzip_encode_dynamic", "uzip_decode", "uzip_stream_copy", "uzip_stream_info", "uzip_version",
               "uzip_e5m2_calibrate", "uzip_e5m2_encode", "uzip_e5m2_decode", "uzip_codebook_make_sentinel",
               "uzip_sentinel_encode", "uzip_sentinel_decode"):
+        getattr(L, f).restype = i
+    f32, i64, cache, rows = ctypes.c_float, ctypes.c_int64, ctypes.POINTER(KvCache), ctypes.POINTER(KvRows)
+    L.uzkv_rotary.argtypes = [rows, rows, u32, u32, u32, u32, u32, vp, i64, vp, u32, u32, f32, i, vp]
+    L.uzkv_rotary_append.argtypes = [rows, rows, rows, rows, u32, u32, u32, vp, i64, vp, u32, u32, f32, vp, cache, vp]
+    L.uzkv_tree_attention_workspace_bytes.argtypes = [u32, u32, u32, u32, u32]
+    L.uzkv_tree_attention_workspace_bytes.restype = sz
+    L.uzkv_tree_attention.argtypes = [rows, rows, vp, u32, u32, u32, vp, i64, vp, f32, cache, vp, sz, vp]
+    L.uzkv_attention_mass.argtypes = [rows, vp, u32, u32, u32, vp, i64, vp, vp, f32, cache, vp, f32, vp, i64, i64, u32, vp]
+    L.uzkv_evict.argtypes = [cache, vp, i64, i64, u32, u32, u32, u32, rows, rows, vp, vp, vp, vp]
+    for f in ("uzkv_rotary", "uzkv_rotary_append", "uzkv_tree_attention", "uzkv_attention_mass", "uzkv_evict"):
         getattr(L, f).restype = i
     if path is None:
         _lib = L

@@ -34,7 +34,7 @@ def _sources():
 
 
 def _inputs():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(INCLUDE, "uzip.h"), __file__]
+    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h")) + [__file__]
 
 
 def stale() -> bool:

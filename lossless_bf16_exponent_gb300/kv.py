@@ -1,0 +1,428 @@
+"""PyTorch front end of the KV-cache operators (``include/uzip_kv.h``): rotary
+positions, attention for a tree of drafted tokens, the attention weight that
+cached tokens collect, and eviction by that weight into a packed buffer that
+:func:`encode` then takes.
+
+As in the codec's front end, this module marshals arguments and checks what
+the C ABI cannot see (devices, types, shapes, strides); a refusal is a
+``ValueError`` raised before anything is enqueued, a status of the library an
+:class:`UzipError`. Work goes to the current CUDA stream of the tensors'
+device and nothing synchronises.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+from dataclasses import dataclass
+
+import torch
+
+from . import _lib
+from ._lib import check
+from .codec import _sp, load
+
+MAX_HEAD_DIM = 256
+MAX_NEW_TOKENS = 256
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.float8_e5m2: 3}
+_LAYOUTS = {"half": 0, "interleaved": 1}
+
+
+def _tensor(t: torch.Tensor, what: str, dtype, shape=None, device=None) -> torch.Tensor:
+    if t.dtype != dtype:
+        raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{what}: expected a CUDA tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{what}: on {t.device}, expected {device}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return t
+
+
+def _dense(t: torch.Tensor, what: str, dtype, shape, device) -> torch.Tensor:
+    if not _tensor(t, what, dtype, shape, device).is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous tensor")
+    return t
+
+
+def _rows(x: torch.Tensor, what: str) -> "_lib.KvRows":
+    """A [sequences, tokens, heads, dim] tensor as the C ABI takes it."""
+    sb, st, sh, sd = x.stride()
+    if sd != 1 and x.shape[3] != 1:
+        raise ValueError(f"{what}: elements of a row must be contiguous")
+    return _lib.KvRows(x.data_ptr(), sb, st, sh)
+
+
+def _writable(x: torch.Tensor, what: str) -> torch.Tensor:
+    """An output: no two of its elements in one place."""
+    expect = 1
+    for n, s in sorted(zip(x.shape, x.stride()), key=lambda v: v[1]):
+        if n > 1 and s < expect:
+            raise ValueError(f"{what}: its elements overlap")
+        if n > 1:
+            expect = s * (n - 1) + expect
+    return x
+
+
+# ----------------------------------------------------------------- rotary
+
+@dataclass(frozen=True)
+class RotaryPlan:
+    """Rates of the pairs of a head, made once and shared by every call."""
+    turns: torch.Tensor  # int64 [rotary_dim / 2]: 64-bit fixed-point turns a position
+    rotary_dim: int
+    layout: str
+    magnitude: float
+
+
+def rotary_rates(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                 original_length: int = 0, low: float = 1.0, high: float = 32.0) -> tuple[list[float], float]:
+    """Radians a position of each pair, and the factor on cosines and sines.
+
+    ``base ** (-2 i / rotary_dim)`` for pair i, and for a context stretched by
+    ``factor``: "linear" divides every rate by it; "base" raises the base to
+    ``base * factor ** (rotary_dim / (rotary_dim - 2))``, which leaves the
+    fastest pair as it is and divides the slowest by ``factor``; "ramp" divides
+    the pairs that turn less than ``low`` times over ``original_length``
+    positions, leaves those that turn more than ``high`` times, mixes linearly
+    between, and scales cosines and sines by ``0.1 ln(factor) + 1``."""
+    if rotary_dim < 2 or rotary_dim % 2 or rotary_dim > MAX_HEAD_DIM:
+        raise ValueError(f"rotary_dim {rotary_dim}: expected an even number in [2, {MAX_HEAD_DIM}]")
+    if not (base > 1.0 and math.isfinite(base) and factor >= 1.0 and math.isfinite(factor)):
+        raise ValueError("expected base > 1 and factor >= 1")
+    if scaling == "base":
+        if rotary_dim == 2:
+            raise ValueError("base scaling needs a rotary_dim above 2")
+        base = base * factor ** (rotary_dim / (rotary_dim - 2))
+    rates = [base ** (-2.0 * i / rotary_dim) for i in range(rotary_dim // 2)]
+    if scaling in ("none", "base"):
+        return rates, 1.0
+    if scaling == "linear":
+        return [f / factor for f in rates], 1.0
+    if scaling == "ramp":
+        if original_length <= 0 or not low < high:
+            raise ValueError("ramp scaling needs original_length > 0 and low < high")
+        out = []
+        for f in rates:
+            turns = original_length * f / (2 * math.pi)
+            g = min(1.0, max(0.0, (turns - low) / (high - low)))
+            out.append(f * (g + (1.0 - g) / factor))
+        return out, 0.1 * math.log(factor) + 1.0
+    raise ValueError(f"scaling {scaling!r}: expected 'none', 'linear', 'base' or 'ramp'")
+
+
+def rotary_plan(rotary_dim: int, base: float = 10000.0, layout: str = "half", scaling: str = "none",
+                factor: float = 1.0, original_length: int = 0, low: float = 1.0, high: float = 32.0,
+                device="cuda") -> RotaryPlan:
+    """The plan of :func:`rotary` and :func:`rotary_append`; see :func:`rotary_rates`
+    for the scalings. ``layout``: "half" turns elements i and i + rotary_dim / 2
+    together, "interleaved" 2 i and 2 i + 1."""
+    if layout not in _LAYOUTS:
+        raise ValueError(f"layout {layout!r}: expected 'half' or 'interleaved'")
+    rates, magnitude = rotary_rates(rotary_dim, base, scaling, factor, original_length, low, high)
+    turns = [int(round(f / (2 * math.pi) * 2.0 ** 64)) for f in rates]
+    turns = torch.tensor([v - (1 << 64) if v >= 1 << 63 else v for v in turns], dtype=torch.int64, device=device)
+    return RotaryPlan(turns, rotary_dim, layout, magnitude)
+
+
+def _rotate(x, positions, plan, out, backward):
+    if x.dtype not in _DTYPES or x.dtype == torch.float8_e5m2:
+        raise ValueError(f"expected bfloat16, float16 or float32 values, got {x.dtype}")
+    if x.dim() not in (3, 4) or not x.is_cuda:
+        raise ValueError("expected a CUDA tensor [tokens, heads, dim] or [sequences, tokens, heads, dim]")
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    else:
+        _writable(_tensor(out, "out", x.dtype, x.shape, x.device), "out")
+    _tensor(positions, "positions", torch.int32, x.shape[:-2], x.device)
+    _tensor(plan.turns, "plan", torch.int64, None, x.device)
+    if x.numel() == 0:
+        return out
+    four, o, pos = (x, out, positions) if x.dim() == 4 else (x[None], out[None], positions[None])
+    if pos.shape[1] > 1 and pos.stride(1) != 1:
+        raise ValueError("positions: expected contiguous rows")
+    b, t, heads, d = four.shape
+    check(load().uzkv_rotary(ctypes.byref(_rows(four, "x")), ctypes.byref(_rows(o, "out")), _DTYPES[x.dtype], b, t,
+                             heads, d, pos.data_ptr(), pos.stride(0), plan.turns.data_ptr(), plan.rotary_dim,
+                             _LAYOUTS[plan.layout], plan.magnitude, backward, _sp(x.device)), "uzkv_rotary")
+    return out
+
+
+def rotary(x: torch.Tensor, positions: torch.Tensor, plan: RotaryPlan,
+           out: torch.Tensor | None = None) -> torch.Tensor:
+    """Turn the pairs of each head of ``x`` ([tokens, heads, dim] or
+    [sequences, tokens, heads, dim], bfloat16, float16 or float32, rows
+    contiguous) by its token's position (int32). Elements past the plan's
+    rotary_dim are copied. ``out`` may be ``x``."""
+    return _rotate(x, positions, plan, out, 0)
+
+
+def rotary_backward(grad: torch.Tensor, positions: torch.Tensor, plan: RotaryPlan,
+                    out: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of :func:`rotary`'s input from that of its output: the same
+    turn, backwards."""
+    return _rotate(grad, positions, plan, out, 1)
+
+
+# ------------------------------------------------------------------ cache
+
+class KVCache:
+    """One layer's cache, as every operator here takes it; made once and kept.
+
+    ``k``, ``v``: pools of pages [pages, kv heads, page tokens, head dim] of
+    bfloat16, float16 or float8_e5m2 (views are fine: rows contiguous, other
+    strides multiples of 16 bytes). ``page_table`` int32 [sequences, pages of a
+    sequence], read for tokens in use only. ``lengths`` int32 [sequences]: tokens
+    of each sequence before the new ones of a call; the tensor is read on the
+    device by each call, so advance it in place. ``status``: None or one int32
+    CUDA element that a call sets to 5 (corrupt) when a length or page number is
+    out of range. A contiguous cache [sequences, heads, tokens, dim] is the
+    pool of whole-sequence pages with ``page_table = arange(sequences)[:, None]``."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, lengths: torch.Tensor,
+                 status: torch.Tensor | None = None):
+        if k.dim() != 4 or k.dtype not in _DTYPES or k.dtype == torch.float32:
+            raise ValueError("k: expected [pages, kv heads, page tokens, head dim] of bfloat16, float16 or float8_e5m2")
+        _tensor(k, "k", k.dtype)
+        _tensor(v, "v", k.dtype, k.shape, k.device)
+        if page_table.dim() != 2:
+            raise ValueError("page_table: expected [sequences, pages of a sequence]")
+        _tensor(page_table, "page_table", torch.int32, None, k.device)
+        if page_table.shape[1] > 1 and page_table.stride(1) != 1:
+            raise ValueError("page_table: expected contiguous rows")
+        _dense(lengths, "lengths", torch.int32, page_table.shape[:1], k.device)
+        if status is not None:
+            _dense(status, "status", torch.int32, torch.Size([1]), k.device)
+        for t, what in ((k, "k"), (v, "v")):
+            _writable(t, what)
+            if t.shape[3] > 1 and t.stride(3) != 1:
+                raise ValueError(f"{what}: elements of a row must be contiguous")
+        self.k, self.v, self.page_table, self.lengths, self.status = k, v, page_table, lengths, status
+        self.device, self.dtype = k.device, k.dtype
+        self.sequences, self.kv_heads, self.head_dim = page_table.shape[0], k.shape[1], k.shape[3]
+        self.page_tokens = k.shape[2]
+        self.capacity = page_table.shape[1] * k.shape[2]
+        self._c = _lib.KvCache(
+            k.data_ptr(), v.data_ptr(), *k.stride()[:3], *v.stride()[:3], page_table.data_ptr(), page_table.stride(0),
+            lengths.data_ptr(), status.data_ptr() if status is not None else None, k.shape[0], k.shape[1], k.shape[2],
+            k.shape[3], page_table.shape[0], page_table.shape[1], _DTYPES[k.dtype], 0)
+        self._ref = ctypes.byref(self._c)
+
+
+def _new_rows(x: torch.Tensor, what: str, cache: KVCache, heads: int | None = None):
+    """Check new tokens' rows [sequences, tokens, heads, head dim] of a cache."""
+    if x.dim() != 4 or x.shape[0] != cache.sequences or x.shape[3] != cache.head_dim or not x.is_cuda \
+            or x.device != cache.device or (heads is not None and x.shape[2] != heads):
+        raise ValueError(f"{what}: expected [{cache.sequences}, tokens, {heads or 'heads'}, {cache.head_dim}] "
+                         f"on {cache.device}, got {tuple(x.shape)} on {x.device}")
+    if x.dtype not in (torch.bfloat16, torch.float16) or cache.dtype not in (x.dtype, torch.float8_e5m2):
+        raise ValueError(f"{what}: {x.dtype} does not go with a cache of {cache.dtype}")
+    return x
+
+
+def _counts(counts, cache):
+    return _dense(counts, "counts", torch.int32, (cache.sequences,), cache.device).data_ptr() if counts is not None else None
+
+
+def rotary_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, plan: RotaryPlan,
+                  cache: KVCache, counts: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Rotate the queries and keys of new tokens, store keys and values in the
+    cache at slots lengths .. lengths + counts - 1 (rounded once to its type) and
+    return the rotated queries, in one launch. ``q`` [sequences, tokens, query
+    heads, dim], ``k`` and ``v`` [sequences, tokens, kv heads, dim] (views of one
+    projection are fine), ``positions`` int32 [sequences, tokens]. Tokens at or
+    past ``counts`` give zero queries and are not stored. ``out`` may be ``q``.
+    Advancing ``cache.lengths`` is the caller's, once the tokens are accepted."""
+    _new_rows(q, "q", cache)
+    b, t, heads, d = q.shape
+    for x, what in ((k, "k"), (v, "v")):
+        _new_rows(x, what, cache, cache.kv_heads)
+        if x.dtype != q.dtype or x.shape[1] != t:
+            raise ValueError(f"{what}: type or tokens differ from q's")
+    _tensor(positions, "positions", torch.int32, q.shape[:2], q.device)
+    if t > 1 and positions.stride(1) != 1:
+        raise ValueError("positions: expected contiguous rows")
+    _tensor(plan.turns, "plan", torch.int64, None, q.device)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    else:
+        _writable(_tensor(out, "out", q.dtype, q.shape, q.device), "out")
+    if q.numel() == 0:
+        return out
+    ref = ctypes.byref
+    check(load().uzkv_rotary_append(ref(_rows(q, "q")), ref(_rows(k, "k")), ref(_rows(v, "v")), ref(_rows(out, "out")),
+                                    _DTYPES[q.dtype], t, heads, positions.data_ptr(), positions.stride(0),
+                                    plan.turns.data_ptr(), plan.rotary_dim, _LAYOUTS[plan.layout], plan.magnitude,
+                                    _counts(counts, cache), cache._ref, _sp(q.device)), "uzkv_rotary_append")
+    return out
+
+
+# -------------------------------------------------------------- attention
+
+def tree_mask(parents, device="cuda") -> torch.Tensor:
+    """Mask rows of drafted trees: ``parents[b][t]`` is the node that token t of
+    sequence b continues, or -1 for one that continues the cache; a parent comes
+    before its child. Returns int64 [sequences, tokens, ceil(tokens / 64)]: bit u
+    of row t is set where u is t or an ancestor of t."""
+    rows = [[int(u) for u in row] for row in parents]
+    t = len(rows[0]) if rows else 0
+    if not 1 <= t <= MAX_NEW_TOKENS or any(len(r) != t for r in rows):
+        raise ValueError(f"parents: expected rows of one length in [1, {MAX_NEW_TOKENS}]")
+    words = -(-t // 64)
+    out = []
+    for row in rows:
+        seen: list[int] = []
+        for i, u in enumerate(row):
+            if not -1 <= u < i:
+                raise ValueError(f"parents: node {i} has parent {u}")
+            seen.append((seen[u] if u >= 0 else 0) | 1 << i)
+        out.append([[(w - (1 << 64) if w >= 1 << 63 else w)
+                     for w in ((s >> 64 * j) & ((1 << 64) - 1) for j in range(words))] for s in seen])
+    return torch.tensor(out, dtype=torch.int64, device=device)
+
+
+def _mask(mask, cache, t):
+    """(address, words between sequences) of a mask."""
+    if mask is None:
+        return None, 0
+    words = -(-t // 64)
+    if mask.dim() != 3 or mask.shape[0] not in (1, cache.sequences) or mask.shape[1:] != (t, words):
+        raise ValueError(f"mask: expected [{cache.sequences} or 1, {t}, {words}], got {tuple(mask.shape)}")
+    _dense(mask, "mask", torch.int64, None, cache.device)
+    return mask.data_ptr(), 0 if mask.shape[0] == 1 else t * words
+
+
+def _query(q: torch.Tensor, cache: KVCache):
+    _new_rows(q, "q", cache)
+    if not 1 <= q.shape[1] <= MAX_NEW_TOKENS:
+        raise ValueError(f"q: {q.shape[1]} new tokens, expected 1 to {MAX_NEW_TOKENS}")
+    if q.shape[2] == 0 or q.shape[2] % cache.kv_heads:
+        raise ValueError(f"q: {q.shape[2]} heads over {cache.kv_heads} kv heads")
+    return q
+
+
+def tree_attention_workspace_bytes(cache: KVCache, tokens: int, heads: int) -> int:
+    return int(load().uzkv_tree_attention_workspace_bytes(cache.sequences, tokens, heads, cache.kv_heads,
+                                                          cache.head_dim))
+
+
+def tree_attention(q: torch.Tensor, cache: KVCache, mask: torch.Tensor | None = None,
+                   counts: torch.Tensor | None = None, scale: float | None = None, out: torch.Tensor | None = None,
+                   lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """Attention of new tokens over the cache that already holds their keys and
+    values (:func:`rotary_append`). ``q`` [sequences, tokens, query heads, dim],
+    1 to 256 tokens; token t sees the first lengths slots and the new tokens of
+    its mask row (:func:`tree_mask`; one tree for all when the mask has one
+    sequence; None: a chain, each token and those before it). Returns ``(out,
+    lse)``: the output, and the float32 log-sum-exp [sequences, tokens, heads].
+    Rows that see nothing, and tokens at or past ``counts``, give 0 and -inf."""
+    _query(q, cache)
+    b, t, heads, d = q.shape
+    address, stride = _mask(mask, cache, t)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    else:
+        _writable(_tensor(out, "out", q.dtype, q.shape, q.device), "out")
+    if lse is None:
+        lse = torch.empty((b, t, heads), dtype=torch.float32, device=q.device)
+    else:
+        _dense(lse, "lse", torch.float32, (b, t, heads), q.device)
+    if workspace is None:
+        workspace = torch.empty(tree_attention_workspace_bytes(cache, t, heads), dtype=torch.uint8, device=q.device)
+    elif not _tensor(workspace, "workspace", torch.uint8, None, q.device).is_contiguous():
+        raise ValueError("workspace: expected a contiguous tensor")
+    check(load().uzkv_tree_attention(ctypes.byref(_rows(q, "q")), ctypes.byref(_rows(out, "out")), lse.data_ptr(),
+                                     _DTYPES[q.dtype], t, heads, address, stride, _counts(counts, cache),
+                                     d ** -0.5 if scale is None else scale, cache._ref, workspace.data_ptr(),
+                                     workspace.numel(), _sp(q.device)), "uzkv_tree_attention")
+    return out, lse
+
+
+def attention_mass(q: torch.Tensor, cache: KVCache, lse: torch.Tensor, mask: torch.Tensor | None = None,
+                   counts: torch.Tensor | None = None, weights: torch.Tensor | None = None,
+                   mass: torch.Tensor | None = None, decay: float = 1.0, scale: float | None = None,
+                   out: torch.Tensor | None = None) -> torch.Tensor:
+    """The attention weight that each cached token collects: float32 [sequences,
+    kv heads, slots], ``decay * mass`` for the tokens already in the cache plus,
+    over the group's heads and the new tokens that see it, ``weights[b, t] *
+    exp(score - lse)``; 0 for slots not in use. ``q``, ``mask``, ``counts`` and
+    ``scale`` as for the :func:`tree_attention` that gave ``lse``; ``weights``
+    float32 [sequences, tokens] (1 for accepted tokens, 0 for the others; None:
+    ones). ``out`` may be ``mass``; its width (default: the cache's capacity) says
+    how many slots are weighed."""
+    _query(q, cache)
+    b, t, heads, d = q.shape
+    address, stride = _mask(mask, cache, t)
+    _dense(lse, "lse", torch.float32, (b, t, heads), q.device)
+    if weights is not None:
+        _dense(weights, "weights", torch.float32, (b, t), q.device)
+    if out is None:
+        out = torch.empty(mass.shape if mass is not None else (b, cache.kv_heads, cache.capacity),
+                          dtype=torch.float32, device=q.device)
+    _tensor(out, "out", torch.float32, None, q.device)
+    if out.dim() != 3 or out.shape[:2] != (b, cache.kv_heads) or not 1 <= out.shape[2] <= cache.capacity:
+        raise ValueError(f"out: expected [{b}, {cache.kv_heads}, 1 to {cache.capacity}], got {tuple(out.shape)}")
+    _writable(out, "out")
+    if mass is not None:
+        _tensor(mass, "mass", torch.float32, out.shape, q.device)
+    for x, what in ((out, "out"), (mass, "mass")):
+        if x is not None and (x.shape[2] > 1 and x.stride(2) != 1 or x.stride() != out.stride()):
+            raise ValueError(f"{what}: expected contiguous rows and the strides of out")
+    check(load().uzkv_attention_mass(ctypes.byref(_rows(q, "q")), lse.data_ptr(), _DTYPES[q.dtype], t, heads, address,
+                                     stride, _counts(counts, cache), weights.data_ptr() if weights is not None else None,
+                                     d ** -0.5 if scale is None else scale, cache._ref,
+                                     mass.data_ptr() if mass is not None else None, decay, out.data_ptr(),
+                                     out.stride(0), out.stride(1), out.shape[2], _sp(q.device)), "uzkv_attention_mass")
+    return out
+
+
+# --------------------------------------------------------------- eviction
+
+@dataclass
+class Packed:
+    """What :func:`evict` keeps: ``k``, ``v`` [sequences, kv heads, keep, dim],
+    ``mass`` float32 and ``kept`` int32 [sequences, kv heads, keep] (slots in
+    ascending order), ``lengths`` int32 [sequences]. Rows past a sequence's length
+    are zero, -1 in ``kept``."""
+    k: torch.Tensor
+    v: torch.Tensor
+    mass: torch.Tensor
+    kept: torch.Tensor
+    lengths: torch.Tensor
+
+
+def evict(cache: KVCache, mass: torch.Tensor, keep: int, sink: int = 0, recent: int = 0,
+          out_k: torch.Tensor | None = None, out_v: torch.Tensor | None = None) -> Packed:
+    """Keep ``keep`` tokens of each sequence and head and pack them: the first
+    ``sink``, the last ``recent`` and those of the largest ``mass`` (float32
+    [sequences, kv heads, slots]; equal masses: the lowest slot first). A sequence
+    of at most ``keep`` tokens keeps them all. ``out_k`` and ``out_v`` default to
+    two halves of one contiguous buffer, ready for :func:`encode`; given ones may
+    be views with room behind for tokens to come, but no part of the cache."""
+    b, heads, d = cache.sequences, cache.kv_heads, cache.head_dim
+    _tensor(mass, "mass", torch.float32, None, cache.device)
+    if mass.dim() != 3 or mass.shape[:2] != (b, heads) or mass.shape[2] < 1:
+        raise ValueError(f"mass: expected [{b}, {heads}, slots], got {tuple(mass.shape)}")
+    if mass.shape[2] > 1 and mass.stride(2) != 1:
+        raise ValueError("mass: expected contiguous rows")
+    if keep < 1 or sink < 0 or recent < 0 or sink + recent > keep:
+        raise ValueError("expected keep >= 1 and 0 <= sink + recent <= keep")
+    shape = (b, heads, keep, d)
+    if out_k is None and out_v is None:
+        out_k, out_v = torch.empty((2, *shape), dtype=cache.dtype, device=cache.device)
+    elif out_k is None or out_v is None:
+        raise ValueError("give both out_k and out_v or neither")
+    for x, what in ((out_k, "out_k"), (out_v, "out_v")):
+        _writable(_tensor(x, what, cache.dtype, shape, cache.device), what)
+    kept = torch.empty((b, heads, keep), dtype=torch.int32, device=cache.device)
+    mass_out = torch.empty((b, heads, keep), dtype=torch.float32, device=cache.device)
+    lengths = torch.empty((b,), dtype=torch.int32, device=cache.device)
+    check(load().uzkv_evict(cache._ref, mass.data_ptr(), mass.stride(0), mass.stride(1), mass.shape[2], keep, sink,
+                            recent, ctypes.byref(_rows(out_k, "out_k")), ctypes.byref(_rows(out_v, "out_v")),
+                            kept.data_ptr(), mass_out.data_ptr(), lengths.data_ptr(), _sp(cache.device)), "uzkv_evict")
+    return Packed(out_k, out_v, mass_out, kept, lengths)
+
+
+__all__ = ["KVCache", "MAX_HEAD_DIM", "MAX_NEW_TOKENS", "Packed", "RotaryPlan", "attention_mass", "evict", "rotary",
+           "rotary_append", "rotary_backward", "rotary_plan", "rotary_rates", "tree_attention",
+           "tree_attention_workspace_bytes", "tree_mask"]
