@@ -1,93 +1,117 @@
-// attention.cu -- attention for a tree of drafted tokens over a paged cache,
-// and the attention weight that each cached token collects.
-//
-// First form: one CTA a query row (attention), one thread a cached token
-// (mass), in 32-bit floats.
+// attention.cu -- entry points of attention for a tree of drafted tokens over a
+// paged cache and of the attention weight that each cached token collects; the
+// kernel that joins the partial results of units that several CTAs shared.
 #include <algorithm>
 
-#include "kv_internal.cuh"
+#include "kv_attention.cuh"
 
 namespace uzkv {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
-
-struct Params {
-    Rows q, out;
-    float* lse;
-    const int64_t* mask;
-    int64_t mask_b;
-    uint32_t mask_words;
-    const int32_t* counts;
-    const float* weights;
-    Cache cache;
-    float scale;
-    uint32_t tokens, q_heads, group;
-    const float* mass_in;
-    float* mass_out;
-    float decay;
-    int64_t mass_b, mass_h;
-    uint32_t slots;
-};
+constexpr int kThreads = 128;
+using Params = AttParams;
 
 __device__ __forceinline__ const int64_t* mask_row(const Params& p, uint32_t b, uint32_t t) {
     return p.mask ? p.mask + b * p.mask_b + (uint64_t)t * p.mask_words : nullptr;
 }
 
-// Grid (tokens, q_heads, sequences).
-template <typename T, typename C>
-__global__ void __launch_bounds__(kThreads) attend_rows_kernel(const __grid_constant__ Params p) {
-    constexpr int kPer = UZKV_MAX_HEAD_DIM / 32;
-    __shared__ float acc_s[kWarps][UZKV_MAX_HEAD_DIM];
-    __shared__ float m_s[kWarps], l_s[kWarps];
-    const uint32_t t = blockIdx.x, hq = blockIdx.y, b = blockIdx.z, h = hq / p.group;
-    const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32, d = p.cache.head_dim;
-    const Span sp = span_of(p.cache, p.counts, p.tokens, b);
-    const int64_t* mask = mask_row(p, b, t);
-    const T* q = reinterpret_cast<const T*>(p.q.p + b * p.q.b + t * p.q.t + hq * p.q.h);
-    float qr[kPer], o[kPer], m = -INFINITY, l = 0.0f;
-    for (int i = 0; i < kPer; i++) {
-        qr[i] = lane + 32 * i < d ? to_f32(q[lane + 32 * i]) * p.scale : 0.0f;
-        o[i] = 0.0f;
+// Join: one warp a query row. Launched as a programmatic dependent of the attention kernel, so that finding its
+// unit's share of the split overlaps that kernel; rows of units that one CTA finished are already written. Also
+// writes the rows of sequences without new tokens, which have no tiles.
+template <typename QT>
+__global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ Params p) {
+    const uint32_t lane = threadIdx.x % 32;
+    const uint64_t w = (uint64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
+    const uint64_t per = (uint64_t)p.cache.kv_heads * p.rows;
+    const uint32_t b = (uint32_t)(w / per), h = (uint32_t)(w % per / p.rows), row = (uint32_t)(w % p.rows);
+    if (b >= p.cache.sequences) {
+        uzip::pdl_wait();
+        return;
     }
-    const uint32_t n = t < sp.fresh ? sp.old + sp.fresh : 0;
-    for (uint32_t j = warp; j < n; j += kWarps) {
-        if (j >= sp.old && !mask_bit(mask, t, j - sp.old)) continue;
-        const Place at = place_of(p.cache, b, j);
-        if (at.page < 0) continue;
-        const C* k = reinterpret_cast<const C*>(k_row(p.cache, at, h));
-        const C* v = reinterpret_cast<const C*>(v_row(p.cache, at, h));
-        float s = 0.0f;
-        for (int i = 0; i < kPer; i++)
-            if (lane + 32 * i < d) s += qr[i] * to_f32(k[lane + 32 * i]);
-        for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, x);
-        const float mn = s > m ? s : m;  // NaN leaves m as it is and comes in through exp
-        const float base = mn == -INFINITY ? 0.0f : mn;
-        const float f = expf(m - base), e = expf(s - base);
-        m = mn;
-        l = l * f + e;
-        for (int i = 0; i < kPer; i++)
-            if (lane + 32 * i < d) o[i] = o[i] * f + e * to_f32(v[lane + 32 * i]);
+    uint64_t total = 0, before = 0;
+    for (uint32_t i = lane; i < p.cache.sequences; i += 32) {
+        const uint32_t n = tiles_of(p, i);
+        total += n;
+        before += i < b ? n : 0;
     }
-    for (int i = 0; i < kPer; i++) acc_s[warp][lane + 32 * i] = o[i];
-    if (lane == 0) {
-        m_s[warp] = m;
-        l_s[warp] = l;
+    for (int o = 16; o; o >>= 1) {
+        total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
+        before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
     }
-    __syncthreads();
-    float top = -INFINITY, sum = 0.0f;
-    for (int w = 0; w < kWarps; w++) top = fmaxf(top, m_s[w]);
-    const float base = top == -INFINITY ? 0.0f : top;
-    for (int w = 0; w < kWarps; w++) sum += l_s[w] * expf(m_s[w] - base);
-    T* out = reinterpret_cast<T*>(p.out.p + b * p.out.b + t * p.out.t + hq * p.out.h);
-    for (uint32_t i = threadIdx.x; i < d; i += kThreads) {
-        float x = 0.0f;
-        for (int w = 0; w < kWarps; w++) x += acc_s[w][i] * expf(m_s[w] - base);
-        out[i] = from_f32<T>(sum == 0.0f ? 0.0f : x / sum);
+    const uint32_t tiles = tiles_of(p, b), mt = row / p.m, r = row % p.m;
+    const uint64_t units = (uint64_t)p.cache.kv_heads * p.mtiles;
+    total *= units;
+    const uint64_t start = before * units + ((uint64_t)h * p.mtiles + mt) * tiles;
+    const uint64_t shares = min(total, (uint64_t)p.grid);
+    // CTA c has the tiles from total * c / shares on
+    uint32_t c0 = 0, c1 = 0;
+    if (tiles) {
+        c0 = (uint32_t)(((start + 1) * shares - 1) / total);
+        c1 = (uint32_t)(((start + tiles) * shares - 1) / total);
     }
-    if (p.lse && threadIdx.x == 0)
-        p.lse[((uint64_t)b * p.tokens + t) * p.q_heads + hq] = sum == 0.0f ? -INFINITY : base + logf(sum);
+    uzip::pdl_wait();
+    if (tiles && c0 == c1) return;
+    const uint32_t t = row / p.group, hq = h * p.group + row % p.group;
+    char* out = p.out.p + b * p.out.b + t * p.out.t + (uint64_t)hq * p.out.h;
+    const uint64_t size = partial_floats(p);
+    auto part_of = [&](uint32_t c) { return p.partial + ((uint64_t)c * 2 + (c == c0)) * size; };
+
+    float top = -INFINITY;
+    if (tiles)
+        for (uint32_t c = c0 + lane; c <= c1; c += 32) {
+            const float2 st = *reinterpret_cast<const float2*>(part_of(c) + (uint64_t)p.m * p.dp + 2 * r);
+            if (st.y != 0.0f) top = fmaxf(top, st.x);
+        }
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    float sum = 0.0f;
+    float4 acc[2] = {make_float4(0, 0, 0, 0), make_float4(0, 0, 0, 0)};
+    if (tiles)
+#pragma unroll 4
+        for (uint32_t c = c0; c <= c1; c++) {
+            const float* part = part_of(c);
+            const float2 st = *reinterpret_cast<const float2*>(part + (uint64_t)p.m * p.dp + 2 * r);
+            const float f = st.y == 0.0f ? 0.0f : exp2_fast(st.x - top);
+            sum += st.y * f;
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                const uint32_t d = 4 * lane + 128 * i;
+                if (d >= p.cache.head_dim || st.y == 0.0f) continue;
+                const float4 v = *reinterpret_cast<const float4*>(part + (uint64_t)r * p.dp + d);
+                acc[i].x += v.x * f;
+                acc[i].y += v.y * f;
+                acc[i].z += v.z * f;
+                acc[i].w += v.w * f;
+            }
+        }
+    const bool none = sum == 0.0f;
+    const float inv = none ? 0.0f : 1.0f / sum;
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        const uint32_t d = 4 * lane + 128 * i;
+        if (d >= p.cache.head_dim) continue;
+        *reinterpret_cast<uint2*>(out + 2 * d) =
+            none ? make_uint2(0, 0) : make_uint2(pack2<QT>(acc[i].x * inv, acc[i].y * inv), pack2<QT>(acc[i].z * inv, acc[i].w * inv));
+    }
+    if (p.lse && lane == 0)
+        p.lse[((uint64_t)b * p.tokens + t) * p.q_heads + hq] = none ? -INFINITY : (top + log2f(sum)) * kLn2;
+}
+
+template <typename QT>
+int launch_join(const Params& p, cudaStream_t s) {
+    const uint64_t warps = (uint64_t)p.cache.sequences * p.cache.kv_heads * p.rows;
+    const uint64_t grid = (warps + kThreads / 32 - 1) / (kThreads / 32);
+    if (grid > 0x7FFFFFFFull) return UZIP_ERR_ARG;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    UZIP_CUDA_TRY(cudaLaunchKernelEx(&cfg, join_kernel<QT>, p));
+    return UZIP_OK;
 }
 
 // Grid (slots / kThreads, kv_heads, sequences).
@@ -120,12 +144,6 @@ __global__ void __launch_bounds__(kThreads) mass_rows_kernel(const __grid_consta
 }
 
 template <typename T, typename C>
-int launch_attend(const Params& p, cudaStream_t s) {
-    attend_rows_kernel<T, C><<<dim3(p.tokens, p.q_heads, p.cache.sequences), kThreads, 0, s>>>(p);
-    UZIP_CUDA_TRY(cudaGetLastError());
-    return UZIP_OK;
-}
-template <typename T, typename C>
 int launch_mass(const Params& p, cudaStream_t s) {
     mass_rows_kernel<T, C><<<dim3((p.slots + kThreads - 1) / kThreads, p.cache.kv_heads, p.cache.sequences), kThreads, 0, s>>>(p);
     UZIP_CUDA_TRY(cudaGetLastError());
@@ -150,6 +168,7 @@ int common(Params& p, const uzkv_rows_t* q, uint32_t dtype, uint32_t tokens, uin
     p.tokens = tokens;
     p.q_heads = q_heads;
     p.group = q_heads / cache->kv_heads;
+    p.rows = tokens * p.group;
     return UZIP_OK;
 }
 
@@ -163,7 +182,9 @@ extern "C" UZIP_API size_t uzkv_tree_attention_workspace_bytes(uint32_t sequence
     if (!sequences || !tokens || tokens > UZKV_MAX_NEW_TOKENS || !q_heads || !kv_heads || q_heads % kv_heads ||
         !head_dim || head_dim > UZKV_MAX_HEAD_DIM)
         return 0;
-    return 16;
+    const uint64_t rows = (uint64_t)tokens * (q_heads / kv_heads), m = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    const uint64_t dp = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
+    return (size_t)(kMaxAttGrid * 2 * m * (dp + 2) * 4);
 }
 
 extern "C" UZIP_API int uzkv_tree_attention(const uzkv_rows_t* q, const uzkv_rows_t* out, float* d_lse, uint32_t dtype,
@@ -179,11 +200,17 @@ extern "C" UZIP_API int uzkv_tree_attention(const uzkv_rows_t* q, const uzkv_row
     if (workspace_bytes < uzkv_tree_attention_workspace_bytes(p.cache.sequences, tokens, q_heads, p.cache.kv_heads, p.cache.head_dim))
         return UZIP_ERR_CAPACITY;
     p.lse = d_lse;
+    p.partial = static_cast<float*>(d_workspace);
+    int sms = 0;
+    if (int rc = sm_count(&sms)) return rc;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const bool fp8 = cache->dtype == UZKV_E5M2;
-    if (dtype == UZKV_BF16)
-        return fp8 ? launch_attend<__nv_bfloat16, E5M2>(p, s) : launch_attend<__nv_bfloat16, __nv_bfloat16>(p, s);
-    return fp8 ? launch_attend<__half, E5M2>(p, s) : launch_attend<__half, __half>(p, s);
+    if (dtype == UZKV_BF16) {
+        if (int rc = fp8 ? attend_bf16_e5m2(p, sms, s) : attend_bf16(p, sms, s)) return rc;
+        return launch_join<__nv_bfloat16>(p, s);
+    }
+    if (int rc = fp8 ? attend_fp16_e5m2(p, sms, s) : attend_fp16(p, sms, s)) return rc;
+    return launch_join<__half>(p, s);
 }
 
 extern "C" UZIP_API int uzkv_attention_mass(const uzkv_rows_t* q, const float* d_lse, uint32_t dtype, uint32_t tokens,

@@ -1,0 +1,297 @@
+// kv_attention.cuh -- what the attention and mass kernels share: parameters,
+// the split of the cache's tiles over the grid, masks, and the warp-level
+// matrix products on 16-bit and E5M2 rows in shared memory.
+//
+// Rows. The group's query heads of all new tokens of one (sequence, KV head)
+// are rows of one product: row r is token r / group, head r % group, so a
+// cached row is read once for all of them.
+//
+// Shared-memory rows are 64, 128, 256 or 512 bytes, in 16-byte chunks whose
+// number is XORed with the row's, so that the eight rows that a matrix load
+// takes at one chunk lie in eight different bank groups.
+//
+// E5M2 rows stay bytes in shared memory. E5M2 is the upper byte of FP16, so a
+// byte permute widens two of them to a pair that the FP16 product takes. A
+// matrix load of 16-bit units gives a thread four consecutive bytes of a key
+// row, where the product's layout wants two pairs eight apart; the sum over
+// the head dimension may run in any order, so the queries are read in the
+// same permuted one. For the values, a transposed load gives the bytes of two
+// neighbouring columns; they go to two products, one for the even and one for
+// the odd columns.
+#pragma once
+
+#include <type_traits>
+
+#include "kv_internal.cuh"
+
+namespace uzkv {
+
+constexpr int kAttThreads = 128;
+constexpr uint32_t kTile = 64;          // cached tokens a step
+constexpr uint32_t kMaxAttGrid = 320;   // bounds the workspace: two CTAs on each of up to 160 SMs
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct AttParams {
+    Rows q, out;
+    float* lse;
+    const int64_t* mask;
+    int64_t mask_b;
+    uint32_t mask_words;
+    const int32_t* counts;
+    const float* weights;
+    Cache cache;
+    float scale;
+    uint32_t tokens, q_heads, group;
+    uint32_t rows;     // tokens * group
+    uint32_t mtiles;   // row tiles of a (sequence, KV head)
+    uint32_t m;        // rows of a tile
+    uint32_t dp;       // floats a row of a partial result takes
+    uint32_t grid;     // CTAs the tiles are split over
+    float* partial;    // [grid][2] results: m rows of dp floats, then m (reference, sum) pairs
+    const float* mass_in;
+    float* mass_out;
+    float decay;
+    int64_t mass_b, mass_h;
+    uint32_t slots;
+};
+
+__device__ __forceinline__ uint64_t partial_floats(const AttParams& p) { return (uint64_t)p.m * (p.dp + 2); }
+
+// ------------------------------------------------------------------- split
+//
+// The tiles of all (sequence, KV head, row tile) units in this order, cut into
+// equal runs, one a CTA: sequences of any lengths load all SMs alike. A unit
+// that several CTAs share leaves partial results: a CTA's first unit in its
+// slot 0 where the unit began before it, its last unit in slot 1 where the
+// unit goes on after it.
+
+struct Unit {
+    uint32_t b, h, mt, tile, tiles;
+    Span span;
+};
+
+__device__ __forceinline__ uint32_t tiles_of(const Span& s) {
+    return s.fresh ? (s.old + s.fresh + kTile - 1) / kTile : 0;
+}
+
+__device__ __forceinline__ uint32_t tiles_of(const AttParams& p, uint32_t b) {
+    return b < p.cache.sequences ? tiles_of(span_of(p.cache, p.counts, p.tokens, b)) : 0;
+}
+
+// All lanes of a warp: tiles of all sequences, one (head, row tile) each.
+__device__ __forceinline__ uint64_t all_tiles(const AttParams& p) {
+    uint64_t n = 0;
+    for (uint32_t b = threadIdx.x % 32; b < p.cache.sequences; b += 32) n += tiles_of(p, b);
+    for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
+    return n;
+}
+
+// All lanes of a warp: the unit and tile at position `at` of the order, at < all tiles * per.
+__device__ __forceinline__ Unit unit_at(const AttParams& p, uint64_t at, uint32_t mtiles) {
+    const uint32_t lane = threadIdx.x % 32;
+    const uint64_t per = (uint64_t)p.cache.kv_heads * mtiles;
+    uint64_t before = 0;
+    Unit u{};
+    for (uint32_t b0 = 0; b0 < p.cache.sequences; b0 += 32) {
+        const uint64_t mine = tiles_of(p, b0 + lane);
+        uint64_t upto = mine;
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+            if (lane >= (uint32_t)o) upto += v;
+        }
+        const uint32_t past = __ballot_sync(0xFFFFFFFFu, (before + upto) * per > at);
+        if (past) {
+            const int l = __ffs(past) - 1;
+            const uint64_t start = __shfl_sync(0xFFFFFFFFu, before + upto - mine, l) * per;
+            u.b = b0 + l;
+            u.tiles = (uint32_t)__shfl_sync(0xFFFFFFFFu, mine, l);
+            const uint64_t in = at - start;
+            const uint32_t unit = (uint32_t)(in / u.tiles);
+            u.tile = (uint32_t)(in % u.tiles);
+            u.h = unit / mtiles;
+            u.mt = unit % mtiles;
+            u.span = span_of(p.cache, p.counts, p.tokens, u.b);
+            return u;
+        }
+        before += __shfl_sync(0xFFFFFFFFu, upto, 31);
+    }
+    return u;
+}
+
+__device__ __forceinline__ void advance(const AttParams& p, Unit& u, uint32_t mtiles) {
+    if (++u.tile < u.tiles) return;
+    u.tile = 0;
+    if (++u.mt < mtiles) return;
+    u.mt = 0;
+    if (++u.h < p.cache.kv_heads) return;
+    u.h = 0;
+    do {
+        if (++u.b >= p.cache.sequences) return;
+        u.span = span_of(p.cache, p.counts, p.tokens, u.b);
+        u.tiles = tiles_of(u.span);
+    } while (!u.tiles);
+}
+
+// ------------------------------------------------------------------- masks
+
+// Which of the slots j0 .. j0 + 63 row r sees, as bits.
+__device__ __forceinline__ uint64_t seen_bits(const AttParams& p, uint32_t b, const Span& s, uint32_t row, uint32_t j0) {
+    const uint32_t t = row / p.group;
+    if (row >= p.rows || t >= s.fresh) return 0;
+    const int64_t u0 = (int64_t)j0 - s.old;
+    if (u0 <= -64) return ~0ull;
+    const int64_t* w = p.mask ? p.mask + b * p.mask_b + (uint64_t)t * p.mask_words : nullptr;
+    auto word = [&](uint32_t i) -> uint64_t {
+        if (w) return i < p.mask_words ? (uint64_t)w[i] : 0;
+        const int32_t n = (int32_t)t + 1 - (int32_t)(64 * i);  // a chain: bits 0 .. t
+        return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1;
+    };
+    uint64_t bits;
+    if (u0 < 0) {
+        bits = ((1ull << -u0) - 1) | word(0) << -u0;
+    } else {
+        const uint32_t i = (uint32_t)u0 / 64, o = (uint32_t)u0 % 64;
+        bits = word(i) >> o;
+        if (o) bits |= word(i + 1) << (64 - o);
+    }
+    const int64_t live = (int64_t)s.fresh - u0;  // slots from j0 on that are in use
+    return live >= 64 ? bits : live <= 0 ? 0 : bits & ((1ull << live) - 1);
+}
+
+// --------------------------------------------------------------- PTX pieces
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+// 16 bytes to shared memory; zeros where !valid.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool valid) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void ldsm4(uint32_t* r, uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t* r, uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+
+template <typename T>
+__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1);
+template <>
+__device__ __forceinline__ void mma16816<__half>(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma16816<__nv_bfloat16>(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Byte offset of 16-byte chunk c of a row in a shared-memory tile of RB-byte rows.
+template <int RB>
+__device__ __forceinline__ uint32_t chunk_at(uint32_t row, uint32_t c) {
+    static_assert(RB == 64 || RB == 128 || RB == 256 || RB == 512, "row bytes");
+    return row * RB + ((c ^ (RB >= 128 ? row & 7 : (row >> 1) & 3)) << 4);
+}
+
+// Weights go to the 16-bit product as exp2(x - max + kLift): lifted in FP16,
+// whose smallest normal number is 2^-14, by 2^8; BF16 has the range of FP32.
+template <typename T>
+constexpr float kLift = 0.0f;
+template <>
+constexpr float kLift<__half> = 8.0f;
+
+// Queries of rows row0 .. row0 + rows - 1 to shared memory as T in RB-byte rows (columns past head_dim
+// and rows past p.rows zero); all threads of the CTA. factor[r], where wanted, is what a score of row r is to be
+// multiplied by to have it in units of log2: scale * log2(e), and for BF16 queries that go to an FP16
+// product the power of two that was taken out of the row to bring its largest element to [1, 2).
+template <typename QT, typename T, int RB, int THREADS>
+__device__ __forceinline__ void load_queries(const AttParams& p, uint32_t b, uint32_t h, uint32_t row0, uint32_t rows,
+                                             char* smem, float* factor) {
+    constexpr bool kCast = !std::is_same<QT, T>::value;
+    constexpr uint32_t kChunks = RB / 16;  // a power of two, at most 32
+    const uint32_t c = threadIdx.x % kChunks, live = p.cache.head_dim / 8;
+    for (uint32_t i = threadIdx.x / kChunks; i < rows; i += THREADS / kChunks) {
+        const uint32_t row = row0 + i;
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (row < p.rows && c < live) {
+            const uint32_t t = row / p.group, g = row - t * p.group;
+            x = *reinterpret_cast<const uint4*>(p.q.p + b * p.q.b + t * p.q.t + (uint64_t)(h * p.group + g) * p.q.h + c * 16);
+        }
+        float f = p.scale * kLog2e;
+        if (kCast) {
+            const QT* e = reinterpret_cast<const QT*>(&x);
+            float v[8], top = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 8; k++) {
+                v[k] = to_f32(e[k]);
+                top = fmaxf(top, fabsf(v[k]));
+            }
+            for (uint32_t o = kChunks / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+            // 2^-e as a float with e the exponent of top; 1 for a row of zeros, subnormals or with an infinity
+            const uint32_t ex = __float_as_uint(top) >> 23;
+            const bool plain = ex > 0 && ex < 254;
+            const float down = plain ? __uint_as_float((254 - ex) << 23) : 1.0f;
+            f *= plain ? __uint_as_float(ex << 23) : 1.0f;
+            uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+            for (int k = 0; k < 4; k++) w[k] = pack2<__half>(v[2 * k] * down, v[2 * k + 1] * down);
+        }
+        *reinterpret_cast<uint4*>(smem + chunk_at<RB>(i, c)) = x;
+        if (factor && c == 0) factor[i] = f;
+    }
+}
+
+// One 16-row fragment of queries for step kk (16 elements) of the head dimension.
+template <bool FP8, int RB>
+__device__ __forceinline__ void query_fragment(uint32_t* a, const char* smem, uint32_t row0, uint32_t kk) {
+    const uint32_t lane = threadIdx.x % 32;
+    if (!FP8) {
+        ldsm4(a, smem_u32(smem) + chunk_at<RB>(row0 + lane % 16, 2 * kk + lane / 16));
+    } else {  // elements 4 l .. 4 l + 3: in the order in which the key bytes come
+        const uint32_t g = lane / 4, l = lane % 4;
+        const uint2 x = *reinterpret_cast<const uint2*>(smem + chunk_at<RB>(row0 + g, 2 * kk + l / 2) + (l & 1) * 8);
+        const uint2 y = *reinterpret_cast<const uint2*>(smem + chunk_at<RB>(row0 + 8 + g, 2 * kk + l / 2) + (l & 1) * 8);
+        a[0] = x.x;
+        a[1] = y.x;
+        a[2] = x.y;
+        a[3] = y.y;
+    }
+}
+
+// Attention kernels by types, one translation unit each; they set p.m, p.mtiles, p.dp and p.grid.
+int attend_bf16(AttParams& p, int sms, cudaStream_t s);
+int attend_bf16_e5m2(AttParams& p, int sms, cudaStream_t s);
+int attend_fp16(AttParams& p, int sms, cudaStream_t s);
+int attend_fp16_e5m2(AttParams& p, int sms, cudaStream_t s);
+
+}  // namespace uzkv
