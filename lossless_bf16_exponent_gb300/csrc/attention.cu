@@ -11,10 +11,6 @@ namespace {
 constexpr int kThreads = 128;
 using Params = AttParams;
 
-__device__ __forceinline__ const int64_t* mask_row(const Params& p, uint32_t b, uint32_t t) {
-    return p.mask ? p.mask + b * p.mask_b + (uint64_t)t * p.mask_words : nullptr;
-}
-
 // Join: one warp a query row. Launched as a programmatic dependent of the attention kernel, so that finding its
 // unit's share of the split overlaps that kernel; rows of units that one CTA finished are already written. Also
 // writes the rows of sequences without new tokens, which have no tiles.
@@ -114,42 +110,6 @@ int launch_join(const Params& p, cudaStream_t s) {
     return UZIP_OK;
 }
 
-// Grid (slots / kThreads, kv_heads, sequences).
-template <typename T, typename C>
-__global__ void __launch_bounds__(kThreads) mass_rows_kernel(const __grid_constant__ Params p) {
-    const uint32_t j = blockIdx.x * kThreads + threadIdx.x, h = blockIdx.y, b = blockIdx.z, d = p.cache.head_dim;
-    if (j >= p.slots) return;
-    const Span sp = span_of(p.cache, p.counts, p.tokens, b);
-    const int64_t at_mass = b * p.mass_b + h * p.mass_h + j;
-    float w = 0.0f;
-    if (j < sp.old + sp.fresh) {
-        const Place at = place_of(p.cache, b, j);
-        const C* k = reinterpret_cast<const C*>(k_row(p.cache, at, h));
-        for (uint32_t t = 0; t < sp.fresh && at.page >= 0; t++) {
-            if (j >= sp.old && !mask_bit(mask_row(p, b, t), t, j - sp.old)) continue;
-            const float weight = p.weights ? p.weights[b * p.tokens + t] : 1.0f;
-            for (uint32_t g = 0; g < p.group; g++) {
-                const uint32_t hq = h * p.group + g;
-                const float lse = p.lse[((uint64_t)b * p.tokens + t) * p.q_heads + hq];
-                if (lse == -INFINITY || weight == 0.0f) continue;
-                const T* q = reinterpret_cast<const T*>(p.q.p + b * p.q.b + t * p.q.t + hq * p.q.h);
-                float s = 0.0f;
-                for (uint32_t i = 0; i < d; i++) s += to_f32(q[i]) * to_f32(k[i]);
-                w += weight * expf(s * p.scale - lse);
-            }
-        }
-    }
-    if (p.mass_in && j < sp.old) w += p.decay * p.mass_in[at_mass];
-    p.mass_out[at_mass] = w;
-}
-
-template <typename T, typename C>
-int launch_mass(const Params& p, cudaStream_t s) {
-    mass_rows_kernel<T, C><<<dim3((p.slots + kThreads - 1) / kThreads, p.cache.kv_heads, p.cache.sequences), kThreads, 0, s>>>(p);
-    UZIP_CUDA_TRY(cudaGetLastError());
-    return UZIP_OK;
-}
-
 // What attention and mass check alike.
 int common(Params& p, const uzkv_rows_t* q, uint32_t dtype, uint32_t tokens, uint32_t q_heads, const int64_t* d_mask,
            int64_t mask_stride_b, const int32_t* d_counts, float scale, const uzkv_cache_t* cache) {
@@ -233,9 +193,10 @@ extern "C" UZIP_API int uzkv_attention_mass(const uzkv_rows_t* q, const float* d
     p.mass_b = mass_stride_b;
     p.mass_h = mass_stride_h;
     p.slots = slots;
+    int sms = 0;
+    if (int rc = sm_count(&sms)) return rc;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const bool fp8 = cache->dtype == UZKV_E5M2;
-    if (dtype == UZKV_BF16)
-        return fp8 ? launch_mass<__nv_bfloat16, E5M2>(p, s) : launch_mass<__nv_bfloat16, __nv_bfloat16>(p, s);
-    return fp8 ? launch_mass<__half, E5M2>(p, s) : launch_mass<__half, __half>(p, s);
+    if (dtype == UZKV_BF16) return fp8 ? mass_bf16_e5m2(p, sms, s) : mass_bf16(p, sms, s);
+    return fp8 ? mass_fp16_e5m2(p, sms, s) : mass_fp16(p, sms, s);
 }

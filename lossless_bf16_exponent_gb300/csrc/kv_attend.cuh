@@ -124,7 +124,9 @@ __global__ void __launch_bounds__(kAttThreads, (AttCfg<QT, FP8, DP, WM>::kCtas))
         const uint64_t r0 = (uint64_t)cur.mt * C::kM;
         if (fresh_unit) {
             __syncthreads();  // the last unit's merge is done with this space
-            load_queries<QT, T, C::kQB, kAttThreads>(p, cur.b, cur.h, (uint32_t)r0, C::kM, qs, FP8 ? factor : nullptr);
+            load_queries<QT, T, DP, kAttThreads, 1>(
+                p, cur.b, cur.h, (uint32_t)r0, C::kM,
+                [&](uint32_t r, uint32_t c) { return reinterpret_cast<uint4*>(qs + chunk_at<C::kQB>(r, c)); }, FP8 ? factor : nullptr);
 #pragma unroll
             for (int x = 0; x < DP / 8; x++)
 #pragma unroll
@@ -440,6 +442,8 @@ int launch_attend_as(AttParams& p, int sms, cudaStream_t stream) {
     p.m = C::kM;
     p.mtiles = (p.rows + C::kM - 1) / C::kM;
     p.dp = DP;
+    p.shift = 6;
+    static_assert(kTile == 1u << 6, "tile");
     p.grid = std::min<uint32_t>((uint32_t)sms * C::kCtas, kMaxAttGrid);
     attend_kernel<QT, FP8, DP, WM><<<p.grid, kAttThreads, C::kSmem, stream>>>(p);
     UZIP_CUDA_TRY(cudaGetLastError());

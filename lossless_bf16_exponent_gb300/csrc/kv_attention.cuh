@@ -27,7 +27,7 @@
 namespace uzkv {
 
 constexpr int kAttThreads = 128;
-constexpr uint32_t kTile = 64;          // cached tokens a step
+constexpr uint32_t kTile = 64;          // cached tokens a step of the warp-level attention
 constexpr uint32_t kMaxAttGrid = 320;   // bounds the workspace: two CTAs on each of up to 160 SMs
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -48,6 +48,7 @@ struct AttParams {
     uint32_t m;        // rows of a tile
     uint32_t dp;       // floats a row of a partial result takes
     uint32_t grid;     // CTAs the tiles are split over
+    uint32_t shift;    // log2 of the cached tokens of a tile
     float* partial;    // [grid][2] results: m rows of dp floats, then m (reference, sum) pairs
     const float* mass_in;
     float* mass_out;
@@ -71,12 +72,12 @@ struct Unit {
     Span span;
 };
 
-__device__ __forceinline__ uint32_t tiles_of(const Span& s) {
-    return s.fresh ? (s.old + s.fresh + kTile - 1) / kTile : 0;
+__device__ __forceinline__ uint32_t tiles_of(const AttParams& p, const Span& s) {
+    return s.fresh ? (s.old + s.fresh + (1u << p.shift) - 1) >> p.shift : 0;
 }
 
 __device__ __forceinline__ uint32_t tiles_of(const AttParams& p, uint32_t b) {
-    return b < p.cache.sequences ? tiles_of(span_of(p.cache, p.counts, p.tokens, b)) : 0;
+    return b < p.cache.sequences ? tiles_of(p, span_of(p.cache, p.counts, p.tokens, b)) : 0;
 }
 
 // All lanes of a warp: tiles of all sequences, one (head, row tile) each.
@@ -129,7 +130,7 @@ __device__ __forceinline__ void advance(const AttParams& p, Unit& u, uint32_t mt
     do {
         if (++u.b >= p.cache.sequences) return;
         u.span = span_of(p.cache, p.counts, p.tokens, u.b);
-        u.tiles = tiles_of(u.span);
+        u.tiles = tiles_of(p, u.span);
     } while (!u.tiles);
 }
 
@@ -230,15 +231,16 @@ constexpr float kLift = 0.0f;
 template <>
 constexpr float kLift<__half> = 8.0f;
 
-// Queries of rows row0 .. row0 + rows - 1 to shared memory as T in RB-byte rows (columns past head_dim
-// and rows past p.rows zero); all threads of the CTA. factor[r], where wanted, is what a score of row r is to be
-// multiplied by to have it in units of log2: scale * log2(e), and for BF16 queries that go to an FP16
-// product the power of two that was taken out of the row to bring its largest element to [1, 2).
-template <typename QT, typename T, int RB, int THREADS>
+// Queries of rows row0 .. row0 + rows - 1 to shared memory as T (columns past head_dim and rows past p.rows
+// zero), by THREADS threads from thread 0 on; at(row, c) is where 16-byte chunk c of a row goes. factor[r *
+// STRIDE], where wanted, is what a score of row r is to be multiplied by to have it in units of log2: scale *
+// log2(e), and for BF16 queries that go to an FP16 product the power of two that was taken out of the row to
+// bring its largest element to [1, 2).
+template <typename QT, typename T, int DP, int THREADS, int STRIDE, typename At>
 __device__ __forceinline__ void load_queries(const AttParams& p, uint32_t b, uint32_t h, uint32_t row0, uint32_t rows,
-                                             char* smem, float* factor) {
+                                             At at, float* factor) {
     constexpr bool kCast = !std::is_same<QT, T>::value;
-    constexpr uint32_t kChunks = RB / 16;  // a power of two, at most 32
+    constexpr uint32_t kChunks = DP / 8;  // a power of two, at most 32
     const uint32_t c = threadIdx.x % kChunks, live = p.cache.head_dim / 8;
     for (uint32_t i = threadIdx.x / kChunks; i < rows; i += THREADS / kChunks) {
         const uint32_t row = row0 + i;
@@ -256,6 +258,7 @@ __device__ __forceinline__ void load_queries(const AttParams& p, uint32_t b, uin
                 v[k] = to_f32(e[k]);
                 top = fmaxf(top, fabsf(v[k]));
             }
+            // rows is a multiple of 16 and so of what a pass takes: no lane of a warp has left the loop
             for (uint32_t o = kChunks / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
             // 2^-e as a float with e the exponent of top; 1 for a row of zeros, subnormals or with an infinity
             const uint32_t ex = __float_as_uint(top) >> 23;
@@ -266,8 +269,8 @@ __device__ __forceinline__ void load_queries(const AttParams& p, uint32_t b, uin
 #pragma unroll
             for (int k = 0; k < 4; k++) w[k] = pack2<__half>(v[2 * k] * down, v[2 * k + 1] * down);
         }
-        *reinterpret_cast<uint4*>(smem + chunk_at<RB>(i, c)) = x;
-        if (factor && c == 0) factor[i] = f;
+        *at(i, c) = x;
+        if (factor && c == 0) factor[i * STRIDE] = f;
     }
 }
 
@@ -293,5 +296,9 @@ int attend_bf16(AttParams& p, int sms, cudaStream_t s);
 int attend_bf16_e5m2(AttParams& p, int sms, cudaStream_t s);
 int attend_fp16(AttParams& p, int sms, cudaStream_t s);
 int attend_fp16_e5m2(AttParams& p, int sms, cudaStream_t s);
+int mass_bf16(AttParams& p, int sms, cudaStream_t s);
+int mass_bf16_e5m2(AttParams& p, int sms, cudaStream_t s);
+int mass_fp16(AttParams& p, int sms, cudaStream_t s);
+int mass_fp16_e5m2(AttParams& p, int sms, cudaStream_t s);
 
 }  // namespace uzkv

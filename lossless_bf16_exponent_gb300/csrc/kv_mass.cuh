@@ -1,0 +1,346 @@
+// kv_mass.cuh -- the attention weight that each cached token collects, on the
+// tensor cores.
+//
+// With the rows' log-sum-exp given, a weight is exp2(s * f - e) with e of the
+// row alone, and a token's mass their sum over rows: no running maximum, no
+// second product. The product is taken with the cached tokens along M:
+// S^T = K Q^T, 128 tokens by up to 256 rows, so that in tensor memory a lane
+// is a token and the sum over rows stays within a thread, in one fixed order.
+// Any number of rows costs only its own columns (a multiple of 16).
+//
+// One CTA an SM takes a run of tiles (kv_attention.cuh's split). Its warps:
+// 0-3 bring keys to a ring of operand tiles (16-byte asynchronous copies; E5M2
+// keys land as bytes and are widened to FP16 tiles), and the rows' queries and
+// factors once a unit; 12 issues the products into two buffers of tensor
+// memory; 4-7 and 8-11 take turns at the tiles, sum, add the decayed old mass
+// and store. More than 256 rows (128 for heads above 128) go in chunks: the
+// CTA passes over its tiles of the unit once a chunk, adding to what the same
+// thread stored before.
+#pragma once
+
+#include <algorithm>
+#include <atomic>
+
+#include "kv_tcgen05.cuh"
+
+namespace uzkv {
+
+constexpr int kMassThreads = 13 * 32;
+constexpr uint32_t kMassTile = 128;
+
+template <typename QT, bool FP8, int DP>
+struct MassCfg {
+    using T = typename std::conditional<FP8, __half, QT>::type;
+    static constexpr uint32_t kMaxN = DP <= 128 ? 256 : 128;          // rows of a chunk
+    static constexpr uint32_t kQBytes = kMaxN * DP * 2;               // one chunk's queries, or two smaller ones'
+    static constexpr uint32_t kTileBytes = kMassTile * DP * 2;
+    static constexpr uint32_t kRawBytes = kMassTile * DP;             // E5M2 bytes of a tile
+    static constexpr uint32_t kRoom = 227 * 1024 - 1024 - 8192;       // less alignment, factors and barriers
+    // 16-bit keys: as many operand tiles as fit. E5M2: few operand tiles, the rest of the space for bytes on their way.
+    static constexpr uint32_t kFit = (kRoom - kQBytes) / kTileBytes;
+    static constexpr uint32_t kTiles = FP8 ? (DP <= 128 ? 2 : 1) : (kFit > 8 ? 8 : kFit);
+    static constexpr uint32_t kRaw = FP8 ? (DP <= 128 ? 4 : 2) : 0;
+    static constexpr uint32_t kSmem = 1024 + kQBytes + kTiles * kTileBytes + kRaw * kRawBytes + 8192;
+    static_assert(kSmem <= 227 * 1024, "shared memory");
+    static_assert(kTiles >= 1, "operand tiles");
+};
+
+// The runs of tiles of one unit and chunk that a CTA passes over; all roles walk the same list.
+struct MassWalk {
+    Unit u;
+    uint64_t left;
+    uint32_t chunk, count, units;
+    __device__ __forceinline__ MassWalk(const Unit& first, uint64_t n) : u(first), left(n), chunk(0), count(0), units(0) {
+        if (left) count = (uint32_t)min((uint64_t)(u.tiles - u.tile), left);
+    }
+    __device__ __forceinline__ bool valid() const { return left != 0; }
+    __device__ __forceinline__ void next(const AttParams& p) {
+        if (++chunk < p.mtiles) return;
+        chunk = 0;
+        left -= count;
+        if (!left) return;
+        u.tile += count - 1;
+        advance(p, u, 1);
+        units++;
+        count = (uint32_t)min((uint64_t)(u.tiles - u.tile), left);
+    }
+    // Which of the two accumulators and summing groups takes tile i: turns over tiles and units, the same in every
+    // chunk, so that the thread that adds a later chunk to a token's mass is the one that stored it.
+    __device__ __forceinline__ uint32_t turn(uint32_t i) const { return (i + units) & 1; }
+};
+
+template <typename QT, bool FP8, int DP>
+__global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const __grid_constant__ AttParams p) {
+    using C = MassCfg<QT, FP8, DP>;
+    using T = typename C::T;
+    extern __shared__ char smem_raw[];
+    char* const smem = smem_raw + (1024 - smem_u32(smem_raw) % 1024) % 1024;
+    char* const qs = smem;
+    char* const tiles = qs + C::kQBytes;
+    char* const raws = tiles + C::kTiles * C::kTileBytes;
+    float2* const rowf = reinterpret_cast<float2*>(raws + C::kRaw * C::kRawBytes);  // [2][256]: factor, exponent
+    uint64_t* const bars = reinterpret_cast<uint64_t*>(rowf + 512);
+    uint32_t* const tmem_at = reinterpret_cast<uint32_t*>(bars + 32);
+    const uint32_t tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    const uint32_t D = p.cache.head_dim, N = p.m;
+    const uint32_t qbuf = 2 * N * DP * 2 <= C::kQBytes ? 2 : 1;  // queries of two units at once where they fit
+    const uint32_t full = smem_u32(bars), freed = full + 8 * 8, q_full = full + 16 * 8, q_freed = full + 18 * 8,
+                   s_full = full + 20 * 8, s_freed = full + 22 * 8;
+    uint32_t columns = 32;
+    while (columns < 2 * N) columns *= 2;
+
+    if (tid == 0) {
+        for (uint32_t i = 0; i < 8; i++) {
+            bar_init(full + 8 * i, 4);   // the four copying warps
+            bar_init(freed + 8 * i, 1);  // the products' commit
+        }
+        for (uint32_t i = 0; i < 2; i++) {
+            bar_init(q_full + 8 * i, 4);
+            bar_init(q_freed + 8 * i, 9);  // the products' commit and the eight summing warps
+            bar_init(s_full + 8 * i, 1);
+            bar_init(s_freed + 8 * i, 4);  // the four warps of the buffer's group
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 12) tc_alloc(smem_u32(tmem_at), columns);
+    if (D < DP) {  // columns past the head dimension stay zero: no copy writes them
+        for (uint32_t i = tid; i < C::kTiles * C::kTileBytes / 16; i += kMassThreads) reinterpret_cast<uint4*>(tiles)[i] = make_uint4(0, 0, 0, 0);
+        fence_async_smem();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_at;
+
+    const uint64_t total = all_tiles(p) * p.cache.kv_heads;
+    const uint64_t shares = min(total, (uint64_t)p.grid);
+    const uint64_t begin = blockIdx.x < shares ? total * blockIdx.x / shares : 0;
+    const uint64_t n = blockIdx.x < shares ? total * (blockIdx.x + 1) / shares - begin : 0;
+    const Unit first = n ? unit_at(p, begin, 1) : Unit{};
+    bool ok = true;
+
+    if (warp < 4) {
+        // ---- copies
+        constexpr uint32_t kES = FP8 ? 1 : 2, kLanes = DP * kES / 16;  // a row's chunks
+        constexpr uint32_t kRing = FP8 ? C::kRaw : C::kTiles;
+        const uint32_t c = lane % kLanes, live = D * kES / 16;
+        MassWalk cw(first, n);        // of the next tile to copy
+        uint32_t cs = 0, copied = 0;  // its place in the run, and how many are copied
+        auto copy = [&]() {
+            if (ok && cw.valid()) {
+                // A warp takes 32 of the tile's rows: each lane finds one, then the warp copies them row by row.
+                if (!FP8 && copied >= kRing) ok = warp_wait(freed + 8 * (copied % kRing), (copied / kRing - 1) & 1);
+                if (FP8) __syncwarp();  // this warp has widened what the slot held: it copies only its own rows
+                const uint32_t j = (cw.u.tile + cs) * kMassTile + warp * 32 + lane;
+                const char* row = nullptr;
+                if (j < cw.u.span.old + cw.u.span.fresh) {
+                    const Place pl = place_of(p.cache, cw.u.b, j);
+                    if (pl.page >= 0) row = k_row(p.cache, pl, cw.u.h);
+                }
+                char* slot = (FP8 ? raws : tiles) + (copied % kRing) * (FP8 ? C::kRawBytes : C::kTileBytes);
+#pragma unroll 8
+                for (uint32_t i = 0; i < kLanes; i++) {
+                    const uint32_t r = i * (32 / kLanes) + lane / kLanes;
+                    const char* src = reinterpret_cast<const char*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(row), r));
+                    const uint32_t R = warp * 32 + r;
+                    const uint32_t at = FP8 ? chunk_at<DP>(R, c) : swizzled(kMassTile, R, c);
+                    if (c < live) copy16(smem_u32(slot) + at, src ? src + c * 16 : p.cache.k, src != nullptr);
+                }
+                copied++;
+                if (++cs == cw.count) {
+                    cs = 0;
+                    cw.next(p);
+                }
+            }
+            copy_commit();
+        };
+        uint32_t seg = 0, sent = 0;
+        for (uint32_t i = 0; i < kRing - 1; i++) copy();
+        for (MassWalk w(first, n); w.valid() && ok; w.next(p), seg++) {
+            // The rows' queries, factors and exponents.
+            const uint32_t qb = seg % qbuf, fb = seg % 2;
+            if (seg >= qbuf) ok = warp_wait(q_freed + 8 * qb, (seg / qbuf - 1) & 1);
+            if (!ok) break;
+            const uint32_t row0 = w.chunk * N;
+            char* q = qs + qb * N * DP * 2;
+            float2* f = rowf + fb * 256;
+            load_queries<QT, T, DP, 128, 2>(
+                p, w.u.b, w.u.h, row0, N, [&](uint32_t r, uint32_t ch) { return reinterpret_cast<uint4*>(q + swizzled(N, r, ch)); },
+                &f[0].x);
+            for (uint32_t r = tid; r < N; r += 128) {
+                const uint32_t row = row0 + r, t = row / p.group;
+                float e = INFINITY;  // a row that adds nothing
+                if (row < p.rows && t < w.u.span.fresh) {
+                    const float lse = p.lse[((uint64_t)w.u.b * p.tokens + t) * p.q_heads + w.u.h * p.group + row % p.group];
+                    const float wt = p.weights ? p.weights[(uint64_t)w.u.b * p.tokens + t] : 1.0f;
+                    if (lse != -INFINITY && wt != 0.0f) e = p.weights ? lse * kLog2e - log2f(wt) : lse * kLog2e;
+                }
+                f[r].y = e;
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) bar_arrive(q_full + 8 * (seg % 2));
+            for (uint32_t i = 0; i < w.count && ok; i++, sent++) {
+                copy_wait<kRing - 2>();
+                if (FP8) {
+                    // Widen this warp's rows of the tile: 16 bytes to two chunks of eight FP16.
+                    if (sent >= C::kTiles) ok = warp_wait(freed + 8 * (sent % C::kTiles), (sent / C::kTiles - 1) & 1);
+                    __syncwarp();
+                    const char* raw = raws + (sent % kRing) * C::kRawBytes;
+                    char* tile = tiles + (sent % C::kTiles) * C::kTileBytes;
+                    if (c < live)
+#pragma unroll 4
+                        for (uint32_t x = 0; x < kLanes; x++) {
+                            const uint32_t R = warp * 32 + x * (32 / kLanes) + lane / kLanes;
+                            const uint4 v = *reinterpret_cast<const uint4*>(raw + chunk_at<DP>(R, c));
+                            *reinterpret_cast<uint4*>(tile + swizzled(kMassTile, R, 2 * c)) =
+                                make_uint4(uzip::prmt(v.x, 0, 0x1404), uzip::prmt(v.x, 0, 0x3424), uzip::prmt(v.y, 0, 0x1404), uzip::prmt(v.y, 0, 0x3424));
+                            *reinterpret_cast<uint4*>(tile + swizzled(kMassTile, R, 2 * c + 1)) =
+                                make_uint4(uzip::prmt(v.z, 0, 0x1404), uzip::prmt(v.z, 0, 0x3424), uzip::prmt(v.w, 0, 0x1404), uzip::prmt(v.w, 0, 0x3424));
+                        }
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) bar_arrive(full + 8 * (sent % C::kTiles));
+                copy();
+            }
+        }
+        copy_wait<0>();
+    } else if (warp == 12) {
+        // ---- products, by one lane
+        if (lane == 0) {
+            const uint32_t idesc = mma_desc<T>(kMassTile, N), steps = (D + 15) / 16;
+            uint32_t seg = 0, k = 0, uses[2] = {0, 0};
+            for (MassWalk w(first, n); w.valid() && ok; w.next(p), seg++) {
+                ok = bar_wait(q_full + 8 * (seg % 2), (seg / 2) & 1);
+                const uint32_t q = smem_u32(qs) + seg % qbuf * N * DP * 2;
+                for (uint32_t i = 0; i < w.count && ok; i++, k++) {
+                    const uint32_t s = k % C::kTiles, side = w.turn(i), used = side ? uses[1]++ : uses[0]++;
+                    ok = bar_wait(full + 8 * s, (k / C::kTiles) & 1);
+                    if (ok && used) ok = bar_wait(s_freed + 8 * side, (used - 1) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t a = smem_u32(tiles) + s * C::kTileBytes;
+                    for (uint32_t x = 0; x < steps; x++)
+                        tc_mma(tmem + side * N, tile_desc(a + (x >> 2) * kMassTile * 128 + (x & 3) * 32),
+                               tile_desc(q + (x >> 2) * N * 128 + (x & 3) * 32), idesc, x != 0);
+                    tc_commit(freed + 8 * s);
+                    tc_commit(s_full + 8 * side);
+                }
+                if (ok) tc_commit(q_freed + 8 * (seg % qbuf));
+            }
+        }
+        __syncwarp();
+    } else {
+        // ---- sums: a thread is a cached token
+        const uint32_t group = warp < 8 ? 0 : 1, quarter = warp % 4;
+        uint32_t seg = 0, used = 0;
+        for (MassWalk w(first, n); w.valid() && ok; w.next(p), seg++) {
+            const Span sp = w.u.span;
+            const float2* f = rowf + seg % 2 * 256;
+            const int64_t row_at = w.u.b * p.mass_b + w.u.h * p.mass_h;
+            ok = warp_wait(q_full + 8 * (seg % 2), (seg / 2) & 1);
+            for (uint32_t i = 0; i < w.count && ok; i++) {
+                if (w.turn(i) != group) continue;
+                const uint32_t j0 = (w.u.tile + i) * kMassTile, j = j0 + quarter * 32 + lane;
+                ok = warp_wait(s_full + 8 * group, used++ & 1);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t at = tmem + group * N + (quarter * 32 << 16);
+                float acc = 0.0f;
+                bool guard = j0 + kMassTile > sp.old;
+                if (!guard) {
+                    float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    for (uint32_t c0 = 0; c0 < N; c0 += 16) {
+                        float v[16];
+                        tc_ld16(v, at + c0);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int x = 0; x < 16; x += 2) {
+                            const float4 e = *reinterpret_cast<const float4*>(f + c0 + x);
+                            part[x % 4] += exp2_fast(v[x] * e.x - e.y);
+                            part[x % 4 + 1] += exp2_fast(v[x + 1] * e.z - e.w);
+                        }
+                    }
+                    acc = (part[0] + part[1]) + (part[2] + part[3]);
+                    // A key that is not finite makes NaN of rows that add nothing too: take those rows out.
+                    guard = __any_sync(0xFFFFFFFFu, acc != acc);
+                }
+                if (guard) {
+                    acc = 0.0f;
+                    const uint32_t row0 = w.chunk * N;
+                    for (uint32_t c0 = 0; c0 < N; c0 += 16) {
+                        float v[16];
+                        tc_ld16(v, at + c0);
+                        tc_wait_ld();
+                        for (int x = 0; x < 16; x++) {
+                            const float2 e = f[c0 + x];
+                            const uint32_t t = (row0 + c0 + x) / p.group;
+                            bool see = e.y != INFINITY;
+                            if (see && j >= sp.old)
+                                see = j < sp.old + sp.fresh &&
+                                      mask_bit(p.mask ? p.mask + w.u.b * p.mask_b + (uint64_t)t * p.mask_words : nullptr, t, j - sp.old);
+                            const float m = exp2_fast(v[x] * e.x - e.y);
+                            acc += see ? m : 0.0f;
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(s_freed + 8 * group);
+                if (j < p.slots) {
+                    if (w.chunk) acc += p.mass_out[row_at + j];
+                    else if (p.mass_in && j < sp.old) acc += p.decay * p.mass_in[row_at + j];
+                    p.mass_out[row_at + j] = acc;
+                }
+            }
+            // This warp's last read of the unit's factors is behind it.
+            __syncwarp();
+            if (lane == 0 && ok) bar_arrive(q_freed + 8 * (seg % qbuf));
+        }
+        // Slots that no tile covers: past the new tokens, or all of a sequence that has none.
+        const uint32_t rows = p.cache.sequences * p.cache.kv_heads;
+        for (uint32_t r = blockIdx.x; r < rows; r += gridDim.x) {
+            const uint32_t b = r / p.cache.kv_heads, h = r % p.cache.kv_heads;
+            const Span sp = span_of(p.cache, p.counts, p.tokens, b);
+            const int64_t row_at = b * p.mass_b + h * p.mass_h;
+            for (uint64_t j = (uint64_t)tiles_of(p, sp) * kMassTile + (tid - 128); j < p.slots; j += 256)
+                p.mass_out[row_at + j] = p.mass_in && j < sp.old ? p.decay * p.mass_in[row_at + j] : 0.0f;
+        }
+    }
+    if (!ok && p.cache.status) *p.cache.status = UZIP_ERR_TIMEOUT;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 12) tc_free(tmem, columns);
+}
+
+template <typename QT, bool FP8, int DP>
+int launch_mass_as(AttParams& p, int sms, cudaStream_t stream) {
+    using C = MassCfg<QT, FP8, DP>;
+    static std::atomic<uint64_t> ready{0};  // a bit for each device whose limit is raised
+    int dev = 0;
+    UZIP_CUDA_TRY(cudaGetDevice(&dev));
+    if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+        UZIP_CUDA_TRY(cudaFuncSetAttribute(mass_kernel<QT, FP8, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem));
+        if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
+    const uint32_t chunks = (p.rows + C::kMaxN - 1) / C::kMaxN;
+    p.mtiles = chunks;
+    p.m = ((p.rows + chunks - 1) / chunks + 15) / 16 * 16;
+    p.shift = 7;
+    static_assert(kMassTile == 1u << 7, "tile");
+    p.grid = (uint32_t)sms;
+    mass_kernel<QT, FP8, DP><<<p.grid, kMassThreads, C::kSmem, stream>>>(p);
+    UZIP_CUDA_TRY(cudaGetLastError());
+    return UZIP_OK;
+}
+
+template <typename QT, bool FP8>
+int launch_mass(AttParams& p, int sms, cudaStream_t s) {
+    if (p.cache.head_dim <= 64) return launch_mass_as<QT, FP8, 64>(p, sms, s);
+    if (p.cache.head_dim <= 128) return launch_mass_as<QT, FP8, 128>(p, sms, s);
+    return launch_mass_as<QT, FP8, 256>(p, sms, s);
+}
+
+}  // namespace uzkv

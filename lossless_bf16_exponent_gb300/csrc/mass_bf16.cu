@@ -1,0 +1,5 @@
+// mass_bf16.cu -- mass kernels of BF16 queries.
+#include "kv_mass.cuh"
+
+int uzkv::mass_bf16(AttParams& p, int sms, cudaStream_t s) { return launch_mass<__nv_bfloat16, false>(p, sms, s); }
+int uzkv::mass_bf16_e5m2(AttParams& p, int sms, cudaStream_t s) { return launch_mass<__nv_bfloat16, true>(p, sms, s); }
