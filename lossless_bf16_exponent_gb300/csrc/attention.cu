@@ -142,7 +142,7 @@ extern "C" UZIP_API size_t uzkv_tree_attention_workspace_bytes(uint32_t sequence
     if (!sequences || !tokens || tokens > UZKV_MAX_NEW_TOKENS || !q_heads || !kv_heads || q_heads % kv_heads ||
         !head_dim || head_dim > UZKV_MAX_HEAD_DIM)
         return 0;
-    const uint64_t rows = (uint64_t)tokens * (q_heads / kv_heads), m = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    const uint64_t rows = (uint64_t)tokens * (q_heads / kv_heads), m = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;  // at least a unit's rows
     const uint64_t dp = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
     return (size_t)(kMaxAttGrid * 2 * m * (dp + 2) * 4);
 }

@@ -1,13 +1,28 @@
-// kv_attend.cuh -- attention over a paged cache by warp-level matrix products:
-// one pass over keys and values with the running maximum and sum of a softmax,
-// the cache's tiles split over a persistent grid.
+// kv_attend.cuh -- attention over a paged cache by warp-level matrix products,
+// for up to 64 rows at a time: one pass over keys and values with the running
+// reference and sum of a softmax.
 //
-// Each CTA of four warps takes a run of tiles of 64 cached tokens. Keys and
-// values come through a ring of shared-memory stages filled by 16-byte
-// asynchronous copies that run ahead across unit boundaries; page numbers are
-// looked up one step before the copies that need them. WM warps share the
-// rows (16 each), 4 / WM share a tile's tokens, so that few rows still keep
-// four warps busy; the token shares are merged once a unit.
+// Bound: HBM, as long as the products of a tile take less time than its bytes
+// (4 D flop a row and token against 2 D bytes an element's width: up to about
+// 64 rows at the warp-level product's rate). So the kernel is built to keep
+// copies in flight: one CTA an SM, four warps that only copy, eight that only
+// compute, and a ring of stages between them. Copying warps find their tokens'
+// pages one tile ahead and run on across unit boundaries.
+//
+// The products have the cached tokens along M: S^T = K Q^T and O^T = V^T P^T,
+// 16 tokens (or 16 columns of V) by 8 rows. Eight rows of a decoding step waste
+// nothing, keys and values are the operand that one matrix load brings whole,
+// queries stay in registers, and a score tile becomes the second product's
+// operand by one 8 x 8 transpose. A warp takes 8 RN rows; WM warps share the
+// rows of a tile and 8 / WM its tokens, which are merged once a unit through
+// shared memory.
+//
+// E5M2: a matrix load of 16-bit units gives a thread four consecutive bytes of
+// a key row, where the product's layout wants two pairs eight apart. The sum
+// over the head dimension may run in any order, so the queries are read in the
+// same permuted one. For the values, a transposed load gives the bytes of two
+// neighbouring columns; the even ones become rows 0-7 of the product, the odd
+// ones rows 8-15.
 #pragma once
 
 #include <algorithm>
@@ -17,445 +32,464 @@
 
 namespace uzkv {
 
-template <typename QT, bool FP8, int DP, int WM>
+template <typename QT, bool FP8, int DP, int RN, int WM>
 struct AttCfg {
     using T = typename std::conditional<FP8, __half, QT>::type;  // type of the products
-    static constexpr int kES = FP8 ? 1 : 2;
-    static constexpr int kRB = DP * kES;         // bytes of a cached row in shared memory
-    static constexpr int kQB = DP * 2;           // bytes of a query row
-    static constexpr int kM = 16 * WM;
-    static constexpr int kWN = 4 / WM;
-    static constexpr int kKeys = kTile / kWN;    // tokens of a tile that a warp takes
+    static constexpr int kRB = DP * (FP8 ? 1 : 2);               // bytes of a cached row in shared memory
+    static constexpr int kM = 8 * RN * WM;                       // rows of a unit
+    static constexpr int kWN = 8 / WM;
+    static constexpr int kTile = kRB == 512 ? 64 : 128;          // cached tokens of a stage
+    static constexpr int kKeys = kTile / kWN;                    // of them, a warp's
+    static constexpr int kSub = kKeys < 32 ? kKeys : 32;         // taken at once
     static constexpr int kStage = 2 * kTile * kRB;
-    static constexpr int kCtas = kStage >= 65536 ? 1 : 2;  // an SM
-    // Merging the token shares goes through the queries' space, which has the larger use's size.
-    static constexpr int kMergeBytes = kWN > 1 ? kM * (DP + 2) * 4 : 0;
-    static constexpr int kQBytes = ((kM * kQB > kMergeBytes ? kM * kQB : kMergeBytes) + 15) / 16 * 16;
-    static constexpr int kFactorBytes = FP8 ? kM * 4 : 0;
-    static constexpr int kOther = kQBytes + kFactorBytes + 2 * (int)kTile * 8;
-    // 228 KB an SM, one of it taken by each CTA
-    static constexpr int kFit = (233472 / kCtas - 1024 - kOther) / kStage;
-    static constexpr int kStages = kFit > 6 ? 6 : kFit;
-    static_assert(kStages >= 2, "a tile in use and one on its way");
+    static constexpr int kBoxRow = DP + 4;                       // floats; 4 more keep the merge's stores off each other's banks
+    static constexpr int kBox = 8 * 8 * kBoxRow * 4;             // eight rows of each computing warp
+    static constexpr int kOther = kBox + 8 * 8 * 8 + 256;        // (reference, sum) pairs, barriers
+    static constexpr int kFit = (227 * 1024 - kOther) / kStage;
+    static constexpr int kStages = kFit > 8 ? 8 : kFit;
     static constexpr int kSmem = kStages * kStage + kOther;
+    static_assert(kStages >= 2, "a tile in use and one on its way");
+    static_assert(kKeys >= 16, "a product's tokens");
 };
 
-template <typename QT, bool FP8, int DP, int WM>
-__global__ void __launch_bounds__(kAttThreads, (AttCfg<QT, FP8, DP, WM>::kCtas)) attend_kernel(const __grid_constant__ AttParams p) {
-    using C = AttCfg<QT, FP8, DP, WM>;
+constexpr int kAttThreads = 12 * 32;  // 8 warps that compute, 4 that copy
+
+// NaN and infinities of a pair of values (FP16 or BF16 patterns) become zero; whether there were any.
+template <typename T>
+__device__ __forceinline__ uint32_t clean2(uint32_t& v) {
+    constexpr uint32_t kExp = std::is_same<T, __half>::value ? 0x7C00u : 0x7F80u;
+    uint32_t bad = 0;
+    if ((v & kExp) == kExp) bad |= 0xFFFFu;
+    if ((v >> 16 & kExp) == kExp) bad |= 0xFFFF0000u;
+    v &= ~bad;
+    return bad;
+}
+
+template <typename QT, bool FP8, int DP, int RN, int WM>
+__global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_constant__ AttParams p) {
+    using C = AttCfg<QT, FP8, DP, RN, WM>;
     using T = typename C::T;
-    extern __shared__ __align__(128) char smem[];
-    char* const kv = smem;
-    char* const qs = smem + C::kStages * C::kStage;
-    float* const factor = reinterpret_cast<float*>(qs + C::kQBytes);
-    int2* const places = reinterpret_cast<int2*>(qs + C::kQBytes + C::kFactorBytes);  // [2][kTile]: page, row
+    extern __shared__ __align__(1024) char smem[];
+    float* const box = reinterpret_cast<float*>(smem + C::kStages * C::kStage);
+    float2* const stat = reinterpret_cast<float2*>(box + 8 * 8 * C::kBoxRow);  // [8 warps][8 rows]
+    const uint32_t full = smem_u32(stat + 64), freed = full + 8 * 8, merge = full + 16 * 8;
     const uint32_t tid = threadIdx.x, lane = tid % 32, warp = tid / 32, g = lane / 4, l = lane % 4;
-    const uint32_t wm = warp % WM, wn = warp / WM;
     const uint32_t D = p.cache.head_dim;
 
     uzip::pdl_launch_dependents();
-    const uint64_t total = all_tiles(p) * p.cache.kv_heads * p.mtiles;
-    const uint64_t shares = min(total, (uint64_t)p.grid);  // no share is empty
-    if (blockIdx.x >= shares) return;
-    const uint64_t begin = total * blockIdx.x / shares, end = total * (blockIdx.x + 1) / shares;
-    const uint32_t n = (uint32_t)(end - begin);
-
-    // Columns past the head dimension stay zero: no copy writes them.
-    if (D < DP)
-        for (uint32_t i = tid; i < C::kStages * C::kStage / 16; i += kAttThreads) reinterpret_cast<uint4*>(kv)[i] = make_uint4(0, 0, 0, 0);
-
-    Unit cur = unit_at(p, begin, p.mtiles);
-    Unit ahead = cur, look = cur;  // of the next tile to copy, and the next to look up
-    uint32_t copied = 0, looked = 0;
-
-    auto find = [&]() {  // place of this thread's token of the next tile to look up
-        int2 at = make_int2(-1, 0);
-        if (looked < n && tid < kTile) {
-            const uint32_t j = look.tile * kTile + tid;
-            if (j < look.span.old + look.span.fresh) {
-                const Place pl = place_of(p.cache, look.b, j);
-                at = make_int2(pl.page, (int)pl.row);
-            }
+    if (tid == 0) {
+        for (int s = 0; s < C::kStages; s++) {
+            bar_init(full + 8 * s, 128);  // every copying thread
+            bar_init(freed + 8 * s, 8);   // every computing warp
         }
-        if (looked < n) {
-            looked++;
-            advance(p, look, p.mtiles);
-        }
-        return at;
-    };
-    auto copy = [&]() {
-        if (copied < n) {
-            constexpr uint32_t kLanes = C::kRB / 16;  // a row's chunks
-            const uint32_t c = tid % kLanes, live = D * C::kES / 16;
-            const int2* at = places + (copied & 1) * kTile;
-            char* stage = kv + (copied % C::kStages) * C::kStage;
-            const char* kb = p.cache.k + ahead.h * p.cache.k_head + c * 16;
-            const char* vb = p.cache.v + ahead.h * p.cache.v_head + c * 16;
-            if (c < live) {
-#pragma unroll
-                for (uint32_t r = tid / kLanes; r < kTile; r += kAttThreads / kLanes) {
-                    const int2 pl = at[r];
-                    const bool ok = pl.x >= 0;
-                    const uint32_t dst = smem_u32(stage) + chunk_at<C::kRB>(r, c);
-                    copy16(dst, ok ? kb + pl.x * p.cache.k_page + pl.y * p.cache.k_token : p.cache.k, ok);
-                    copy16(dst + kTile * C::kRB, ok ? vb + pl.x * p.cache.v_page + pl.y * p.cache.v_token : p.cache.v, ok);
-                }
-            }
-            copied++;
-            advance(p, ahead, p.mtiles);
-        }
-        copy_commit();
-    };
-
-    // Fill the ring: stages - 1 tiles in flight.
-    if (tid < kTile) places[tid] = find(); else find();
-    for (int s = 0; s < C::kStages - 1; s++) {
-        const int2 next = find();
-        __syncthreads();
-        copy();
-        if (tid < kTile) places[(copied & 1) * kTile + tid] = next;
+        bar_init(merge, 8);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    if (D < DP)  // columns past the head dimension stay zero: no copy writes them
+        for (uint32_t i = tid; i < C::kStages * C::kStage / 16; i += kAttThreads) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
+    const Split split = split_of(p);
+    const uint64_t total = split.all * p.cache.kv_heads * p.mtiles;
+    const uint64_t shares = min(total, (uint64_t)p.grid);  // no share is empty
+    const bool any = blockIdx.x < shares;
+    const uint64_t begin = any ? total * blockIdx.x / shares : 0;
+    const uint32_t n = any ? (uint32_t)(total * (blockIdx.x + 1) / shares - begin) : 0;
+    Unit cur = any ? unit_at(p, split, begin, p.mtiles) : Unit{};
+    __syncthreads();
+    bool ok = true;
 
-    float o[DP / 8][4], top[2], sum[2];
-    bool fresh_unit = true;
-    const uint32_t row0 = wm * 16 + g;  // and row0 + 8
-
-    for (uint32_t i = 0; i < n; i++) {
-        const uint64_t r0 = (uint64_t)cur.mt * C::kM;
-        if (fresh_unit) {
-            __syncthreads();  // the last unit's merge is done with this space
-            load_queries<QT, T, DP, kAttThreads, 1>(
-                p, cur.b, cur.h, (uint32_t)r0, C::kM,
-                [&](uint32_t r, uint32_t c) { return reinterpret_cast<uint4*>(qs + chunk_at<C::kQB>(r, c)); }, FP8 ? factor : nullptr);
-#pragma unroll
-            for (int x = 0; x < DP / 8; x++)
-#pragma unroll
-                for (int y = 0; y < 4; y++) o[x][y] = 0.0f;
-            top[0] = top[1] = -INFINITY;
-            sum[0] = sum[1] = 0.0f;
-        }
-        const int2 next = find();
-        copy_wait<C::kStages - 2>();
-        __syncthreads();
-        copy();
-        if (tid < kTile) places[(copied & 1) * kTile + tid] = next;
-
-        char* const stage = kv + (i % C::kStages) * C::kStage;
-        const uint32_t ks = smem_u32(stage), vs = ks + kTile * C::kRB;
-        const uint32_t j0 = cur.tile * kTile;
-        const uint32_t mykey = wn * C::kKeys;
-        float s[C::kKeys / 8][4];
-#pragma unroll
-        for (int x = 0; x < C::kKeys / 8; x++)
-#pragma unroll
-            for (int y = 0; y < 4; y++) s[x][y] = 0.0f;
-
-        // Scores: rows by the warp's tokens.
-        if (!FP8) {
-#pragma unroll
-            for (int kk = 0; kk < DP / 16; kk++) {
-                if (kk * 16 >= D) break;
-                uint32_t a[4];
-                query_fragment<FP8, C::kQB>(a, qs, wm * 16, kk);
-#pragma unroll
-                for (int x = 0; x < C::kKeys / 16; x++) {
-                    uint32_t bfr[4];
-                    ldsm4(bfr, ks + chunk_at<C::kRB>(mykey + x * 16 + (lane / 16) * 8 + lane % 8, 2 * kk + (lane / 8) % 2));
-                    mma16816<T>(s[2 * x], a, bfr[0], bfr[1]);
-                    mma16816<T>(s[2 * x + 1], a, bfr[2], bfr[3]);
+    if (warp >= 8) {
+        // ---- copies: a warp takes a quarter of a tile's tokens
+        constexpr uint32_t kMine = C::kTile / 4, kLanes = C::kRB / 16;
+        const uint32_t w = warp - 8, c = lane % kLanes, live = D * (FP8 ? 1 : 2) / 16;
+        Place at{-1, 0};
+        auto find = [&](uint32_t i) {  // this lane's token of the tile under `cur`, which is the i-th of the run
+            Place pl{-1, 0};
+            const uint32_t j = cur.tile * C::kTile + w * kMine + lane;
+            if (i < n && lane < kMine && j < cur.span.old + cur.span.fresh) pl = place_of(p.cache, cur.b, j);
+            return pl;
+        };
+        at = find(0);
+        for (uint32_t i = 0; i < n && ok; i++) {
+            const char* krow = at.page >= 0 ? k_row(p.cache, at, cur.h) : nullptr;
+            const char* vrow = at.page >= 0 ? v_row(p.cache, at, cur.h) : nullptr;
+            advance(p, cur, p.mtiles);
+            at = find(i + 1);
+            const uint32_t s = i % C::kStages;
+            if (i >= C::kStages) ok = warp_wait(freed + 8 * s, (i / C::kStages - 1) & 1);
+            if (!ok) break;
+            const uint32_t ks = smem_u32(smem + s * C::kStage);
+#pragma unroll 8
+            for (uint32_t x = 0; x < kMine * kLanes / 32; x++) {
+                const uint32_t r = x * (32 / kLanes) + lane / kLanes;
+                const char* ka = reinterpret_cast<const char*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(krow), r));
+                const char* va = reinterpret_cast<const char*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(vrow), r));
+                const uint32_t dst = ks + chunk_at<C::kRB>(w * kMine + r, c);
+                if (c < live) {
+                    copy16(dst, ka ? ka + c * 16 : p.cache.k, ka != nullptr);
+                    copy16(dst + C::kTile * C::kRB, va ? va + c * 16 : p.cache.v, va != nullptr);
                 }
             }
-        } else {
-#pragma unroll
-            for (int kp = 0; kp < DP / 32; kp++) {
-                if (kp * 32 >= D) break;
-                uint32_t a[2][4];
-                query_fragment<FP8, C::kQB>(a[0], qs, wm * 16, 2 * kp);
-                query_fragment<FP8, C::kQB>(a[1], qs, wm * 16, 2 * kp + 1);
-#pragma unroll
-                for (int x = 0; x < C::kKeys / 16; x++) {
-                    uint32_t r[4];
-                    ldsm4(r, ks + chunk_at<C::kRB>(mykey + x * 16 + ((lane / 8) & 1) * 8 + lane % 8, 2 * kp + lane / 16));
-#pragma unroll
-                    for (int y = 0; y < 4; y++)
-                        mma16816<T>(s[2 * x + (y & 1)], a[y >> 1], uzip::prmt(r[y], 0, 0x1404), uzip::prmt(r[y], 0, 0x3424));
-                }
-            }
+            bar_arrive_copies(full + 8 * s);
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else {
+        // ---- products
+        const uint32_t wm = warp % WM, wn = warp / WM, mykey = wn * C::kKeys;
+        uint32_t q[RN][DP / 16][2];
+        float o[DP / 16][RN][4], f[RN][2], ref[RN][2], sum[RN][2];  // rows 2 l and 2 l + 1 of each tile of eight
+        uint32_t merges = 0;
+        bool begun = false;
+        // Column of o[x][.][y]: x * 16 + g + 8 (y / 2), or with the even and odd columns apart.
+        auto column = [&](int x, int y) { return x * 16 + (FP8 ? 2 * g + y / 2 : g + 8 * (y / 2)); };
 
-        // Running maximum and sum; scores in units of log2.
-        const float f0 = FP8 ? factor[row0] : p.scale * kLog2e, f1 = FP8 ? factor[row0 + 8] : f0;
+        for (uint32_t i = 0; i < n && ok; i++) {
+            const uint32_t row0 = cur.mt * C::kM + wm * 8 * RN;
+            if (!begun) {
+                begun = true;
+                // This warp's queries, as the second operand: row g of each tile of eight.
 #pragma unroll
-        for (int x = 0; x < C::kKeys / 8; x++) {
-            s[x][0] *= f0;
-            s[x][1] *= f0;
-            s[x][2] *= f1;
-            s[x][3] *= f1;
-        }
-        const bool masked = j0 + kTile > cur.span.old;
-        bool dirty = false;
-        uint64_t seen[2] = {~0ull, ~0ull};
-        if (masked) {
-            // A value that a row does not see must not reach it through 0 * NaN: non-finite values of new tokens
-            // leave the tile here and are added below to the rows that see them.
-            int found = 0;
-            for (uint32_t c = tid; c < kTile * (C::kRB / 16); c += kAttThreads) {
-                const uint32_t r = c / (C::kRB / 16);
-                if (j0 + r < cur.span.old) continue;
-                uint32_t* w = reinterpret_cast<uint32_t*>(stage + kTile * C::kRB + chunk_at<C::kRB>(r, c % (C::kRB / 16)));
+                for (int t = 0; t < RN; t++) {
+                    const uint32_t row = row0 + 8 * t + g;
+                    const uint32_t tok = row / p.group, head = row - tok * p.group;
+                    const bool have = row < p.rows;
+                    const char* src = p.q.p + cur.b * p.q.b + (have ? tok * p.q.t + (uint64_t)(cur.h * p.group + head) * p.q.h : 0);
+                    float top = 0.0f;
 #pragma unroll
-                for (int y = 0; y < 4; y++) {
-                    uint32_t v = w[y], keep = 0;
-                    if (FP8) {
-                        for (int z = 0; z < 4; z++) keep |= ((v >> (8 * z)) & 0x7C) != 0x7C ? 0xFFu << (8 * z) : 0;
-                    } else {
-                        constexpr uint32_t kExp = std::is_same<T, __half>::value ? 0x7C00u : 0x7F80u;
-                        for (int z = 0; z < 2; z++) keep |= ((v >> (16 * z)) & kExp) != kExp ? 0xFFFFu << (16 * z) : 0;
+                    for (int kk = 0; kk < DP / 16; kk++)
+#pragma unroll
+                        for (int y = 0; y < 2; y++) {
+                            const uint32_t d = kk * 16 + (FP8 ? 4 * l + 2 * y : 2 * l + 8 * y);
+                            q[t][kk][y] = have && d < D ? *reinterpret_cast<const uint32_t*>(src + 2 * d) : 0;
+                            if (!std::is_same<QT, T>::value) {
+                                const QT* e = reinterpret_cast<const QT*>(&q[t][kk][y]);
+                                top = fmaxf(top, fmaxf(fabsf(to_f32(e[0])), fabsf(to_f32(e[1]))));
+                            }
+                        }
+                    float up = 1.0f;
+                    if (!std::is_same<QT, T>::value) {
+                        // BF16 queries of an FP16 product: a power of two out of the row brings its largest element to [1, 2).
+                        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+                        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+                        const uint32_t ex = __float_as_uint(top) >> 23;
+                        const bool plain = ex > 0 && ex < 254;  // not a row of zeros or subnormals, or with an infinity
+                        const float down = plain ? __uint_as_float((254 - ex) << 23) : 1.0f;
+                        up = plain ? __uint_as_float(ex << 23) : 1.0f;
+#pragma unroll
+                        for (int kk = 0; kk < DP / 16; kk++)
+#pragma unroll
+                            for (int y = 0; y < 2; y++) {
+                                const QT* e = reinterpret_cast<const QT*>(&q[t][kk][y]);
+                                q[t][kk][y] = pack2<__half>(to_f32(e[0]) * down, to_f32(e[1]) * down);
+                            }
                     }
-                    if (keep != 0xFFFFFFFFu) {
-                        w[y] = v & keep;
-                        found = 1;
-                    }
-                }
-            }
-            dirty = __syncthreads_or(found);
-            seen[0] = seen_bits(p, cur.b, cur.span, (uint32_t)r0 + row0, j0) >> mykey;
-            seen[1] = seen_bits(p, cur.b, cur.span, (uint32_t)r0 + row0 + 8, j0) >> mykey;
-#pragma unroll
-            for (int x = 0; x < C::kKeys / 8; x++)
-#pragma unroll
-                for (int y = 0; y < 4; y++)
-                    if (!((seen[y >> 1] >> (x * 8 + 2 * l + (y & 1))) & 1)) s[x][y] = -INFINITY;
-        }
-        float most[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-        for (int x = 0; x < C::kKeys / 8; x++) {
-            most[0] = fmaxf(most[0], fmaxf(s[x][0], s[x][1]));
-            most[1] = fmaxf(most[1], fmaxf(s[x][2], s[x][3]));
-        }
-        float ref[2], fade[2];
-        bool moved = false;
-#pragma unroll
-        for (int y = 0; y < 2; y++) {
-            most[y] = fmaxf(most[y], __shfl_xor_sync(0xFFFFFFFFu, most[y], 1));
-            most[y] = fmaxf(most[y], __shfl_xor_sync(0xFFFFFFFFu, most[y], 2));
-            const float now = fmaxf(top[y], most[y]);
-            fade[y] = top[y] == -INFINITY ? 0.0f : exp2_fast(top[y] - now);  // 0: nothing so far
-            moved |= now != top[y];
-            top[y] = now;
-            ref[y] = now == -INFINITY ? 0.0f : now - kLift<T>;
-        }
-        if (__any_sync(0xFFFFFFFFu, moved)) {
-            sum[0] *= fade[0];
-            sum[1] *= fade[1];
-#pragma unroll
-            for (int x = 0; x < DP / 8; x++) {
-                o[x][0] *= fade[0];
-                o[x][1] *= fade[0];
-                o[x][2] *= fade[1];
-                o[x][3] *= fade[1];
-            }
-        }
-        uint32_t pr[C::kKeys / 8][2];  // weights, rounded to the products' type; their sum is of the unrounded ones
-#pragma unroll
-        for (int x = 0; x < C::kKeys / 8; x++) {
-            const float e0 = exp2_fast(s[x][0] - ref[0]), e1 = exp2_fast(s[x][1] - ref[0]);
-            const float e2 = exp2_fast(s[x][2] - ref[1]), e3 = exp2_fast(s[x][3] - ref[1]);
-            sum[0] += e0 + e1;
-            sum[1] += e2 + e3;
-            pr[x][0] = pack2<T>(e0, e1);
-            pr[x][1] = pack2<T>(e2, e3);
-        }
-
-        // Values.
-#pragma unroll
-        for (int ksx = 0; ksx < C::kKeys / 16; ksx++) {
-            const uint32_t a[4] = {pr[2 * ksx][0], pr[2 * ksx][1], pr[2 * ksx + 1][0], pr[2 * ksx + 1][1]};
-            const uint32_t key = mykey + ksx * 16 + ((lane / 8) & 1) * 8 + lane % 8;
-            if (!FP8) {
-#pragma unroll
-                for (int x = 0; x < DP / 16; x++) {
-                    if (x * 16 >= D) break;
-                    uint32_t bfr[4];
-                    ldsm4_t(bfr, vs + chunk_at<C::kRB>(key, 2 * x + lane / 16));
-                    mma16816<T>(o[2 * x], a, bfr[0], bfr[1]);
-                    mma16816<T>(o[2 * x + 1], a, bfr[2], bfr[3]);
-                }
-            } else {
-#pragma unroll
-                for (int x = 0; x < DP / 32; x++) {
-                    if (x * 32 >= D) break;
-                    uint32_t r[4];
-                    ldsm4_t(r, vs + chunk_at<C::kRB>(key, 2 * x + lane / 16));
-#pragma unroll
-                    for (int y = 0; y < 2; y++) {  // 16 columns: the even ones, then the odd ones
-                        mma16816<T>(o[4 * x + 2 * y], a, uzip::prmt(r[2 * y], 0, 0x2404), uzip::prmt(r[2 * y + 1], 0, 0x2404));
-                        mma16816<T>(o[4 * x + 2 * y + 1], a, uzip::prmt(r[2 * y], 0, 0x3414), uzip::prmt(r[2 * y + 1], 0, 0x3414));
-                    }
-                }
-            }
-        }
-        // Column of o[x][y] (and y + 2): x * 8 + 2 l + y, or with the even and odd columns apart.
-        auto column = [&](int x, int y) { return FP8 ? (x / 2) * 16 + 4 * l + 2 * y + (x & 1) : x * 8 + 2 * l + y; };
-
-        if (dirty) {
-            const uint32_t upto = cur.span.old + cur.span.fresh;
-            for (uint32_t k = 0; k < C::kKeys; k++) {
-                const uint32_t j = j0 + mykey + k;
-                if (j < cur.span.old || j >= upto) continue;
-                const Place pl = place_of(p.cache, cur.b, j);
-                if (pl.page < 0) continue;
-                const char* v = v_row(p.cache, pl, cur.h);
-#pragma unroll
-                for (int x = 0; x < DP / 8; x++)
 #pragma unroll
                     for (int y = 0; y < 2; y++) {
-                        const uint32_t d = column(x, y);
-                        if (d >= D) continue;
-                        const float e = FP8 ? to_f32(reinterpret_cast<const E5M2*>(v)[d]) : to_f32(reinterpret_cast<const T*>(v)[d]);
-                        if (isfinite(e)) continue;
-                        if ((seen[0] >> k) & 1) o[x][y] += e;
-                        if ((seen[1] >> k) & 1) o[x][y + 2] += e;
+                        f[t][y] = p.scale * kLog2e * __shfl_sync(0xFFFFFFFFu, up, (2 * l + y) * 4);  // from a lane with that row
+                        ref[t][y] = -INFINITY;
+                        sum[t][y] = 0.0f;
                     }
+                }
+#pragma unroll
+                for (int x = 0; x < DP / 16; x++)
+#pragma unroll
+                    for (int t = 0; t < RN; t++)
+#pragma unroll
+                        for (int y = 0; y < 4; y++) o[x][t][y] = 0.0f;
             }
-        }
+            const uint32_t s = i % C::kStages;
+            ok = warp_wait(full + 8 * s, (i / C::kStages) & 1);
+            if (!ok) break;
+            const uint32_t ks = smem_u32(smem + s * C::kStage), vs = ks + C::kTile * C::kRB;
+            const uint32_t j0 = cur.tile * C::kTile + mykey;
+            const bool masked = cur.tile * C::kTile + C::kTile > cur.span.old;
 
-        // End of the unit or of this CTA's run: a whole unit's rows are done, a part goes to the workspace.
-        const Unit done = cur;
-        const bool to_end = done.tile + 1 == done.tiles;
-        advance(p, cur, p.mtiles);
-        static_assert(kTile == 64, "seen_bits");
-        if (!to_end && i + 1 < n) {
-            fresh_unit = false;
-            continue;
-        }
-        fresh_unit = true;
-        for (int y = 0; y < 2; y++) {
-            sum[y] += __shfl_xor_sync(0xFFFFFFFFu, sum[y], 1);
-            sum[y] += __shfl_xor_sync(0xFFFFFFFFu, sum[y], 2);
-        }
-        float mref[2] = {top[0] == -INFINITY ? 0.0f : top[0] - kLift<T>, top[1] == -INFINITY ? 0.0f : top[1] - kLift<T>};
-        if (C::kWN > 1) {
-            // Token shares, one warp after the other, through the queries' space.
-            float* box = reinterpret_cast<float*>(qs);
-            float* stat = box + C::kM * DP;
-            for (int w = C::kWN - 1; w >= 0; w--) {
-                __syncthreads();
-                if ((int)wn != w) continue;
+#pragma unroll
+            for (int sub = 0; sub < C::kKeys / C::kSub; sub++) {
+                const uint32_t key0 = mykey + sub * C::kSub;
+                constexpr int kB = C::kSub / 16;             // blocks of 16 tokens
+                constexpr int kChains = kB * RN == 1 ? 2 : 1;  // a lone accumulator would wait for itself at every step
+                float sc[kChains][kB][RN][4];
+#pragma unroll
+                for (int h = 0; h < kChains; h++)
+#pragma unroll
+                    for (int x = 0; x < kB; x++)
+#pragma unroll
+                        for (int t = 0; t < RN; t++)
+#pragma unroll
+                            for (int y = 0; y < 4; y++) sc[h][x][t][y] = 0.0f;
+#pragma unroll
+                for (int x = 0; x < kB; x++) {
+                    const uint32_t base = ks + chunk_at<C::kRB>(key0 + x * 16 + lane % 16, lane / 16);
+                    if (!FP8) {
+#pragma unroll
+                        for (int kk = 0; kk < DP / 16; kk++) {
+                            uint32_t a[4];
+                            ldsm4(a, base ^ (kk << 5));
+#pragma unroll
+                            for (int t = 0; t < RN; t++) mma16816<T>(sc[kk % kChains][x][t], a, q[t][kk][0], q[t][kk][1]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int kp = 0; kp < DP / 32; kp++) {
+                            uint32_t r[4];
+                            ldsm4(r, base ^ (kp << 5));
+#pragma unroll
+                            for (int y = 0; y < 2; y++) {
+                                const uint32_t a[4] = {uzip::prmt(r[2 * y], 0, 0x1404), uzip::prmt(r[2 * y + 1], 0, 0x1404),
+                                                       uzip::prmt(r[2 * y], 0, 0x3424), uzip::prmt(r[2 * y + 1], 0, 0x3424)};
+#pragma unroll
+                                for (int t = 0; t < RN; t++)
+                                    mma16816<T>(sc[y % kChains][x][t], a, q[t][2 * kp + y][0], q[t][2 * kp + y][1]);
+                            }
+                        }
+                    }
+                }
+                // Scores in units of log2: element y of a block is token g + 8 (y / 2) and row 2 l + y % 2.
+                uint64_t seen[RN][2];
+                if (masked)
+#pragma unroll
+                    for (int t = 0; t < RN; t++)
+#pragma unroll
+                        for (int y = 0; y < 2; y++)
+                            seen[t][y] = seen_bits(p, cur.b, cur.span, row0 + 8 * t + 2 * l + y, j0 + sub * C::kSub);
+                float most[RN][2];
+                bool rise = false;
+#pragma unroll
+                for (int t = 0; t < RN; t++) {
+                    most[t][0] = most[t][1] = -INFINITY;
+#pragma unroll
+                    for (int x = 0; x < kB; x++)
+#pragma unroll
+                        for (int y = 0; y < 4; y++) {
+                            float v = sc[0][x][t][y];
+                            if (kChains == 2) v += sc[kChains - 1][x][t][y];
+                            v *= f[t][y & 1];
+                            if (masked && !((seen[t][y & 1] >> (x * 16 + g + 8 * (y / 2))) & 1)) v = -INFINITY;
+                            sc[0][x][t][y] = v;
+                            most[t][y & 1] = fmaxf(most[t][y & 1], v);
+                        }
+                    rise |= most[t][0] > ref[t][0] + kSlack || most[t][1] > ref[t][1] + kSlack;
+                }
+                if (__any_sync(0xFFFFFFFFu, rise)) {
+#pragma unroll
+                    for (int t = 0; t < RN; t++) {
+                        float fade[2];
+#pragma unroll
+                        for (int y = 0; y < 2; y++) {
+                            float m = most[t][y];
+                            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
+                            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
+                            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
+                            m = fmaxf(m, ref[t][y]);
+                            fade[y] = ref[t][y] == -INFINITY ? 0.0f : exp2_fast(ref[t][y] - m);  // 0: nothing so far
+                            ref[t][y] = m;
+                            sum[t][y] *= fade[y];
+                        }
+#pragma unroll
+                        for (int x = 0; x < DP / 16; x++)
+#pragma unroll
+                            for (int y = 0; y < 4; y++) o[x][t][y] *= fade[y & 1];
+                    }
+                }
+                // Weights, rounded to the products' type; their sum is of the unrounded ones.
+                uint32_t w[kB][RN][2];
+#pragma unroll
+                for (int t = 0; t < RN; t++) {
+                    const float r0 = ref[t][0] == -INFINITY ? 0.0f : ref[t][0] - kLift<T>;
+                    const float r1 = ref[t][1] == -INFINITY ? 0.0f : ref[t][1] - kLift<T>;
+#pragma unroll
+                    for (int x = 0; x < kB; x++) {
+                        const float e0 = exp2_fast(sc[0][x][t][0] - r0), e1 = exp2_fast(sc[0][x][t][1] - r1);
+                        const float e2 = exp2_fast(sc[0][x][t][2] - r0), e3 = exp2_fast(sc[0][x][t][3] - r1);
+                        sum[t][0] += e0 + e2;
+                        sum[t][1] += e1 + e3;
+                        w[x][t][0] = transpose8(pack2<T>(e0, e1));
+                        w[x][t][1] = transpose8(pack2<T>(e2, e3));
+                    }
+                }
+                // A value that a row does not see must not reach it through 0 * NaN: where the tile has new tokens,
+                // non-finite values are taken out of the product and added below to the rows that see them.
+                uint32_t odd = 0;
+#pragma unroll
+                for (int x = 0; x < kB; x++) {
+                    if (!FP8) {
+                        const uint32_t base = vs + chunk_at<C::kRB>(key0 + x * 16 + (lane / 16) * 8 + lane % 8, (lane / 8) % 2);
+#pragma unroll
+                        for (int dx = 0; dx < DP / 16; dx++) {
+                            uint32_t a[4];
+                            ldsm4_t(a, base ^ (dx << 5));
+                            if (masked)
+#pragma unroll
+                                for (int y = 0; y < 4; y++) odd |= clean2<T>(a[y]);
+#pragma unroll
+                            for (int t = 0; t < RN; t++) mma16816<T>(o[dx][t], a, w[x][t][0], w[x][t][1]);
+                        }
+                    } else {
+                        const uint32_t base = vs + chunk_at<C::kRB>(key0 + x * 16 + ((lane / 8) % 2) * 8 + lane % 8, lane / 16);
+#pragma unroll
+                        for (int dp = 0; dp < DP / 32; dp++) {
+                            uint32_t r[4];
+                            ldsm4_t(r, base ^ (dp << 5));
+#pragma unroll
+                            for (int y = 0; y < 2; y++) {
+                                uint32_t a[4] = {uzip::prmt(r[2 * y], 0, 0x2404), uzip::prmt(r[2 * y], 0, 0x3414),
+                                                 uzip::prmt(r[2 * y + 1], 0, 0x2404), uzip::prmt(r[2 * y + 1], 0, 0x3414)};
+                                if (masked)
+#pragma unroll
+                                    for (int z = 0; z < 4; z++) odd |= clean2<T>(a[z]);
+#pragma unroll
+                                for (int t = 0; t < RN; t++) mma16816<T>(o[2 * dp + y][t], a, w[x][t][0], w[x][t][1]);
+                            }
+                        }
+                    }
+                }
+                if (masked && __any_sync(0xFFFFFFFFu, odd != 0)) {
+                    const uint32_t upto = cur.span.old + cur.span.fresh;
+                    for (uint32_t k = 0; k < C::kSub; k++) {
+                        const uint32_t j = j0 + sub * C::kSub + k;
+                        if (j >= upto) break;
+                        const Place pl = place_of(p.cache, cur.b, j);
+                        if (pl.page < 0) continue;
+                        const char* v = v_row(p.cache, pl, cur.h);
+#pragma unroll
+                        for (int x = 0; x < DP / 16; x++)
+#pragma unroll
+                            for (int y = 0; y < 4; y += 2) {
+                                const uint32_t d = column(x, y);
+                                if (d >= D) continue;
+                                const float e = FP8 ? to_f32(reinterpret_cast<const E5M2*>(v)[d]) : to_f32(reinterpret_cast<const T*>(v)[d]);
+                                if (isfinite(e)) continue;
+#pragma unroll
+                                for (int t = 0; t < RN; t++) {
+                                    if ((seen[t][0] >> k) & 1) o[x][t][y] += e;
+                                    if ((seen[t][1] >> k) & 1) o[x][t][y + 1] += e;
+                                }
+                            }
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) bar_arrive(freed + 8 * s);
+
+            const Unit done = cur;
+            advance(p, cur, p.mtiles);
+            const bool to_end = done.tile + 1 == done.tiles;
+            if (!to_end && i + 1 < n) continue;
+            // ---- end of the unit or of this CTA's run: merge the warps' token shares. A whole unit's rows are
+            // finished, a part of one goes to the workspace.
+            begun = false;
+            const bool from_start = done.tile <= i;  // its first tile is in this run
+            float* const part = p.partial + ((uint64_t)blockIdx.x * 2 + (from_start ? 1 : 0)) * partial_floats(p);
+#pragma unroll
+            for (int t = 0; t < RN; t++) {
+                float* mine = box + warp * 8 * C::kBoxRow;
+#pragma unroll
+                for (int x = 0; x < DP / 16; x++)
+#pragma unroll
+                    for (int y = 0; y < 2; y++) {
+                        float* at = mine + (2 * l + y) * C::kBoxRow + column(x, 0);
+                        if (!FP8) {
+                            at[0] = o[x][t][y];
+                            at[8] = o[x][t][y + 2];
+                        } else {
+                            *reinterpret_cast<float2*>(at) = make_float2(o[x][t][y], o[x][t][y + 2]);
+                        }
+                    }
 #pragma unroll
                 for (int y = 0; y < 2; y++) {
-                    const uint32_t r = row0 + 8 * y;
-                    float mine = 1.0f, theirs = 0.0f;
-                    if (w < C::kWN - 1) {
-                        const float om = stat[2 * r], os = stat[2 * r + 1];
-                        const float both = sum[y] == 0.0f ? om : os == 0.0f ? mref[y] : fmaxf(om, mref[y]);
-                        mine = sum[y] == 0.0f ? 0.0f : exp2_fast(mref[y] - both);
-                        theirs = os == 0.0f ? 0.0f : exp2_fast(om - both);
-                        sum[y] = sum[y] * mine + os * theirs;
-                        mref[y] = both;
-                    }
-#pragma unroll
-                    for (int x = 0; x < DP / 8; x++) {
-                        float2* at = reinterpret_cast<float2*>(box + r * DP + (x ^ (r & 7)) * 8 + 2 * l);  // rows apart in the banks
-                        float a0 = o[x][2 * y], a1 = o[x][2 * y + 1];
-                        if (w < C::kWN - 1) {
-                            const float2 v = *at;
-                            a0 = a0 * mine + v.x * theirs;
-                            a1 = a1 * mine + v.y * theirs;
-                            o[x][2 * y] = a0;
-                            o[x][2 * y + 1] = a1;
-                        }
-                        if (w) *at = make_float2(a0, a1);
-                    }
-                    __syncwarp();
-                    if (w && l == 0) {
-                        stat[2 * r] = mref[y];
-                        stat[2 * r + 1] = sum[y];
-                    }
+                    float v = sum[t][y];
+                    v += __shfl_xor_sync(0xFFFFFFFFu, v, 4);
+                    v += __shfl_xor_sync(0xFFFFFFFFu, v, 8);
+                    v += __shfl_xor_sync(0xFFFFFFFFu, v, 16);
+                    if (g == 0) stat[warp * 8 + 2 * l + y] = make_float2(ref[t][y] == -INFINITY ? 0.0f : ref[t][y] - kLift<T>, v);
                 }
-            }
-        }
-        if (wn != 0) continue;
-        const bool started = done.tile <= i;  // its first tile is in this run
-        if (started && to_end) {
+                __syncwarp();
+                if (lane == 0) bar_arrive(merge);
+                ok = warp_wait(merge, merges++ & 1);
+                if (!ok) break;
+                // Four columns a thread, D / 4 threads a row.
+                const uint32_t per = D / 4;
+                for (uint32_t e = tid; e < WM * 8 * per; e += 256) {
+                    const uint32_t r8 = e / per, d = (e - r8 * per) * 4, rm = r8 / 8, rn = r8 % 8;
+                    const uint32_t r = rm * 8 * RN + 8 * t + rn, row = done.mt * C::kM + r;
+                    if (row >= p.rows) continue;
+                    float top = -INFINITY;
 #pragma unroll
-            for (int y = 0; y < 2; y++) {
-                const uint32_t row = (uint32_t)r0 + row0 + 8 * y;
-                if (row >= p.rows) continue;
-                const uint32_t t = row / p.group, hq = done.h * p.group + row % p.group;
-                const bool none = t >= done.span.fresh || sum[y] == 0.0f;
-                const float inv = none ? 0.0f : 1.0f / sum[y];
-                char* out = p.out.p + done.b * p.out.b + t * p.out.t + (uint64_t)hq * p.out.h;
-                if (!FP8) {
+                    for (int k = 0; k < C::kWN; k++) {
+                        const float2 st = stat[(k * WM + rm) * 8 + rn];
+                        if (st.y != 0.0f) top = fmaxf(top, st.x);
+                    }
+                    float all = 0.0f;
+                    float4 acc = make_float4(0, 0, 0, 0);
 #pragma unroll
-                    for (int x = 0; x < DP / 8; x++)
-                        if ((uint32_t)x * 8 < D)
-                            *reinterpret_cast<uint32_t*>(out + 2 * (x * 8 + 2 * l)) =
-                                none ? 0u : pack2<QT>(o[x][2 * y] * inv, o[x][2 * y + 1] * inv);
-                } else {
-#pragma unroll
-                    for (int x = 0; x < DP / 16; x++)
-                        if ((uint32_t)x * 16 < D)
-                            *reinterpret_cast<uint2*>(out + 2 * (x * 16 + 4 * l)) =
-                                none ? make_uint2(0, 0)
-                                     : make_uint2(pack2<QT>(o[2 * x][2 * y] * inv, o[2 * x + 1][2 * y] * inv),
-                                                  pack2<QT>(o[2 * x][2 * y + 1] * inv, o[2 * x + 1][2 * y + 1] * inv));
-                }
-                if (p.lse && l == 0)
-                    p.lse[((uint64_t)done.b * p.tokens + t) * p.q_heads + hq] = none ? -INFINITY : (mref[y] + log2f(sum[y])) * kLn2;
-            }
-        } else {
-            float* part = p.partial + ((uint64_t)blockIdx.x * 2 + (started ? 1 : 0)) * partial_floats(p);
-#pragma unroll
-            for (int y = 0; y < 2; y++) {
-                const uint32_t r = row0 + 8 * y, row = (uint32_t)r0 + r;
-                if (row >= p.rows) continue;
-#pragma unroll
-                for (int x = 0; x < DP / 8; x++) {
-                    if (column(x, 0) >= D) continue;
-                    if (!FP8) {
-                        *reinterpret_cast<float2*>(part + (uint64_t)r * DP + column(x, 0)) = make_float2(o[x][2 * y], o[x][2 * y + 1]);
-                    } else if (x % 2 == 0) {
-                        *reinterpret_cast<float4*>(part + (uint64_t)r * DP + column(x, 0)) =
-                            make_float4(o[x][2 * y], o[x + 1][2 * y], o[x][2 * y + 1], o[x + 1][2 * y + 1]);
+                    for (int k = 0; k < C::kWN; k++) {
+                        const float2 st = stat[(k * WM + rm) * 8 + rn];
+                        const float4 v = *reinterpret_cast<const float4*>(box + ((k * WM + rm) * 8 + rn) * C::kBoxRow + d);
+                        if (st.y == 0.0f) continue;
+                        const float e2 = exp2_fast(st.x - top);
+                        all += st.y * e2;
+                        acc.x += v.x * e2;
+                        acc.y += v.y * e2;
+                        acc.z += v.z * e2;
+                        acc.w += v.w * e2;
+                    }
+                    const uint32_t tok = row / p.group, hq = done.h * p.group + (row - tok * p.group);
+                    const bool none = tok >= done.span.fresh || all == 0.0f;
+                    if (from_start && to_end) {
+                        const float inv = none ? 0.0f : 1.0f / all;
+                        *reinterpret_cast<uint2*>(p.out.p + done.b * p.out.b + tok * p.out.t + (uint64_t)hq * p.out.h + 2 * d) =
+                            none ? make_uint2(0, 0)
+                                 : make_uint2(pack2<QT>(acc.x * inv, acc.y * inv), pack2<QT>(acc.z * inv, acc.w * inv));
+                        if (p.lse && d == 0)
+                            p.lse[((uint64_t)done.b * p.tokens + tok) * p.q_heads + hq] = none ? -INFINITY : (top + log2f(all)) * kLn2;
+                    } else {
+                        *reinterpret_cast<float4*>(part + (uint64_t)r * DP + d) = acc;
+                        if (d == 0) *reinterpret_cast<float2*>(part + (uint64_t)C::kM * DP + 2 * r) = make_float2(top, none ? 0.0f : all);
                     }
                 }
-                if (l == 0) {
-                    part[(uint64_t)C::kM * DP + 2 * r] = mref[y];
-                    part[(uint64_t)C::kM * DP + 2 * r + 1] = row / p.group < done.span.fresh ? sum[y] : 0.0f;
-                }
+                __syncwarp();
+                if (lane == 0) bar_arrive(merge);
+                ok = warp_wait(merge, merges++ & 1);
+                if (!ok) break;
             }
         }
     }
+    if (!ok && p.cache.status) *p.cache.status = UZIP_ERR_TIMEOUT;
 }
 
-template <typename QT, bool FP8, int DP, int WM>
+template <typename QT, bool FP8, int DP, int RN, int WM>
 int launch_attend_as(AttParams& p, int sms, cudaStream_t stream) {
-    using C = AttCfg<QT, FP8, DP, WM>;
+    using C = AttCfg<QT, FP8, DP, RN, WM>;
     static std::atomic<uint64_t> ready{0};  // a bit for each device whose limit is raised
     int dev = 0;
     UZIP_CUDA_TRY(cudaGetDevice(&dev));
     if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
-        UZIP_CUDA_TRY(cudaFuncSetAttribute(attend_kernel<QT, FP8, DP, WM>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem));
+        UZIP_CUDA_TRY(cudaFuncSetAttribute(attend_kernel<QT, FP8, DP, RN, WM>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem));
         if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
     p.m = C::kM;
     p.mtiles = (p.rows + C::kM - 1) / C::kM;
     p.dp = DP;
-    p.shift = 6;
-    static_assert(kTile == 1u << 6, "tile");
-    p.grid = std::min<uint32_t>((uint32_t)sms * C::kCtas, kMaxAttGrid);
-    attend_kernel<QT, FP8, DP, WM><<<p.grid, kAttThreads, C::kSmem, stream>>>(p);
+    p.shift = C::kTile == 128 ? 7 : 6;
+    p.grid = std::min<uint32_t>((uint32_t)sms, kMaxAttGrid);
+    attend_kernel<QT, FP8, DP, RN, WM><<<p.grid, kAttThreads, C::kSmem, stream>>>(p);
     UZIP_CUDA_TRY(cudaGetLastError());
     return UZIP_OK;
 }
 
-// Rows a CTA takes at once: the fewest that hold all, up to 64.
+// Rows a CTA takes at once: the fewest of 8 (heads up to 128), 16, 32 and 64 that hold all, else 64.
 template <typename QT, bool FP8, int DP>
 int launch_attend_rows(AttParams& p, int sms, cudaStream_t s) {
-    if (p.rows <= 16) return launch_attend_as<QT, FP8, DP, 1>(p, sms, s);
-    if (p.rows <= 32) return launch_attend_as<QT, FP8, DP, 2>(p, sms, s);
-    return launch_attend_as<QT, FP8, DP, 4>(p, sms, s);
+    if constexpr (DP <= 128) {
+        if (p.rows <= 8) return launch_attend_as<QT, FP8, DP, 1, 1>(p, sms, s);
+        if (p.rows <= 16) return launch_attend_as<QT, FP8, DP, 2, 1>(p, sms, s);
+        if (p.rows <= 32) return launch_attend_as<QT, FP8, DP, 2, 2>(p, sms, s);
+        return launch_attend_as<QT, FP8, DP, 2, 4>(p, sms, s);
+    } else {  // eight rows a warp: 16 would not leave registers for the output
+        if (p.rows <= 16) return launch_attend_as<QT, FP8, DP, 1, 2>(p, sms, s);
+        if (p.rows <= 32) return launch_attend_as<QT, FP8, DP, 1, 4>(p, sms, s);
+        return launch_attend_as<QT, FP8, DP, 1, 8>(p, sms, s);
+    }
 }
 
 template <typename QT, bool FP8>

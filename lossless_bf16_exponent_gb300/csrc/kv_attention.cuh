@@ -11,13 +11,7 @@
 // takes at one chunk lie in eight different bank groups.
 //
 // E5M2 rows stay bytes in shared memory. E5M2 is the upper byte of FP16, so a
-// byte permute widens two of them to a pair that the FP16 product takes. A
-// matrix load of 16-bit units gives a thread four consecutive bytes of a key
-// row, where the product's layout wants two pairs eight apart; the sum over
-// the head dimension may run in any order, so the queries are read in the
-// same permuted one. For the values, a transposed load gives the bytes of two
-// neighbouring columns; they go to two products, one for the even and one for
-// the odd columns.
+// byte permute widens two of them to a pair that the FP16 product takes.
 #pragma once
 
 #include <type_traits>
@@ -26,9 +20,7 @@
 
 namespace uzkv {
 
-constexpr int kAttThreads = 128;
-constexpr uint32_t kTile = 64;          // cached tokens a step of the warp-level attention
-constexpr uint32_t kMaxAttGrid = 320;   // bounds the workspace: two CTAs on each of up to 160 SMs
+constexpr uint32_t kMaxAttGrid = 160;   // bounds the workspace; one CTA an SM
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -80,22 +72,31 @@ __device__ __forceinline__ uint32_t tiles_of(const AttParams& p, uint32_t b) {
     return b < p.cache.sequences ? tiles_of(p, span_of(p.cache, p.counts, p.tokens, b)) : 0;
 }
 
-// All lanes of a warp: tiles of all sequences, one (head, row tile) each.
-__device__ __forceinline__ uint64_t all_tiles(const AttParams& p) {
-    uint64_t n = 0;
-    for (uint32_t b = threadIdx.x % 32; b < p.cache.sequences; b += 32) n += tiles_of(p, b);
-    for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
-    return n;
+// What a warp knows of the split: the tiles of all sequences (one head and row tile each), and of sequence `lane`.
+struct Split {
+    uint64_t all;
+    uint32_t mine;
+};
+
+// All lanes of a warp.
+__device__ __forceinline__ Split split_of(const AttParams& p) {
+    const uint32_t lane = threadIdx.x % 32;
+    Split s;
+    s.mine = tiles_of(p, lane);
+    s.all = s.mine;
+    for (uint32_t b = lane + 32; b < p.cache.sequences; b += 32) s.all += tiles_of(p, b);
+    for (int o = 16; o; o >>= 1) s.all += __shfl_xor_sync(0xFFFFFFFFu, s.all, o);
+    return s;
 }
 
-// All lanes of a warp: the unit and tile at position `at` of the order, at < all tiles * per.
-__device__ __forceinline__ Unit unit_at(const AttParams& p, uint64_t at, uint32_t mtiles) {
+// All lanes of a warp: the unit and tile at position `at` of the order, at < all tiles * kv_heads * mtiles.
+__device__ __forceinline__ Unit unit_at(const AttParams& p, const Split& s, uint64_t at, uint32_t mtiles) {
     const uint32_t lane = threadIdx.x % 32;
     const uint64_t per = (uint64_t)p.cache.kv_heads * mtiles;
     uint64_t before = 0;
     Unit u{};
     for (uint32_t b0 = 0; b0 < p.cache.sequences; b0 += 32) {
-        const uint64_t mine = tiles_of(p, b0 + lane);
+        const uint64_t mine = b0 ? tiles_of(p, b0 + lane) : s.mine;
         uint64_t upto = mine;
         for (int o = 1; o < 32; o <<= 1) {
             const uint64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
@@ -107,11 +108,11 @@ __device__ __forceinline__ Unit unit_at(const AttParams& p, uint64_t at, uint32_
             const uint64_t start = __shfl_sync(0xFFFFFFFFu, before + upto - mine, l) * per;
             u.b = b0 + l;
             u.tiles = (uint32_t)__shfl_sync(0xFFFFFFFFu, mine, l);
-            const uint64_t in = at - start;
-            const uint32_t unit = (uint32_t)(in / u.tiles);
-            u.tile = (uint32_t)(in % u.tiles);
+            const uint32_t in = (uint32_t)(at - start);  // within one sequence
+            const uint32_t unit = in / u.tiles;
+            u.tile = in - unit * u.tiles;
             u.h = unit / mtiles;
-            u.mt = unit % mtiles;
+            u.mt = unit - u.h * mtiles;
             u.span = span_of(p.cache, p.counts, p.tokens, u.b);
             return u;
         }
@@ -211,10 +212,43 @@ __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
     return d;
 }
 
+// An 8 x 8 matrix of 16-bit elements across the warp, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t d;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(x));
+    return d;
+}
+
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// Waits for the phase of the given parity to end. Bounded: false after about a second, which only a fault in the
+// kernel's own counting could bring about; the caller then leaves its loop.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
+    for (uint32_t i = 0; i < (1u << 20); i++) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+        if (done) return true;
+    }
+    return false;
+}
+// The same for a whole warp, which stays together whatever the outcome.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, bar_wait(bar, parity)); }
+
+// One arrival once this thread's copies so far have landed; counted among the barrier's own.
+__device__ __forceinline__ void bar_arrive_copies(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // Byte offset of 16-byte chunk c of a row in a shared-memory tile of RB-byte rows.
@@ -224,12 +258,15 @@ __device__ __forceinline__ uint32_t chunk_at(uint32_t row, uint32_t c) {
     return row * RB + ((c ^ (RB >= 128 ? row & 7 : (row >> 1) & 3)) << 4);
 }
 
-// Weights go to the 16-bit product as exp2(x - max + kLift): lifted in FP16,
-// whose smallest normal number is 2^-14, by 2^8; BF16 has the range of FP32.
+// Weights go to the 16-bit product as exp2(x - reference), and the reference may trail the running maximum by
+// kSlack before a row is rescaled, so that most steps need neither the maximum over the warp nor the rescaling.
+// FP16, whose largest number is below 2^16 and whose smallest normal one is 2^-14, has the reference 2^6 below the
+// maximum it was taken from: weights up to 2^14. BF16 has the range of FP32.
+constexpr float kSlack = 8.0f;
 template <typename T>
 constexpr float kLift = 0.0f;
 template <>
-constexpr float kLift<__half> = 8.0f;
+constexpr float kLift<__half> = 6.0f;
 
 // Queries of rows row0 .. row0 + rows - 1 to shared memory as T (columns past head_dim and rows past p.rows
 // zero), by THREADS threads from thread 0 on; at(row, c) is where 16-byte chunk c of a row goes. factor[r *
@@ -271,23 +308,6 @@ __device__ __forceinline__ void load_queries(const AttParams& p, uint32_t b, uin
         }
         *at(i, c) = x;
         if (factor && c == 0) factor[i * STRIDE] = f;
-    }
-}
-
-// One 16-row fragment of queries for step kk (16 elements) of the head dimension.
-template <bool FP8, int RB>
-__device__ __forceinline__ void query_fragment(uint32_t* a, const char* smem, uint32_t row0, uint32_t kk) {
-    const uint32_t lane = threadIdx.x % 32;
-    if (!FP8) {
-        ldsm4(a, smem_u32(smem) + chunk_at<RB>(row0 + lane % 16, 2 * kk + lane / 16));
-    } else {  // elements 4 l .. 4 l + 3: in the order in which the key bytes come
-        const uint32_t g = lane / 4, l = lane % 4;
-        const uint2 x = *reinterpret_cast<const uint2*>(smem + chunk_at<RB>(row0 + g, 2 * kk + l / 2) + (l & 1) * 8);
-        const uint2 y = *reinterpret_cast<const uint2*>(smem + chunk_at<RB>(row0 + 8 + g, 2 * kk + l / 2) + (l & 1) * 8);
-        a[0] = x.x;
-        a[1] = y.x;
-        a[2] = x.y;
-        a[3] = y.y;
     }
 }
 

@@ -112,11 +112,12 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const __grid_cons
     tc_fence_after();
     const uint32_t tmem = *tmem_at;
 
-    const uint64_t total = all_tiles(p) * p.cache.kv_heads;
+    const Split split = split_of(p);
+    const uint64_t total = split.all * p.cache.kv_heads;
     const uint64_t shares = min(total, (uint64_t)p.grid);
     const uint64_t begin = blockIdx.x < shares ? total * blockIdx.x / shares : 0;
     const uint64_t n = blockIdx.x < shares ? total * (blockIdx.x + 1) / shares - begin : 0;
-    const Unit first = n ? unit_at(p, begin, 1) : Unit{};
+    const Unit first = n ? unit_at(p, split, begin, 1) : Unit{};
     bool ok = true;
 
     if (warp < 4) {

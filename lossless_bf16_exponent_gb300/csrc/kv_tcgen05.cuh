@@ -1,5 +1,5 @@
 // kv_tcgen05.cuh -- the fifth-generation tensor core in inline PTX: shared-
-// memory operand tiles, tensor memory, mbarriers with bounded waits.
+// memory operand tiles and tensor memory.
 //
 // An operand tile of R rows is one or more column blocks of 64 16-bit elements
 // (128 bytes): block k at k * R * 128 bytes, row r of a block at r * 128, its
@@ -63,26 +63,5 @@ __device__ __forceinline__ void tc_ld16(float* v, uint32_t addr) {
 
 // Writes of this thread to shared memory become visible to the tensor core's reads.
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-__device__ __forceinline__ void bar_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-// Waits for the phase of the given parity to end. Bounded: false after about a second, which only a fault in the
-// kernel's own counting could bring about; the caller then leaves its loop.
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
-    for (uint32_t i = 0; i < (1u << 20); i++) {
-        uint32_t done;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done) : "r"(bar), "r"(parity) : "memory");
-        if (done) return true;
-    }
-    return false;
-}
-// The same for a whole warp, which stays together whatever the outcome.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, bar_wait(bar, parity)); }
 
 }  // namespace uzkv
