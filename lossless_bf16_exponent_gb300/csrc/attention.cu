@@ -26,7 +26,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
     }
     uint64_t total = 0, before = 0;
     for (uint32_t i = lane; i < p.cache.sequences; i += 32) {
-        const uint32_t n = tiles_of(p, i);
+        const uint32_t n = width_of(p, tiles_of(p, i));
         total += n;
         before += i < b ? n : 0;
     }
@@ -37,9 +37,9 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
     const uint32_t tiles = tiles_of(p, b), mt = row / p.m, r = row % p.m;
     const uint64_t units = (uint64_t)p.cache.kv_heads * p.mtiles;
     total *= units;
-    const uint64_t start = before * units + ((uint64_t)h * p.mtiles + mt) * tiles;
+    const uint64_t start = before * units + ((uint64_t)h * p.mtiles + mt) * width_of(p, tiles) + p.unit_cost;  // of its tiles
     const uint64_t shares = min(total, (uint64_t)p.grid);
-    // CTA c has the tiles from total * c / shares on
+    // CTA c has the positions from total * c / shares on
     uint32_t c0 = 0, c1 = 0;
     if (tiles) {
         c0 = (uint32_t)(((start + 1) * shares - 1) / total);
@@ -110,6 +110,11 @@ int launch_join(const Params& p, cudaStream_t s) {
     return UZIP_OK;
 }
 
+// Rows of a (sequence, KV head) from which attention goes to the fifth-generation tensor cores.
+constexpr uint32_t kManyRows = 33;
+
+bool many(uint64_t rows, uint32_t head_dim) { return rows >= kManyRows && head_dim <= 128; }
+
 // What attention and mass check alike.
 int common(Params& p, const uzkv_rows_t* q, uint32_t dtype, uint32_t tokens, uint32_t q_heads, const int64_t* d_mask,
            int64_t mask_stride_b, const int32_t* d_counts, float scale, const uzkv_cache_t* cache) {
@@ -142,7 +147,7 @@ extern "C" UZIP_API size_t uzkv_tree_attention_workspace_bytes(uint32_t sequence
     if (!sequences || !tokens || tokens > UZKV_MAX_NEW_TOKENS || !q_heads || !kv_heads || q_heads % kv_heads ||
         !head_dim || head_dim > UZKV_MAX_HEAD_DIM)
         return 0;
-    const uint64_t rows = (uint64_t)tokens * (q_heads / kv_heads), m = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;  // at least a unit's rows
+    const uint64_t rows = (uint64_t)tokens * (q_heads / kv_heads), m = many(rows, head_dim) ? (rows <= 128 ? 128 : 256) : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;  // at least a unit's rows
     const uint64_t dp = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
     return (size_t)(kMaxAttGrid * 2 * m * (dp + 2) * 4);
 }
@@ -164,13 +169,12 @@ extern "C" UZIP_API int uzkv_tree_attention(const uzkv_rows_t* q, const uzkv_row
     int sms = 0;
     if (int rc = sm_count(&sms)) return rc;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const bool fp8 = cache->dtype == UZKV_E5M2;
-    if (dtype == UZKV_BF16) {
-        if (int rc = fp8 ? attend_bf16_e5m2(p, sms, s) : attend_bf16(p, sms, s)) return rc;
-        return launch_join<__nv_bfloat16>(p, s);
-    }
-    if (int rc = fp8 ? attend_fp16_e5m2(p, sms, s) : attend_fp16(p, sms, s)) return rc;
-    return launch_join<__half>(p, s);
+    using Launch = int (*)(AttParams&, int, cudaStream_t);
+    static constexpr Launch kLaunch[2][2][2] = {  // [many rows][FP16][E5M2 cache]
+        {{attend_bf16, attend_bf16_e5m2}, {attend_fp16, attend_fp16_e5m2}},
+        {{attend_many_bf16, attend_many_bf16_e5m2}, {attend_many_fp16, attend_many_fp16_e5m2}}};
+    if (int rc = kLaunch[many(p.rows, p.cache.head_dim)][dtype == UZKV_FP16][cache->dtype == UZKV_E5M2](p, sms, s)) return rc;
+    return dtype == UZKV_BF16 ? launch_join<__nv_bfloat16>(p, s) : launch_join<__half>(p, s);
 }
 
 extern "C" UZIP_API int uzkv_attention_mass(const uzkv_rows_t* q, const float* d_lse, uint32_t dtype, uint32_t tokens,

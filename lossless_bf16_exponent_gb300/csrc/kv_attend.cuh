@@ -54,17 +54,6 @@ struct AttCfg {
 
 constexpr int kAttThreads = 12 * 32;  // 8 warps that compute, 4 that copy
 
-// NaN and infinities of a pair of values (FP16 or BF16 patterns) become zero; whether there were any.
-template <typename T>
-__device__ __forceinline__ uint32_t clean2(uint32_t& v) {
-    constexpr uint32_t kExp = std::is_same<T, __half>::value ? 0x7C00u : 0x7F80u;
-    uint32_t bad = 0;
-    if ((v & kExp) == kExp) bad |= 0xFFFFu;
-    if ((v >> 16 & kExp) == kExp) bad |= 0xFFFF0000u;
-    v &= ~bad;
-    return bad;
-}
-
 template <typename QT, bool FP8, int DP, int RN, int WM>
 __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_constant__ AttParams p) {
     using C = AttCfg<QT, FP8, DP, RN, WM>;
@@ -88,12 +77,10 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
     if (D < DP)  // columns past the head dimension stay zero: no copy writes them
         for (uint32_t i = tid; i < C::kStages * C::kStage / 16; i += kAttThreads) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
     const Split split = split_of(p);
-    const uint64_t total = split.all * p.cache.kv_heads * p.mtiles;
-    const uint64_t shares = min(total, (uint64_t)p.grid);  // no share is empty
-    const bool any = blockIdx.x < shares;
-    const uint64_t begin = any ? total * blockIdx.x / shares : 0;
-    const uint32_t n = any ? (uint32_t)(total * (blockIdx.x + 1) / shares - begin) : 0;
-    Unit cur = any ? unit_at(p, split, begin, p.mtiles) : Unit{};
+    const Run run = run_of(p, split, p.mtiles);
+    Unit cur{};
+    cur.pos = ~0ull;
+    if (run.begin != run.end) cur = unit_at(p, split, run.begin, p.mtiles);
     __syncthreads();
     bool ok = true;
 
@@ -102,18 +89,18 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
         constexpr uint32_t kMine = C::kTile / 4, kLanes = C::kRB / 16;
         const uint32_t w = warp - 8, c = lane % kLanes, live = D * (FP8 ? 1 : 2) / 16;
         Place at{-1, 0};
-        auto find = [&](uint32_t i) {  // this lane's token of the tile under `cur`, which is the i-th of the run
+        auto find = [&]() {  // this lane's token of the tile under `cur`
             Place pl{-1, 0};
             const uint32_t j = cur.tile * C::kTile + w * kMine + lane;
-            if (i < n && lane < kMine && j < cur.span.old + cur.span.fresh) pl = place_of(p.cache, cur.b, j);
+            if (cur.pos < run.end && lane < kMine && j < cur.span.old + cur.span.fresh) pl = place_of(p.cache, cur.b, j);
             return pl;
         };
-        at = find(0);
-        for (uint32_t i = 0; i < n && ok; i++) {
+        at = find();
+        for (uint32_t i = 0; cur.pos < run.end && ok; i++) {
             const char* krow = at.page >= 0 ? k_row(p.cache, at, cur.h) : nullptr;
             const char* vrow = at.page >= 0 ? v_row(p.cache, at, cur.h) : nullptr;
             advance(p, cur, p.mtiles);
-            at = find(i + 1);
+            at = find();
             const uint32_t s = i % C::kStages;
             if (i >= C::kStages) ok = warp_wait(freed + 8 * s, (i / C::kStages - 1) & 1);
             if (!ok) break;
@@ -137,15 +124,16 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
         const uint32_t wm = warp % WM, wn = warp / WM, mykey = wn * C::kKeys;
         uint32_t q[RN][DP / 16][2];
         float o[DP / 16][RN][4], f[RN][2], ref[RN][2], sum[RN][2];  // rows 2 l and 2 l + 1 of each tile of eight
-        uint32_t merges = 0;
+        uint32_t merges = 0, first = 0;  // first: the tile with which this CTA began the unit
         bool begun = false;
         // Column of o[x][.][y]: x * 16 + g + 8 (y / 2), or with the even and odd columns apart.
         auto column = [&](int x, int y) { return x * 16 + (FP8 ? 2 * g + y / 2 : g + 8 * (y / 2)); };
 
-        for (uint32_t i = 0; i < n && ok; i++) {
+        for (uint32_t i = 0; cur.pos < run.end && ok; i++) {
             const uint32_t row0 = cur.mt * C::kM + wm * 8 * RN;
             if (!begun) {
                 begun = true;
+                first = cur.tile;
                 // This warp's queries, as the second operand: row g of each tile of eight.
 #pragma unroll
                 for (int t = 0; t < RN; t++) {
@@ -374,11 +362,11 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
             const Unit done = cur;
             advance(p, cur, p.mtiles);
             const bool to_end = done.tile + 1 == done.tiles;
-            if (!to_end && i + 1 < n) continue;
+            if (!to_end && cur.pos < run.end) continue;
             // ---- end of the unit or of this CTA's run: merge the warps' token shares. A whole unit's rows are
             // finished, a part of one goes to the workspace.
             begun = false;
-            const bool from_start = done.tile <= i;  // its first tile is in this run
+            const bool from_start = first == 0;
             float* const part = p.partial + ((uint64_t)blockIdx.x * 2 + (from_start ? 1 : 0)) * partial_floats(p);
 #pragma unroll
             for (int t = 0; t < RN; t++) {
@@ -471,6 +459,7 @@ int launch_attend_as(AttParams& p, int sms, cudaStream_t stream) {
     p.mtiles = (p.rows + C::kM - 1) / C::kM;
     p.dp = DP;
     p.shift = C::kTile == 128 ? 7 : 6;
+    p.unit_cost = 3;
     p.grid = std::min<uint32_t>((uint32_t)sms, kMaxAttGrid);
     attend_kernel<QT, FP8, DP, RN, WM><<<p.grid, kAttThreads, C::kSmem, stream>>>(p);
     UZIP_CUDA_TRY(cudaGetLastError());

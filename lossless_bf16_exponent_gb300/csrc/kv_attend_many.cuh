@@ -1,0 +1,532 @@
+// kv_attend_many.cuh -- attention over a paged cache for many rows (large
+// trees, many heads a KV head; head dimension up to 128) on the fifth-
+// generation tensor cores.
+//
+// Bound: the tensor cores, 4 D flop a row and token. Two streams of work share
+// a CTA: each has 128 rows of queries, a 128 x 128 score tile and an output in
+// tensor memory, and a group of four warps in which a thread is a row, so the
+// running reference and sum of its softmax are a thread's own. While one
+// stream's group turns scores into weights, the other's products run. A unit
+// of more than 128 rows gives each stream 128 of them, and both go through
+// every tile of 128 cached tokens; one of up to 128 rows gives both streams
+// the same rows, and they take the tiles in turn and are merged at its end.
+//
+//   S = Q K^T        Q and K tiles in shared memory, S in tensor memory
+//   P = exp2(S - r)  by the stream's group; P, 16-bit, replaces S in tensor memory
+//   O += P V         P from tensor memory, V from shared memory as it lies in the
+//                    cache (the product's N, the head dimension, contiguous)
+//
+// Warps: 0-3 bring keys and values to a ring of operand tiles (E5M2 as bytes,
+// then widened), 4-7 and 8-11 are the streams' groups, which also load their
+// unit's queries and write its output, 12 issues the products.
+#pragma once
+
+#include <algorithm>
+#include <atomic>
+
+#include "kv_tcgen05.cuh"
+
+namespace uzkv {
+
+constexpr int kManyThreads = 13 * 32;
+constexpr uint32_t kManyTile = 128;
+
+template <typename QT, bool FP8, int DP>
+struct ManyCfg {
+    using T = typename std::conditional<FP8, __half, QT>::type;
+    static constexpr uint32_t kQTile = 128 * DP * 2;                 // queries of a stream
+    static constexpr uint32_t kTileBytes = kManyTile * DP * 2;       // keys or values
+    static constexpr uint32_t kRawBytes = kManyTile * DP;            // their E5M2 bytes
+    static constexpr uint32_t kOther = 2560 + 256;                   // factors and statistics; barriers
+    static constexpr uint32_t kRoom = 227 * 1024 - kOther - 2 * kQTile;
+    static constexpr uint32_t kRaw = FP8 ? 4 : 0;
+    static constexpr uint32_t kFit = (kRoom - kRaw * kRawBytes) / kTileBytes;
+    static constexpr uint32_t kTiles = kFit > 8 ? 8 : kFit;
+    static constexpr uint32_t kSmem = kOther + 2 * kQTile + kTiles * kTileBytes + kRaw * kRawBytes;
+    static_assert(kTiles >= 3, "the keys of two tiles and a tile of values");
+};
+
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+__device__ __forceinline__ void tc_ld32(uint32_t* r, uint32_t addr) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,"
+        "%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
+        "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
+        "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
+        "r"(r[31])
+        : "memory");
+}
+
+// Descriptor of a tile whose contiguous dimension is the product's N: blocks of 64 elements `block` bytes apart,
+// groups of 8 rows 1024 bytes apart, 128-byte swizzle.
+__device__ __forceinline__ uint64_t rows_desc(uint32_t addr, uint32_t block) {
+    return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)(block >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
+           (uint64_t)2 << 61;
+}
+
+// One CTA's share of a unit: its tiles as jobs of the two streams. With up to 128 rows the streams take tiles in
+// turn, else both take each; either way jobs alternate between them.
+struct ManyPart {
+    Unit u;
+    uint32_t count, rows;  // tiles in this run; rows of the unit that exist
+    bool both;             // more than 128 rows
+    __device__ __forceinline__ ManyPart(const AttParams& p, const Unit& unit, uint64_t end) : u(unit) {
+        count = (uint32_t)min((uint64_t)(u.tiles - u.tile), end - u.pos);
+        rows = min(p.m, p.rows - u.mt * p.m);
+        both = rows > 128;
+    }
+    __device__ __forceinline__ uint32_t jobs() const { return both ? 2 * count : count; }
+    __device__ __forceinline__ uint32_t tile_of(uint32_t job) const { return both ? job / 2 : job; }
+    __device__ __forceinline__ uint32_t jobs_of(uint32_t stream) const { return both ? count : (count + 1 - stream) / 2; }
+    __device__ __forceinline__ Unit next(const AttParams& p) const {
+        Unit n = u;
+        n.tile += count - 1;
+        n.pos += count - 1;
+        advance(p, n, p.mtiles);
+        return n;
+    }
+};
+
+template <typename QT, bool FP8, int DP>
+__global__ void __launch_bounds__(kManyThreads, 1) attend_many_kernel(const __grid_constant__ AttParams p) {
+    using C = ManyCfg<QT, FP8, DP>;
+    using T = typename C::T;
+    extern __shared__ __align__(1024) char smem[];
+    char* const qs = smem;
+    char* const tiles = qs + 2 * C::kQTile;
+    char* const raws = tiles + C::kTiles * C::kTileBytes;
+    float* const factor = reinterpret_cast<float*>(raws + C::kRaw * C::kRawBytes);  // [256], or [128] of shared rows ...
+    float2* const stat = reinterpret_cast<float2*>(factor + 128);  // ... and then [2][128]: each stream's reference and sum
+    uint64_t* const bars = reinterpret_cast<uint64_t*>(factor + 640);
+    uint32_t* const dirty = reinterpret_cast<uint32_t*>(bars + 24);  // [8]: a unit's tiles had non-finite values taken out
+    uint32_t* const tmem_at = dirty + 8;
+    const uint32_t tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    const uint32_t D = p.cache.head_dim;
+    const uint32_t full = smem_u32(bars), freed = full + 8 * 8, s_full = full + 16 * 8, p_full = full + 18 * 8,
+                   q_full = full + 20 * 8, o_full = full + 21 * 8, stat_full = full + 22 * 8, unit_done = full + 23 * 8;
+
+    uzip::pdl_launch_dependents();
+    if (tid == 0) {
+        for (uint32_t i = 0; i < 8; i++) {
+            bar_init(full + 8 * i, 4);   // the four copying warps
+            bar_init(freed + 8 * i, 1);  // the products' commit
+            dirty[i] = 0;
+        }
+        for (uint32_t i = 0; i < 2; i++) {
+            bar_init(s_full + 8 * i, 1);
+            bar_init(p_full + 8 * i, 4);  // the four warps of the stream's group
+        }
+        bar_init(q_full, 8);
+        bar_init(o_full, 1);
+        bar_init(stat_full, 8);
+        bar_init(unit_done, 8);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 12) tc_alloc(smem_u32(tmem_at), 512);
+    if (D < DP) {  // columns past the head dimension stay zero: no copy writes them
+        for (uint32_t i = tid; i < C::kTiles * C::kTileBytes / 16; i += kManyThreads) reinterpret_cast<uint4*>(tiles)[i] = make_uint4(0, 0, 0, 0);
+        fence_async_smem();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_at;
+
+    const Split split = split_of(p);
+    const Run run = run_of(p, split, p.mtiles);
+    Unit unit{};
+    unit.pos = ~0ull;
+    if (run.begin != run.end) unit = unit_at(p, split, run.begin, p.mtiles);
+    bool ok = true;
+
+    if (warp < 4) {
+        // ---- copies: keys, then values of each tile; a warp takes 32 of its rows
+        constexpr uint32_t kES = FP8 ? 1 : 2, kLanes = DP * kES / 16;  // a row's chunks
+        constexpr uint32_t kRing = FP8 ? C::kRaw : C::kTiles;
+        const uint32_t c = lane % kLanes, live = D * kES / 16;
+        Unit ahead = unit;     // tile to copy next
+        uint32_t copied = 0;   // operand tiles copied: even ones are keys
+        Place at{-1, 0};
+        auto find = [&]() {
+            Place pl{-1, 0};
+            const uint32_t j = ahead.tile * kManyTile + warp * 32 + lane;
+            if (ahead.pos < run.end && j < ahead.span.old + ahead.span.fresh) pl = place_of(p.cache, ahead.b, j);
+            return pl;
+        };
+        at = find();
+        auto copy = [&]() {
+            if (ok && ahead.pos < run.end) {
+                if (!FP8 && copied >= kRing) ok = warp_wait(freed + 8 * (copied % kRing), (copied / kRing - 1) & 1);
+                __syncwarp();
+                const bool values = copied & 1;
+                const char* row = at.page < 0 ? nullptr : values ? v_row(p.cache, at, ahead.h) : k_row(p.cache, at, ahead.h);
+                char* slot = (FP8 ? raws : tiles) + (copied % kRing) * (FP8 ? C::kRawBytes : C::kTileBytes);
+#pragma unroll 8
+                for (uint32_t i = 0; i < kLanes; i++) {
+                    const uint32_t r = i * (32 / kLanes) + lane / kLanes;
+                    const char* src = reinterpret_cast<const char*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(row), r));
+                    const uint32_t R = warp * 32 + r;
+                    const uint32_t to = FP8 ? chunk_at<DP>(R, c) : swizzled(kManyTile, R, c);
+                    if (c < live) copy16(smem_u32(slot) + to, src ? src + c * 16 : p.cache.k, src != nullptr);
+                }
+                copied++;
+                if (values) {
+                    advance(p, ahead, p.mtiles);
+                    at = find();
+                }
+            }
+            copy_commit();
+        };
+        for (uint32_t i = 0; i < kRing - 1; i++) copy();
+        Unit cur = unit;
+        uint32_t sent = 0, index = 0;  // units so far
+        while (cur.pos < run.end && ok) {
+            const uint32_t j0 = cur.tile * kManyTile;
+            for (uint32_t values = 0; values < 2 && ok; values++, sent++) {
+                copy_wait<kRing - 2>();
+                char* const tile = tiles + (sent % C::kTiles) * C::kTileBytes;
+                if (FP8) {
+                    // Widen this warp's rows: 16 bytes to two chunks of eight FP16.
+                    if (sent >= C::kTiles) ok = warp_wait(freed + 8 * (sent % C::kTiles), (sent / C::kTiles - 1) & 1);
+                    if (!ok) break;
+                    __syncwarp();
+                    const char* raw = raws + (sent % kRing) * C::kRawBytes;
+                    if (c < live)
+#pragma unroll 4
+                        for (uint32_t x = 0; x < kLanes; x++) {
+                            const uint32_t R = warp * 32 + x * (32 / kLanes) + lane / kLanes;
+                            const uint4 v = *reinterpret_cast<const uint4*>(raw + chunk_at<DP>(R, c));
+                            *reinterpret_cast<uint4*>(tile + swizzled(kManyTile, R, 2 * c)) =
+                                make_uint4(uzip::prmt(v.x, 0, 0x1404), uzip::prmt(v.x, 0, 0x3424), uzip::prmt(v.y, 0, 0x1404), uzip::prmt(v.y, 0, 0x3424));
+                            *reinterpret_cast<uint4*>(tile + swizzled(kManyTile, R, 2 * c + 1)) =
+                                make_uint4(uzip::prmt(v.z, 0, 0x1404), uzip::prmt(v.z, 0, 0x3424), uzip::prmt(v.w, 0, 0x1404), uzip::prmt(v.w, 0, 0x3424));
+                        }
+                }
+                if (values && j0 + kManyTile > cur.span.old) {
+                    // A value that a row does not see must not reach it through 0 * NaN: non-finite values of a tile
+                    // with new tokens leave it here, and the unit's end adds them to the rows that see them. Each
+                    // thread looks at the chunks it wrote.
+                    bool bad = false;
+                    if (c < live)
+                        for (uint32_t x = 0; x < kLanes; x++) {
+                            const uint32_t R = warp * 32 + x * (32 / kLanes) + lane / kLanes;
+                            for (uint32_t half = 0; half < (FP8 ? 2 : 1); half++) {
+                                uint32_t* w = reinterpret_cast<uint32_t*>(tile + swizzled(kManyTile, R, FP8 ? 2 * c + half : c));
+                                for (int y = 0; y < 4; y++) {
+                                    uint32_t v = w[y];
+                                    if (clean2<T>(v)) {
+                                        w[y] = v;
+                                        bad = true;
+                                    }
+                                }
+                            }
+                        }
+                    if (bad) *reinterpret_cast<volatile uint32_t*>(dirty + index % 8) = 1;
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) bar_arrive(full + 8 * (sent % C::kTiles));
+                copy();
+            }
+            const bool to_end = cur.tile + 1 == cur.tiles;
+            advance(p, cur, p.mtiles);
+            if (to_end) index++;
+        }
+        copy_wait<0>();
+    } else if (warp == 12) {
+        // ---- products, by one lane
+        if (lane == 0) {
+            const uint32_t n = (D + 15) / 16 * 16;  // columns of the output
+            const uint32_t iqk = mma_desc<T>(128, kManyTile), ipv = mma_desc<T>(128, n) | 1u << 16;  // V: N contiguous
+            uint32_t base = 0, index = 0, weights[2] = {0, 0};  // operand tiles of earlier units; units; jobs of each stream
+            while (unit.pos < run.end && ok) {
+                const ManyPart part(p, unit, run.end);
+                const uint32_t jobs = part.jobs();
+                auto score = [&](uint32_t j) {
+                    const uint32_t t = base + 2 * part.tile_of(j), s = t % C::kTiles, x = j & 1;
+                    if (!part.both || !x) ok = bar_wait(full + 8 * s, (t / C::kTiles) & 1);
+                    if (!ok) return;
+                    tc_fence_after();
+                    const uint32_t q = smem_u32(qs) + (part.both ? x * C::kQTile : 0), k = smem_u32(tiles) + s * C::kTileBytes;
+                    for (uint32_t i = 0; i < n / 16; i++)
+                        tc_mma(tmem + x * 256, tile_desc(q + (i >> 2) * 128 * 128 + (i & 3) * 32),
+                               tile_desc(k + (i >> 2) * kManyTile * 128 + (i & 3) * 32), iqk, i != 0);
+                    tc_commit(s_full + 8 * x);
+                    if (!part.both || x) tc_commit(freed + 8 * s);
+                };
+                ok = bar_wait(q_full, index & 1);
+                if (ok) score(0);
+                if (ok && jobs > 1) score(1);
+                for (uint32_t j = 0; j < jobs && ok; j++) {
+                    const uint32_t t = base + 2 * part.tile_of(j) + 1, s = t % C::kTiles, x = j & 1;
+                    ok = bar_wait(full + 8 * s, (t / C::kTiles) & 1);
+                    const uint32_t done = x ? weights[1]++ : weights[0]++;
+                    if (ok) ok = bar_wait(p_full + 8 * x, done & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t v = smem_u32(tiles) + s * C::kTileBytes;
+                    for (uint32_t i = 0; i < kManyTile / 16; i++)
+                        tc_mma_ts(tmem + x * 256 + 128, tmem + x * 256 + i * 8, rows_desc(v + i * 2048, kManyTile * 128), ipv,
+                                  j > 1 || i != 0);
+                    if (!part.both || x) tc_commit(freed + 8 * s);
+                    if (j + 2 < jobs) score(j + 2);
+                }
+                if (ok) tc_commit(o_full);
+                base += 2 * part.count;
+                index++;
+                unit = part.next(p);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ---- a stream's softmax, queries and output: thread `row` of 128
+        const uint32_t x = warp < 8 ? 0 : 1, row = (warp % 4) * 32 + lane;
+        const uint32_t lanes = warp % 4 * 32 << 16, st = tmem + x * 256 + lanes, ot = st + 128;
+        uint32_t index = 0, scored = 0;
+        while (unit.pos < run.end && ok) {
+            const ManyPart part(p, unit, run.end);
+            const Unit& u = part.u;
+            const uint32_t row0 = u.mt * p.m;
+            if (part.both)
+                load_queries<QT, T, DP, 128, 1>(
+                    p, tid % 128, u.b, u.h, row0 + x * 128, 128,
+                    [&](uint32_t r, uint32_t ch) { return reinterpret_cast<uint4*>(qs + x * C::kQTile + swizzled(128, r, ch)); },
+                    factor + x * 128);
+            else  // half of the shared rows each
+                load_queries<QT, T, DP, 128, 1>(
+                    p, tid % 128, u.b, u.h, row0 + x * 64, 64,
+                    [&](uint32_t r, uint32_t ch) { return reinterpret_cast<uint4*>(qs + swizzled(128, x * 64 + r, ch)); },
+                    factor + x * 64);
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) bar_arrive(q_full);
+            ok = warp_wait(q_full, index & 1);  // factors of the other warps too
+            if (!ok) break;
+            const uint32_t mine = part.both ? x * 128 + row : row;  // row of the unit
+            const float f = factor[mine];
+            float ref = -INFINITY, sum = 0.0f;
+            const uint32_t jobs = part.jobs_of(x);
+            for (uint32_t j = 0; j < jobs; j++) {
+                const uint32_t j0 = (u.tile + (part.both ? j : 2 * j + x)) * kManyTile;
+                ok = warp_wait(s_full + 8 * x, scored++ & 1);
+                if (!ok) break;
+                tc_fence_after();
+                const bool masked = j0 + kManyTile > u.span.old;
+                uint64_t seen[2] = {~0ull, ~0ull};
+                if (masked) {
+                    seen[0] = seen_bits(p, u.b, u.span, row0 + mine, j0);
+                    seen[1] = seen_bits(p, u.b, u.span, row0 + mine, j0 + 64);
+                }
+                uint32_t w[64];
+                float most, add;
+                auto weigh = [&](float r) {  // weights against reference r, their sum, and the largest exponent
+                    most = -INFINITY;
+                    float part_sum[4] = {0.0f, 0.0f, 0.0f, 0.0f}, part_top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                    for (int c = 0; c < 4; c++) {
+                        uint32_t v[32];
+                        tc_ld32(v, st + 32 * c);
+                        tc_wait_ld();
+                        const uint32_t bits = (uint32_t)(seen[c / 2] >> (32 * (c & 1)));
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            float a = __uint_as_float(v[i]) * f - r, b = __uint_as_float(v[i + 1]) * f - r;
+                            if (masked) {
+                                if (!(bits >> i & 1)) a = -INFINITY;
+                                if (!(bits >> i & 2)) b = -INFINITY;
+                            }
+                            part_top[0] = fmaxf(part_top[0], a);
+                            part_top[1] = fmaxf(part_top[1], b);
+                            a = exp2_fast(a);
+                            b = exp2_fast(b);
+                            part_sum[i & 2] += a;
+                            part_sum[(i & 2) + 1] += b;
+                            w[16 * c + i / 2] = pack2<T>(a, b);
+                        }
+                    }
+                    most = fmaxf(part_top[0], part_top[1]);
+                    add = (part_sum[0] + part_sum[1]) + (part_sum[2] + part_sum[3]);
+                };
+                const float r = ref == -INFINITY ? 0.0f : ref - kLift<T>;
+                weigh(r);
+                const bool rise = ref == -INFINITY ? most > -INFINITY : most > kSlack + kLift<T>;
+                if (__any_sync(0xFFFFFFFFu, rise)) {
+                    const float now = fmaxf(ref, most + r);
+                    const float fade = ref == -INFINITY ? 0.0f : exp2_fast(ref - now);  // 0: nothing so far
+                    ref = now;
+                    sum *= fade;
+                    if (j > 0)  // the stream's products are complete up to its last tile
+                        for (uint32_t c = 0; c < D; c += 32) {
+                            uint32_t v[32];
+                            tc_ld32(v, ot + c);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; i++) v[i] = __float_as_uint(__uint_as_float(v[i]) * fade);
+                            tc_st32(ot + c, v);
+                        }
+                    weigh(ref == -INFINITY ? 0.0f : ref - kLift<T>);
+                }
+                sum += add;
+                tc_st32(st, w);
+                tc_st32(st + 32, w + 32);
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(p_full + 8 * x);
+            }
+            if (!ok) break;
+            // ---- output
+            ok = warp_wait(o_full, index & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const bool odd = *reinterpret_cast<volatile uint32_t*>(dirty + index % 8) != 0;
+            float mref = ref == -INFINITY ? 0.0f : ref - kLift<T>;
+            // Streams that took the tiles of the same rows in turn: each merges half of the columns.
+            float2 other = make_float2(0.0f, 0.0f);
+            if (!part.both) stat[x * 128 + row] = make_float2(mref, sum);
+            __syncwarp();
+            if (lane == 0) bar_arrive(stat_full);
+            ok = warp_wait(stat_full, index & 1);
+            if (!ok) break;
+            float keep = 1.0f, give = 0.0f;
+            if (!part.both) {
+                other = stat[(1 - x) * 128 + row];
+                const float top = sum == 0.0f ? other.x : other.y == 0.0f ? mref : fmaxf(mref, other.x);
+                keep = sum == 0.0f ? 0.0f : exp2_fast(mref - top);
+                give = other.y == 0.0f ? 0.0f : exp2_fast(other.x - top);
+                sum = (sum == 0.0f ? 0.0f : sum * keep) + (other.y == 0.0f ? 0.0f : other.y * give);
+                mref = top;
+            }
+            const uint32_t grow = row0 + mine, tok = grow / p.group, hq = u.h * p.group + (grow - tok * p.group);
+            const bool exists = grow < p.rows, none = !exists || tok >= u.span.fresh || sum == 0.0f;
+            const bool from_start = u.tile == 0, to_end = u.tile + part.count == u.tiles;
+            const float inv = none ? 0.0f : 1.0f / sum;
+            float* const dst = p.partial + ((uint64_t)blockIdx.x * 2 + (from_start ? 1 : 0)) * partial_floats(p);
+            char* const out = p.out.p + u.b * p.out.b + tok * p.out.t + (uint64_t)hq * p.out.h;
+            const uint32_t ot0 = tmem + 128 + lanes;
+            for (uint32_t c = 0; c < D; c += 32) {
+                if (!part.both && (c / 32 & 1) != x) continue;
+                uint32_t v[32];
+                __syncwarp();
+                if (part.both) {
+                    tc_ld32(v, ot + c);
+                    tc_wait_ld();
+                } else {
+                    uint32_t o2[32];
+                    tc_ld32(v, (x ? ot0 + 256 : ot0) + c);
+                    tc_ld32(o2, (x ? ot0 : ot0 + 256) + c);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; i++) {  // a stream without weight may have no output at all
+                        const float a = keep == 0.0f ? 0.0f : __uint_as_float(v[i]) * keep;
+                        const float b = give == 0.0f ? 0.0f : __uint_as_float(o2[i]) * give;
+                        v[i] = __float_as_uint(a + b);
+                    }
+                }
+                if (odd && exists) {
+                    const uint32_t upto = min((u.tile + part.count) * kManyTile, u.span.old + u.span.fresh);
+                    const uint32_t from = max(u.tile * kManyTile, u.span.old / kManyTile * kManyTile);
+                    for (uint32_t j = from; j < upto; j++) {
+                        if (!(seen_bits(p, u.b, u.span, grow, j) & 1)) continue;
+                        const Place pl = place_of(p.cache, u.b, j);
+                        if (pl.page < 0) continue;
+                        const char* vr = v_row(p.cache, pl, u.h);
+#pragma unroll
+                        for (int i = 0; i < 32; i++) {
+                            if (c + i >= D) continue;
+                            const float e = FP8 ? to_f32(reinterpret_cast<const E5M2*>(vr)[c + i]) : to_f32(reinterpret_cast<const T*>(vr)[c + i]);
+                            if (!isfinite(e)) v[i] = __float_as_uint(__uint_as_float(v[i]) + e);
+                        }
+                    }
+                }
+                if (!exists) {
+                } else if (from_start && to_end) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) {
+                        if (c + i >= D) continue;
+                        uint4 y = make_uint4(0, 0, 0, 0);
+                        if (!none) {
+                            uint32_t* z = reinterpret_cast<uint32_t*>(&y);
+#pragma unroll
+                            for (int k = 0; k < 4; k++)
+                                z[k] = pack2<QT>(__uint_as_float(v[i + 2 * k]) * inv, __uint_as_float(v[i + 2 * k + 1]) * inv);
+                        }
+                        *reinterpret_cast<uint4*>(out + 2 * (c + i)) = y;
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+                        if (c + i < D)
+                            *reinterpret_cast<uint4*>(dst + (uint64_t)mine * DP + c + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                }
+            }
+            if (exists && (part.both || x == 0)) {
+                if (from_start && to_end) {
+                    if (p.lse) p.lse[((uint64_t)u.b * p.tokens + tok) * p.q_heads + hq] = none ? -INFINITY : (mref + log2f(sum)) * kLn2;
+                } else {
+                    *reinterpret_cast<float2*>(dst + (uint64_t)p.m * DP + 2 * mine) = make_float2(mref, none ? 0.0f : sum);
+                }
+            }
+            // All reads of the unit's accumulators, statistics and flag are over before the next unit's queries are announced.
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(unit_done);
+            ok = warp_wait(unit_done, index & 1);
+            if (!ok) break;
+            if (odd && x == 0 && row == 0) *reinterpret_cast<volatile uint32_t*>(dirty + index % 8) = 0;
+            index++;
+            unit = part.next(p);
+        }
+    }
+    if (!ok && p.cache.status) *p.cache.status = UZIP_ERR_TIMEOUT;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 12) tc_free(tmem, 512);
+}
+
+template <typename QT, bool FP8, int DP>
+int launch_many_as(AttParams& p, int sms, cudaStream_t stream) {
+    using C = ManyCfg<QT, FP8, DP>;
+    static std::atomic<uint64_t> ready{0};  // a bit for each device whose limit is raised
+    int dev = 0;
+    UZIP_CUDA_TRY(cudaGetDevice(&dev));
+    if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+        UZIP_CUDA_TRY(cudaFuncSetAttribute(attend_many_kernel<QT, FP8, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem));
+        if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
+    p.m = p.rows <= 128 ? 128 : 256;
+    p.mtiles = (p.rows + p.m - 1) / p.m;
+    p.dp = DP;
+    p.shift = 7;
+    static_assert(kManyTile == 1u << 7, "tile");
+    p.unit_cost = 5;
+    p.grid = std::min<uint32_t>((uint32_t)sms, kMaxAttGrid);
+    attend_many_kernel<QT, FP8, DP><<<p.grid, kManyThreads, C::kSmem, stream>>>(p);
+    UZIP_CUDA_TRY(cudaGetLastError());
+    return UZIP_OK;
+}
+
+template <typename QT, bool FP8>
+int launch_many(AttParams& p, int sms, cudaStream_t s) {
+    return p.cache.head_dim <= 64 ? launch_many_as<QT, FP8, 64>(p, sms, s) : launch_many_as<QT, FP8, 128>(p, sms, s);
+}
+
+}  // namespace uzkv

@@ -41,6 +41,7 @@ struct AttParams {
     uint32_t dp;       // floats a row of a partial result takes
     uint32_t grid;     // CTAs the tiles are split over
     uint32_t shift;    // log2 of the cached tokens of a tile
+    uint32_t unit_cost;  // tiles that a unit weighs beyond its own
     float* partial;    // [grid][2] results: m rows of dp floats, then m (reference, sum) pairs
     const float* mass_in;
     float* mass_out;
@@ -54,14 +55,17 @@ __device__ __forceinline__ uint64_t partial_floats(const AttParams& p) { return 
 // ------------------------------------------------------------------- split
 //
 // The tiles of all (sequence, KV head, row tile) units in this order, cut into
-// equal runs, one a CTA: sequences of any lengths load all SMs alike. A unit
-// that several CTAs share leaves partial results: a CTA's first unit in its
-// slot 0 where the unit began before it, its last unit in slot 1 where the
-// unit goes on after it.
+// equal runs, one a CTA: sequences of any lengths load all SMs alike. Each unit
+// has `unit_cost` positions before its tiles, which stand for the time of its
+// queries' load and its output, so that many short units weigh as much as they
+// take. A unit that several CTAs share leaves partial results: a CTA's first
+// unit in its slot 0 where the unit began before it, its last unit in slot 1
+// where the unit goes on after it.
 
 struct Unit {
     uint32_t b, h, mt, tile, tiles;
     Span span;
+    uint64_t pos;  // position of the tile
 };
 
 __device__ __forceinline__ uint32_t tiles_of(const AttParams& p, const Span& s) {
@@ -72,7 +76,10 @@ __device__ __forceinline__ uint32_t tiles_of(const AttParams& p, uint32_t b) {
     return b < p.cache.sequences ? tiles_of(p, span_of(p.cache, p.counts, p.tokens, b)) : 0;
 }
 
-// What a warp knows of the split: the tiles of all sequences (one head and row tile each), and of sequence `lane`.
+// Positions that a unit of so many tiles takes.
+__device__ __forceinline__ uint32_t width_of(const AttParams& p, uint32_t tiles) { return tiles ? tiles + p.unit_cost : 0; }
+
+// What a warp knows of the split: the positions of all sequences (one head and row tile each), and of sequence `lane`.
 struct Split {
     uint64_t all;
     uint32_t mine;
@@ -82,21 +89,21 @@ struct Split {
 __device__ __forceinline__ Split split_of(const AttParams& p) {
     const uint32_t lane = threadIdx.x % 32;
     Split s;
-    s.mine = tiles_of(p, lane);
+    s.mine = width_of(p, tiles_of(p, lane));
     s.all = s.mine;
-    for (uint32_t b = lane + 32; b < p.cache.sequences; b += 32) s.all += tiles_of(p, b);
+    for (uint32_t b = lane + 32; b < p.cache.sequences; b += 32) s.all += width_of(p, tiles_of(p, b));
     for (int o = 16; o; o >>= 1) s.all += __shfl_xor_sync(0xFFFFFFFFu, s.all, o);
     return s;
 }
 
-// All lanes of a warp: the unit and tile at position `at` of the order, at < all tiles * kv_heads * mtiles.
+// All lanes of a warp: the first unit and tile at or after position `at` of the order, at < all * kv_heads * mtiles.
 __device__ __forceinline__ Unit unit_at(const AttParams& p, const Split& s, uint64_t at, uint32_t mtiles) {
     const uint32_t lane = threadIdx.x % 32;
     const uint64_t per = (uint64_t)p.cache.kv_heads * mtiles;
     uint64_t before = 0;
     Unit u{};
     for (uint32_t b0 = 0; b0 < p.cache.sequences; b0 += 32) {
-        const uint64_t mine = b0 ? tiles_of(p, b0 + lane) : s.mine;
+        const uint64_t mine = b0 ? width_of(p, tiles_of(p, b0 + lane)) : s.mine;
         uint64_t upto = mine;
         for (int o = 1; o < 32; o <<= 1) {
             const uint64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
@@ -106,11 +113,13 @@ __device__ __forceinline__ Unit unit_at(const AttParams& p, const Split& s, uint
         if (past) {
             const int l = __ffs(past) - 1;
             const uint64_t start = __shfl_sync(0xFFFFFFFFu, before + upto - mine, l) * per;
+            const uint32_t width = (uint32_t)__shfl_sync(0xFFFFFFFFu, mine, l);
             u.b = b0 + l;
-            u.tiles = (uint32_t)__shfl_sync(0xFFFFFFFFu, mine, l);
+            u.tiles = width - p.unit_cost;
             const uint32_t in = (uint32_t)(at - start);  // within one sequence
-            const uint32_t unit = in / u.tiles;
-            u.tile = in - unit * u.tiles;
+            const uint32_t unit = in / width, off = in - unit * width;
+            u.tile = off > p.unit_cost ? off - p.unit_cost : 0;
+            u.pos = at + (off < p.unit_cost ? p.unit_cost - off : 0);
             u.h = unit / mtiles;
             u.mt = unit - u.h * mtiles;
             u.span = span_of(p.cache, p.counts, p.tokens, u.b);
@@ -118,21 +127,38 @@ __device__ __forceinline__ Unit unit_at(const AttParams& p, const Split& s, uint
         }
         before += __shfl_sync(0xFFFFFFFFu, upto, 31);
     }
+    u.pos = ~0ull;
     return u;
 }
 
+// On to the next tile.
 __device__ __forceinline__ void advance(const AttParams& p, Unit& u, uint32_t mtiles) {
+    u.pos++;
     if (++u.tile < u.tiles) return;
     u.tile = 0;
+    u.pos += p.unit_cost;
     if (++u.mt < mtiles) return;
     u.mt = 0;
     if (++u.h < p.cache.kv_heads) return;
     u.h = 0;
     do {
-        if (++u.b >= p.cache.sequences) return;
+        if (++u.b >= p.cache.sequences) {
+            u.pos = ~0ull;
+            return;
+        }
         u.span = span_of(p.cache, p.counts, p.tokens, u.b);
         u.tiles = tiles_of(p, u.span);
     } while (!u.tiles);
+}
+
+// A CTA's run of positions.
+struct Run {
+    uint64_t begin, end;
+};
+__device__ __forceinline__ Run run_of(const AttParams& p, const Split& s, uint32_t mtiles) {
+    const uint64_t total = s.all * p.cache.kv_heads * mtiles, shares = min(total, (uint64_t)p.grid);  // no share is empty
+    if (blockIdx.x >= shares) return Run{0, 0};
+    return Run{total * blockIdx.x / shares, total * (blockIdx.x + 1) / shares};
 }
 
 // ------------------------------------------------------------------- masks
@@ -251,6 +277,17 @@ __device__ __forceinline__ void bar_arrive_copies(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
+// NaN and infinities of a pair of values (FP16 or BF16 patterns) become zero; whether there were any.
+template <typename T>
+__device__ __forceinline__ uint32_t clean2(uint32_t& v) {
+    constexpr uint32_t kExp = std::is_same<T, __half>::value ? 0x7C00u : 0x7F80u;
+    uint32_t bad = 0;
+    if ((v & kExp) == kExp) bad |= 0xFFFFu;
+    if ((v >> 16 & kExp) == kExp) bad |= 0xFFFF0000u;
+    v &= ~bad;
+    return bad;
+}
+
 // Byte offset of 16-byte chunk c of a row in a shared-memory tile of RB-byte rows.
 template <int RB>
 __device__ __forceinline__ uint32_t chunk_at(uint32_t row, uint32_t c) {
@@ -269,17 +306,17 @@ template <>
 constexpr float kLift<__half> = 6.0f;
 
 // Queries of rows row0 .. row0 + rows - 1 to shared memory as T (columns past head_dim and rows past p.rows
-// zero), by THREADS threads from thread 0 on; at(row, c) is where 16-byte chunk c of a row goes. factor[r *
+// zero), by THREADS threads numbered tid; at(row, c) is where 16-byte chunk c of a row goes. factor[r *
 // STRIDE], where wanted, is what a score of row r is to be multiplied by to have it in units of log2: scale *
 // log2(e), and for BF16 queries that go to an FP16 product the power of two that was taken out of the row to
 // bring its largest element to [1, 2).
 template <typename QT, typename T, int DP, int THREADS, int STRIDE, typename At>
-__device__ __forceinline__ void load_queries(const AttParams& p, uint32_t b, uint32_t h, uint32_t row0, uint32_t rows,
-                                             At at, float* factor) {
+__device__ __forceinline__ void load_queries(const AttParams& p, uint32_t tid, uint32_t b, uint32_t h, uint32_t row0,
+                                             uint32_t rows, At at, float* factor) {
     constexpr bool kCast = !std::is_same<QT, T>::value;
     constexpr uint32_t kChunks = DP / 8;  // a power of two, at most 32
-    const uint32_t c = threadIdx.x % kChunks, live = p.cache.head_dim / 8;
-    for (uint32_t i = threadIdx.x / kChunks; i < rows; i += THREADS / kChunks) {
+    const uint32_t c = tid % kChunks, live = p.cache.head_dim / 8;
+    for (uint32_t i = tid / kChunks; i < rows; i += THREADS / kChunks) {
         const uint32_t row = row0 + i;
         uint4 x = make_uint4(0, 0, 0, 0);
         if (row < p.rows && c < live) {
@@ -316,6 +353,10 @@ int attend_bf16(AttParams& p, int sms, cudaStream_t s);
 int attend_bf16_e5m2(AttParams& p, int sms, cudaStream_t s);
 int attend_fp16(AttParams& p, int sms, cudaStream_t s);
 int attend_fp16_e5m2(AttParams& p, int sms, cudaStream_t s);
+int attend_many_bf16(AttParams& p, int sms, cudaStream_t s);  // more rows, heads up to 128
+int attend_many_bf16_e5m2(AttParams& p, int sms, cudaStream_t s);
+int attend_many_fp16(AttParams& p, int sms, cudaStream_t s);
+int attend_many_fp16_e5m2(AttParams& p, int sms, cudaStream_t s);
 int mass_bf16(AttParams& p, int sms, cudaStream_t s);
 int mass_bf16_e5m2(AttParams& p, int sms, cudaStream_t s);
 int mass_fp16(AttParams& p, int sms, cudaStream_t s);

@@ -35,12 +35,12 @@ struct MassCfg {
     static constexpr uint32_t kQBytes = kMaxN * DP * 2;               // one chunk's queries, or two smaller ones'
     static constexpr uint32_t kTileBytes = kMassTile * DP * 2;
     static constexpr uint32_t kRawBytes = kMassTile * DP;             // E5M2 bytes of a tile
-    static constexpr uint32_t kRoom = 227 * 1024 - 1024 - 8192;       // less alignment, factors and barriers
+    static constexpr uint32_t kRoom = 227 * 1024 - 8192;              // less factors and barriers
     // 16-bit keys: as many operand tiles as fit. E5M2: few operand tiles, the rest of the space for bytes on their way.
     static constexpr uint32_t kFit = (kRoom - kQBytes) / kTileBytes;
     static constexpr uint32_t kTiles = FP8 ? (DP <= 128 ? 2 : 1) : (kFit > 8 ? 8 : kFit);
     static constexpr uint32_t kRaw = FP8 ? (DP <= 128 ? 4 : 2) : 0;
-    static constexpr uint32_t kSmem = 1024 + kQBytes + kTiles * kTileBytes + kRaw * kRawBytes + 8192;
+    static constexpr uint32_t kSmem = kQBytes + kTiles * kTileBytes + kRaw * kRawBytes + 8192;
     static_assert(kSmem <= 227 * 1024, "shared memory");
     static_assert(kTiles >= 1, "operand tiles");
 };
@@ -48,21 +48,19 @@ struct MassCfg {
 // The runs of tiles of one unit and chunk that a CTA passes over; all roles walk the same list.
 struct MassWalk {
     Unit u;
-    uint64_t left;
+    uint64_t end;
     uint32_t chunk, count, units;
-    __device__ __forceinline__ MassWalk(const Unit& first, uint64_t n) : u(first), left(n), chunk(0), count(0), units(0) {
-        if (left) count = (uint32_t)min((uint64_t)(u.tiles - u.tile), left);
-    }
-    __device__ __forceinline__ bool valid() const { return left != 0; }
+    __device__ __forceinline__ MassWalk(const Unit& first, uint64_t e) : u(first), end(e), chunk(0), units(0) { take(); }
+    __device__ __forceinline__ void take() { count = valid() ? (uint32_t)min((uint64_t)(u.tiles - u.tile), end - u.pos) : 0; }
+    __device__ __forceinline__ bool valid() const { return u.pos < end; }
     __device__ __forceinline__ void next(const AttParams& p) {
         if (++chunk < p.mtiles) return;
         chunk = 0;
-        left -= count;
-        if (!left) return;
         u.tile += count - 1;
+        u.pos += count - 1;
         advance(p, u, 1);
         units++;
-        count = (uint32_t)min((uint64_t)(u.tiles - u.tile), left);
+        take();
     }
     // Which of the two accumulators and summing groups takes tile i: turns over tiles and units, the same in every
     // chunk, so that the thread that adds a later chunk to a token's mass is the one that stored it.
@@ -73,8 +71,7 @@ template <typename QT, bool FP8, int DP>
 __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const __grid_constant__ AttParams p) {
     using C = MassCfg<QT, FP8, DP>;
     using T = typename C::T;
-    extern __shared__ char smem_raw[];
-    char* const smem = smem_raw + (1024 - smem_u32(smem_raw) % 1024) % 1024;
+    extern __shared__ __align__(1024) char smem[];
     char* const qs = smem;
     char* const tiles = qs + C::kQBytes;
     char* const raws = tiles + C::kTiles * C::kTileBytes;
@@ -113,11 +110,10 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const __grid_cons
     const uint32_t tmem = *tmem_at;
 
     const Split split = split_of(p);
-    const uint64_t total = split.all * p.cache.kv_heads;
-    const uint64_t shares = min(total, (uint64_t)p.grid);
-    const uint64_t begin = blockIdx.x < shares ? total * blockIdx.x / shares : 0;
-    const uint64_t n = blockIdx.x < shares ? total * (blockIdx.x + 1) / shares - begin : 0;
-    const Unit first = n ? unit_at(p, split, begin, 1) : Unit{};
+    const Run run = run_of(p, split, 1);
+    Unit first{};
+    first.pos = ~0ull;
+    if (run.begin != run.end) first = unit_at(p, split, run.begin, 1);
     bool ok = true;
 
     if (warp < 4) {
@@ -125,7 +121,7 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const __grid_cons
         constexpr uint32_t kES = FP8 ? 1 : 2, kLanes = DP * kES / 16;  // a row's chunks
         constexpr uint32_t kRing = FP8 ? C::kRaw : C::kTiles;
         const uint32_t c = lane % kLanes, live = D * kES / 16;
-        MassWalk cw(first, n);        // of the next tile to copy
+        MassWalk cw(first, run.end);        // of the next tile to copy
         uint32_t cs = 0, copied = 0;  // its place in the run, and how many are copied
         auto copy = [&]() {
             if (ok && cw.valid()) {
@@ -157,7 +153,7 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const __grid_cons
         };
         uint32_t seg = 0, sent = 0;
         for (uint32_t i = 0; i < kRing - 1; i++) copy();
-        for (MassWalk w(first, n); w.valid() && ok; w.next(p), seg++) {
+        for (MassWalk w(first, run.end); w.valid() && ok; w.next(p), seg++) {
             // The rows' queries, factors and exponents.
             const uint32_t qb = seg % qbuf, fb = seg % 2;
             if (seg >= qbuf) ok = warp_wait(q_freed + 8 * qb, (seg / qbuf - 1) & 1);
@@ -166,7 +162,7 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const __grid_cons
             char* q = qs + qb * N * DP * 2;
             float2* f = rowf + fb * 256;
             load_queries<QT, T, DP, 128, 2>(
-                p, w.u.b, w.u.h, row0, N, [&](uint32_t r, uint32_t ch) { return reinterpret_cast<uint4*>(q + swizzled(N, r, ch)); },
+                p, tid, w.u.b, w.u.h, row0, N, [&](uint32_t r, uint32_t ch) { return reinterpret_cast<uint4*>(q + swizzled(N, r, ch)); },
                 &f[0].x);
             for (uint32_t r = tid; r < N; r += 128) {
                 const uint32_t row = row0 + r, t = row / p.group;
@@ -212,7 +208,7 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const __grid_cons
         if (lane == 0) {
             const uint32_t idesc = mma_desc<T>(kMassTile, N), steps = (D + 15) / 16;
             uint32_t seg = 0, k = 0, uses[2] = {0, 0};
-            for (MassWalk w(first, n); w.valid() && ok; w.next(p), seg++) {
+            for (MassWalk w(first, run.end); w.valid() && ok; w.next(p), seg++) {
                 ok = bar_wait(q_full + 8 * (seg % 2), (seg / 2) & 1);
                 const uint32_t q = smem_u32(qs) + seg % qbuf * N * DP * 2;
                 for (uint32_t i = 0; i < w.count && ok; i++, k++) {
@@ -236,7 +232,7 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const __grid_cons
         // ---- sums: a thread is a cached token
         const uint32_t group = warp < 8 ? 0 : 1, quarter = warp % 4;
         uint32_t seg = 0, used = 0;
-        for (MassWalk w(first, n); w.valid() && ok; w.next(p), seg++) {
+        for (MassWalk w(first, run.end); w.valid() && ok; w.next(p), seg++) {
             const Span sp = w.u.span;
             const float2* f = rowf + seg % 2 * 256;
             const int64_t row_at = w.u.b * p.mass_b + w.u.h * p.mass_h;
@@ -330,6 +326,7 @@ int launch_mass_as(AttParams& p, int sms, cudaStream_t stream) {
     p.mtiles = chunks;
     p.m = ((p.rows + chunks - 1) / chunks + 15) / 16 * 16;
     p.shift = 7;
+    p.unit_cost = 3;
     static_assert(kMassTile == 1u << 7, "tile");
     p.grid = (uint32_t)sms;
     mass_kernel<QT, FP8, DP><<<p.grid, kMassThreads, C::kSmem, stream>>>(p);
