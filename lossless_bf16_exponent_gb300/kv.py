@@ -45,12 +45,12 @@ def _dense(t: torch.Tensor, what: str, dtype, shape, device) -> torch.Tensor:
     return t
 
 
-def _rows(x: torch.Tensor, what: str) -> "_lib.KvRows":
-    """A [sequences, tokens, heads, dim] tensor as the C ABI takes it."""
-    sb, st, sh, sd = x.stride()
-    if sd != 1 and x.shape[3] != 1:
+def _rows(x: torch.Tensor, what: str) -> _lib.KvRows:
+    """A [sequences, tokens, heads, dim] or [tokens, heads, dim] tensor as the C ABI takes it."""
+    *outer, st, sh, sd = x.stride()
+    if sd != 1 and x.shape[-1] != 1:
         raise ValueError(f"{what}: elements of a row must be contiguous")
-    return _lib.KvRows(x.data_ptr(), sb, st, sh)
+    return _lib.KvRows(x.data_ptr(), outer[0] if outer else 0, st, sh)
 
 
 def _writable(x: torch.Tensor, what: str) -> torch.Tensor:
@@ -73,6 +73,15 @@ class RotaryPlan:
     rotary_dim: int
     layout: str
     magnitude: float
+
+    def __post_init__(self):
+        if self.layout not in _LAYOUTS:
+            raise ValueError(f"layout {self.layout!r}: expected 'half' or 'interleaved'")
+        if self.turns.dtype != torch.int64 or self.turns.shape != (self.rotary_dim // 2,) or not self.turns.is_contiguous():
+            raise ValueError("turns: expected a contiguous int64 tensor of rotary_dim / 2")
+        # What each call passes on, looked up once.
+        object.__setattr__(self, "index", self.turns.get_device())
+        object.__setattr__(self, "args", (self.turns.data_ptr(), self.rotary_dim, _LAYOUTS[self.layout], self.magnitude))
 
 
 def rotary_rates(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -117,34 +126,41 @@ def rotary_plan(rotary_dim: int, base: float = 10000.0, layout: str = "half", sc
     """The plan of :func:`rotary` and :func:`rotary_append`; see :func:`rotary_rates`
     for the scalings. ``layout``: "half" turns elements i and i + rotary_dim / 2
     together, "interleaved" 2 i and 2 i + 1."""
-    if layout not in _LAYOUTS:
-        raise ValueError(f"layout {layout!r}: expected 'half' or 'interleaved'")
     rates, magnitude = rotary_rates(rotary_dim, base, scaling, factor, original_length, low, high)
     turns = [int(round(f / (2 * math.pi) * 2.0 ** 64)) for f in rates]
     turns = torch.tensor([v - (1 << 64) if v >= 1 << 63 else v for v in turns], dtype=torch.int64, device=device)
     return RotaryPlan(turns, rotary_dim, layout, magnitude)
 
 
+def _positions(positions, shape, index) -> int:
+    """Check int32 positions of tokens; the stride between their rows."""
+    if positions.dtype != torch.int32 or positions.shape != shape or positions.get_device() != index:
+        raise ValueError(f"positions: expected int32 {tuple(shape)} on the tensors' device")
+    if shape[-1] > 1 and positions.stride(-1) != 1:
+        raise ValueError("positions: expected contiguous rows")
+    return positions.stride(0) if len(shape) == 2 else 0
+
+
 def _rotate(x, positions, plan, out, backward):
+    index, dims = x.get_device(), x.dim()
     if x.dtype not in _DTYPES or x.dtype == torch.float8_e5m2:
         raise ValueError(f"expected bfloat16, float16 or float32 values, got {x.dtype}")
-    if x.dim() not in (3, 4) or not x.is_cuda:
+    if dims not in (3, 4) or index < 0:
         raise ValueError("expected a CUDA tensor [tokens, heads, dim] or [sequences, tokens, heads, dim]")
+    if plan.index != index:
+        raise ValueError("plan: on another device")
+    shape = x.shape
+    step = _positions(positions, shape[:-2], index)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = torch.empty(shape, dtype=x.dtype, device=x.device)
     else:
-        _writable(_tensor(out, "out", x.dtype, x.shape, x.device), "out")
-    _tensor(positions, "positions", torch.int32, x.shape[:-2], x.device)
-    _tensor(plan.turns, "plan", torch.int64, None, x.device)
+        _writable(_tensor(out, "out", x.dtype, shape, x.device), "out")
     if x.numel() == 0:
         return out
-    four, o, pos = (x, out, positions) if x.dim() == 4 else (x[None], out[None], positions[None])
-    if pos.shape[1] > 1 and pos.stride(1) != 1:
-        raise ValueError("positions: expected contiguous rows")
-    b, t, heads, d = four.shape
-    check(load().uzkv_rotary(ctypes.byref(_rows(four, "x")), ctypes.byref(_rows(o, "out")), _DTYPES[x.dtype], b, t,
-                             heads, d, pos.data_ptr(), pos.stride(0), plan.turns.data_ptr(), plan.rotary_dim,
-                             _LAYOUTS[plan.layout], plan.magnitude, backward, _sp(x.device)), "uzkv_rotary")
+    t, heads, d = shape[-3:]
+    check(load().uzkv_rotary(ctypes.byref(_rows(x, "x")), ctypes.byref(_rows(out, "out")), _DTYPES[x.dtype],
+                             shape[0] if dims == 4 else 1, t, heads, d, positions.data_ptr(), step, *plan.args,
+                             backward, _sp(index)), "uzkv_rotary")
     return out
 
 
@@ -198,7 +214,8 @@ class KVCache:
             if t.shape[3] > 1 and t.stride(3) != 1:
                 raise ValueError(f"{what}: elements of a row must be contiguous")
         self.k, self.v, self.page_table, self.lengths, self.status = k, v, page_table, lengths, status
-        self.device, self.dtype = k.device, k.dtype
+        self.device, self.dtype, self.index = k.device, k.dtype, k.get_device()
+        self.takes = (torch.bfloat16, torch.float16) if k.dtype == torch.float8_e5m2 else (k.dtype,)
         self.sequences, self.kv_heads, self.head_dim = page_table.shape[0], k.shape[1], k.shape[3]
         self.page_tokens = k.shape[2]
         self.capacity = page_table.shape[1] * k.shape[2]
@@ -207,21 +224,38 @@ class KVCache:
             lengths.data_ptr(), status.data_ptr() if status is not None else None, k.shape[0], k.shape[1], k.shape[2],
             k.shape[3], page_table.shape[0], page_table.shape[1], _DTYPES[k.dtype], 0)
         self._ref = ctypes.byref(self._c)
+        self._workspace_bytes: dict[tuple[int, int], int] = {}  # by (tokens, heads)
 
 
-def _new_rows(x: torch.Tensor, what: str, cache: KVCache, heads: int | None = None):
+def _new_rows(x: torch.Tensor, what: str, cache: KVCache, heads: int | None = None) -> _lib.KvRows:
     """Check new tokens' rows [sequences, tokens, heads, head dim] of a cache."""
-    if x.dim() != 4 or x.shape[0] != cache.sequences or x.shape[3] != cache.head_dim or not x.is_cuda \
-            or x.device != cache.device or (heads is not None and x.shape[2] != heads):
+    shape = x.shape
+    if len(shape) != 4 or shape[0] != cache.sequences or shape[3] != cache.head_dim or x.get_device() != cache.index \
+            or (heads is not None and shape[2] != heads):
         raise ValueError(f"{what}: expected [{cache.sequences}, tokens, {heads or 'heads'}, {cache.head_dim}] "
-                         f"on {cache.device}, got {tuple(x.shape)} on {x.device}")
-    if x.dtype not in (torch.bfloat16, torch.float16) or cache.dtype not in (x.dtype, torch.float8_e5m2):
+                         f"on {cache.device}, got {tuple(shape)} on {x.device}")
+    if x.dtype not in cache.takes:
         raise ValueError(f"{what}: {x.dtype} does not go with a cache of {cache.dtype}")
-    return x
+    return _rows(x, what)
+
+
+def _new_out(out: torch.Tensor | None, q: torch.Tensor):
+    """The output of q's shape (a new one where None), and its rows."""
+    if out is None:
+        b, t, heads, d = q.shape
+        out = torch.empty((b, t, heads, d), dtype=q.dtype, device=q.device)
+        return out, _lib.KvRows(out.data_ptr(), t * heads * d, heads * d, d)
+    _writable(_tensor(out, "out", q.dtype, q.shape, q.device), "out")
+    return out, _rows(out, "out")
 
 
 def _counts(counts, cache):
-    return _dense(counts, "counts", torch.int32, (cache.sequences,), cache.device).data_ptr() if counts is not None else None
+    if counts is None:
+        return None
+    if counts.dtype != torch.int32 or counts.shape != (cache.sequences,) or counts.get_device() != cache.index \
+            or not counts.is_contiguous():
+        raise ValueError(f"counts: expected a contiguous int32 tensor of {cache.sequences} on {cache.device}")
+    return counts.data_ptr()
 
 
 def rotary_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, plan: RotaryPlan,
@@ -233,27 +267,21 @@ def rotary_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: 
     projection are fine), ``positions`` int32 [sequences, tokens]. Tokens at or
     past ``counts`` give zero queries and are not stored. ``out`` may be ``q``.
     Advancing ``cache.lengths`` is the caller's, once the tokens are accepted."""
-    _new_rows(q, "q", cache)
-    b, t, heads, d = q.shape
-    for x, what in ((k, "k"), (v, "v")):
-        _new_rows(x, what, cache, cache.kv_heads)
-        if x.dtype != q.dtype or x.shape[1] != t:
-            raise ValueError(f"{what}: type or tokens differ from q's")
-    _tensor(positions, "positions", torch.int32, q.shape[:2], q.device)
-    if t > 1 and positions.stride(1) != 1:
-        raise ValueError("positions: expected contiguous rows")
-    _tensor(plan.turns, "plan", torch.int64, None, q.device)
-    if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    else:
-        _writable(_tensor(out, "out", q.dtype, q.shape, q.device), "out")
+    rq = _new_rows(q, "q", cache)
+    rk, rv = _new_rows(k, "k", cache, cache.kv_heads), _new_rows(v, "v", cache, cache.kv_heads)
+    _, t, heads, _ = q.shape
+    if k.shape[1] != t or v.shape[1] != t or k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError("k, v: type or tokens differ from q's")
+    if plan.index != cache.index:
+        raise ValueError("plan: on another device")
+    step = _positions(positions, q.shape[:2], cache.index)
+    out, ro = _new_out(out, q)
     if q.numel() == 0:
         return out
     ref = ctypes.byref
-    check(load().uzkv_rotary_append(ref(_rows(q, "q")), ref(_rows(k, "k")), ref(_rows(v, "v")), ref(_rows(out, "out")),
-                                    _DTYPES[q.dtype], t, heads, positions.data_ptr(), positions.stride(0),
-                                    plan.turns.data_ptr(), plan.rotary_dim, _LAYOUTS[plan.layout], plan.magnitude,
-                                    _counts(counts, cache), cache._ref, _sp(q.device)), "uzkv_rotary_append")
+    check(load().uzkv_rotary_append(ref(rq), ref(rk), ref(rv), ref(ro), _DTYPES[q.dtype], t, heads, positions.data_ptr(),
+                                    step, *plan.args, _counts(counts, cache), cache._ref, _sp(cache.index)),
+          "uzkv_rotary_append")
     return out
 
 
@@ -283,27 +311,37 @@ def tree_mask(parents, device="cuda") -> torch.Tensor:
 
 def _mask(mask, cache, t):
     """(address, words between sequences) of a mask."""
-    if mask is None:
-        return None, 0
     words = -(-t // 64)
     if mask.dim() != 3 or mask.shape[0] not in (1, cache.sequences) or mask.shape[1:] != (t, words):
         raise ValueError(f"mask: expected [{cache.sequences} or 1, {t}, {words}], got {tuple(mask.shape)}")
-    _dense(mask, "mask", torch.int64, None, cache.device)
+    if mask.dtype != torch.int64 or mask.get_device() != cache.index or not mask.is_contiguous():
+        raise ValueError(f"mask: expected a contiguous int64 tensor on {cache.device}")
     return mask.data_ptr(), 0 if mask.shape[0] == 1 else t * words
 
 
-def _query(q: torch.Tensor, cache: KVCache):
-    _new_rows(q, "q", cache)
+def _query(q: torch.Tensor, cache: KVCache) -> _lib.KvRows:
+    rows = _new_rows(q, "q", cache)
     if not 1 <= q.shape[1] <= MAX_NEW_TOKENS:
         raise ValueError(f"q: {q.shape[1]} new tokens, expected 1 to {MAX_NEW_TOKENS}")
     if q.shape[2] == 0 or q.shape[2] % cache.kv_heads:
         raise ValueError(f"q: {q.shape[2]} heads over {cache.kv_heads} kv heads")
-    return q
+    return rows
+
+
+def _floats(x: torch.Tensor, what: str, shape, cache: KVCache) -> int:
+    """Address of a contiguous float32 tensor of the given shape."""
+    if x.dtype != torch.float32 or x.shape != shape or x.get_device() != cache.index or not x.is_contiguous():
+        raise ValueError(f"{what}: expected contiguous float32 {tuple(shape)} on {cache.device}")
+    return x.data_ptr()
 
 
 def tree_attention_workspace_bytes(cache: KVCache, tokens: int, heads: int) -> int:
-    return int(load().uzkv_tree_attention_workspace_bytes(cache.sequences, tokens, heads, cache.kv_heads,
-                                                          cache.head_dim))
+    size = cache._workspace_bytes.get((tokens, heads))
+    if size is None:
+        size = int(load().uzkv_tree_attention_workspace_bytes(cache.sequences, tokens, heads, cache.kv_heads,
+                                                              cache.head_dim))
+        cache._workspace_bytes[tokens, heads] = size
+    return size
 
 
 def tree_attention(q: torch.Tensor, cache: KVCache, mask: torch.Tensor | None = None,
@@ -316,25 +354,22 @@ def tree_attention(q: torch.Tensor, cache: KVCache, mask: torch.Tensor | None = 
     sequence; None: a chain, each token and those before it). Returns ``(out,
     lse)``: the output, and the float32 log-sum-exp [sequences, tokens, heads].
     Rows that see nothing, and tokens at or past ``counts``, give 0 and -inf."""
-    _query(q, cache)
+    rq = _query(q, cache)
     b, t, heads, d = q.shape
-    address, stride = _mask(mask, cache, t)
-    if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    else:
-        _writable(_tensor(out, "out", q.dtype, q.shape, q.device), "out")
+    address, stride = _mask(mask, cache, t) if mask is not None else (None, 0)
+    out, ro = _new_out(out, q)
     if lse is None:
-        lse = torch.empty((b, t, heads), dtype=torch.float32, device=q.device)
+        lse = torch.empty((b, t, heads), dtype=torch.float32, device=cache.device)
+        at_lse = lse.data_ptr()
     else:
-        _dense(lse, "lse", torch.float32, (b, t, heads), q.device)
+        at_lse = _floats(lse, "lse", (b, t, heads), cache)
     if workspace is None:
-        workspace = torch.empty(tree_attention_workspace_bytes(cache, t, heads), dtype=torch.uint8, device=q.device)
-    elif not _tensor(workspace, "workspace", torch.uint8, None, q.device).is_contiguous():
+        workspace = torch.empty(tree_attention_workspace_bytes(cache, t, heads), dtype=torch.uint8, device=cache.device)
+    elif not _tensor(workspace, "workspace", torch.uint8, None, cache.device).is_contiguous():
         raise ValueError("workspace: expected a contiguous tensor")
-    check(load().uzkv_tree_attention(ctypes.byref(_rows(q, "q")), ctypes.byref(_rows(out, "out")), lse.data_ptr(),
-                                     _DTYPES[q.dtype], t, heads, address, stride, _counts(counts, cache),
-                                     d ** -0.5 if scale is None else scale, cache._ref, workspace.data_ptr(),
-                                     workspace.numel(), _sp(q.device)), "uzkv_tree_attention")
+    check(load().uzkv_tree_attention(ctypes.byref(rq), ctypes.byref(ro), at_lse, _DTYPES[q.dtype], t, heads, address,
+                                     stride, _counts(counts, cache), d ** -0.5 if scale is None else scale, cache._ref,
+                                     workspace.data_ptr(), workspace.numel(), _sp(cache.index)), "uzkv_tree_attention")
     return out, lse
 
 
@@ -350,29 +385,34 @@ def attention_mass(q: torch.Tensor, cache: KVCache, lse: torch.Tensor, mask: tor
     float32 [sequences, tokens] (1 for accepted tokens, 0 for the others; None:
     ones). ``out`` may be ``mass``; its width (default: the cache's capacity) says
     how many slots are weighed."""
-    _query(q, cache)
+    rq = _query(q, cache)
     b, t, heads, d = q.shape
-    address, stride = _mask(mask, cache, t)
-    _dense(lse, "lse", torch.float32, (b, t, heads), q.device)
-    if weights is not None:
-        _dense(weights, "weights", torch.float32, (b, t), q.device)
+    address, stride = _mask(mask, cache, t) if mask is not None else (None, 0)
+    at_lse = _floats(lse, "lse", (b, t, heads), cache)
+    at_weights = _floats(weights, "weights", (b, t), cache) if weights is not None else None
+    kv_heads = cache.kv_heads
     if out is None:
-        out = torch.empty(mass.shape if mass is not None else (b, cache.kv_heads, cache.capacity),
-                          dtype=torch.float32, device=q.device)
-    _tensor(out, "out", torch.float32, None, q.device)
-    if out.dim() != 3 or out.shape[:2] != (b, cache.kv_heads) or not 1 <= out.shape[2] <= cache.capacity:
-        raise ValueError(f"out: expected [{b}, {cache.kv_heads}, 1 to {cache.capacity}], got {tuple(out.shape)}")
-    _writable(out, "out")
+        out = torch.empty(mass.shape if mass is not None else (b, kv_heads, cache.capacity), dtype=torch.float32,
+                          device=cache.device)
+    else:
+        _writable(_tensor(out, "out", torch.float32, None, cache.device), "out")
+    shape = out.shape
+    if len(shape) != 3 or shape[0] != b or shape[1] != kv_heads or not 1 <= shape[2] <= cache.capacity:
+        raise ValueError(f"out: expected [{b}, {kv_heads}, 1 to {cache.capacity}], got {tuple(shape)}")
+    sb, sh, sn = out.stride()
+    if shape[2] > 1 and sn != 1:
+        raise ValueError("out: expected contiguous rows")
+    at_mass = None
     if mass is not None:
-        _tensor(mass, "mass", torch.float32, out.shape, q.device)
-    for x, what in ((out, "out"), (mass, "mass")):
-        if x is not None and (x.shape[2] > 1 and x.stride(2) != 1 or x.stride() != out.stride()):
-            raise ValueError(f"{what}: expected contiguous rows and the strides of out")
-    check(load().uzkv_attention_mass(ctypes.byref(_rows(q, "q")), lse.data_ptr(), _DTYPES[q.dtype], t, heads, address,
-                                     stride, _counts(counts, cache), weights.data_ptr() if weights is not None else None,
-                                     d ** -0.5 if scale is None else scale, cache._ref,
-                                     mass.data_ptr() if mass is not None else None, decay, out.data_ptr(),
-                                     out.stride(0), out.stride(1), out.shape[2], _sp(q.device)), "uzkv_attention_mass")
+        if mass.dtype != torch.float32 or mass.get_device() != cache.index or mass.shape != shape:
+            raise ValueError(f"mass: expected float32 {tuple(shape)} on {cache.device}")
+        if mass.stride() != (sb, sh, sn):
+            raise ValueError("mass: expected the strides of out")
+        at_mass = mass.data_ptr()
+    check(load().uzkv_attention_mass(ctypes.byref(rq), at_lse, _DTYPES[q.dtype], t, heads, address, stride,
+                                     _counts(counts, cache), at_weights, d ** -0.5 if scale is None else scale,
+                                     cache._ref, at_mass, decay, out.data_ptr(), sb, sh, shape[2], _sp(cache.index)),
+          "uzkv_attention_mass")
     return out
 
 
@@ -400,26 +440,34 @@ def evict(cache: KVCache, mass: torch.Tensor, keep: int, sink: int = 0, recent: 
     two halves of one contiguous buffer, ready for :func:`encode`; given ones may
     be views with room behind for tokens to come, but no part of the cache."""
     b, heads, d = cache.sequences, cache.kv_heads, cache.head_dim
-    _tensor(mass, "mass", torch.float32, None, cache.device)
-    if mass.dim() != 3 or mass.shape[:2] != (b, heads) or mass.shape[2] < 1:
-        raise ValueError(f"mass: expected [{b}, {heads}, slots], got {tuple(mass.shape)}")
-    if mass.shape[2] > 1 and mass.stride(2) != 1:
+    if mass.dtype != torch.float32 or mass.get_device() != cache.index or mass.dim() != 3 \
+            or mass.shape[0] != b or mass.shape[1] != heads or mass.shape[2] < 1:
+        raise ValueError(f"mass: expected float32 [{b}, {heads}, slots] on {cache.device}, got {mass.dtype} "
+                         f"{tuple(mass.shape)} on {mass.device}")
+    sb, sh, sn = mass.stride()
+    if mass.shape[2] > 1 and sn != 1:
         raise ValueError("mass: expected contiguous rows")
     if keep < 1 or sink < 0 or recent < 0 or sink + recent > keep:
         raise ValueError("expected keep >= 1 and 0 <= sink + recent <= keep")
-    shape = (b, heads, keep, d)
+    device = cache.device
     if out_k is None and out_v is None:
-        out_k, out_v = torch.empty((2, *shape), dtype=cache.dtype, device=cache.device)
+        both = torch.empty((2, b, heads, keep, d), dtype=cache.dtype, device=device)
+        out_k, out_v = both.unbind()
+        rows = heads * keep * d
+        rk = _lib.KvRows(both.data_ptr(), rows, keep * d, d)
+        rv = _lib.KvRows(both.data_ptr() + b * rows * both.element_size(), rows, keep * d, d)
     elif out_k is None or out_v is None:
         raise ValueError("give both out_k and out_v or neither")
-    for x, what in ((out_k, "out_k"), (out_v, "out_v")):
-        _writable(_tensor(x, what, cache.dtype, shape, cache.device), what)
-    kept = torch.empty((b, heads, keep), dtype=torch.int32, device=cache.device)
-    mass_out = torch.empty((b, heads, keep), dtype=torch.float32, device=cache.device)
-    lengths = torch.empty((b,), dtype=torch.int32, device=cache.device)
-    check(load().uzkv_evict(cache._ref, mass.data_ptr(), mass.stride(0), mass.stride(1), mass.shape[2], keep, sink,
-                            recent, ctypes.byref(_rows(out_k, "out_k")), ctypes.byref(_rows(out_v, "out_v")),
-                            kept.data_ptr(), mass_out.data_ptr(), lengths.data_ptr(), _sp(cache.device)), "uzkv_evict")
+    else:
+        for x, what in ((out_k, "out_k"), (out_v, "out_v")):
+            _writable(_tensor(x, what, cache.dtype, (b, heads, keep, d), device), what)
+        rk, rv = _rows(out_k, "out_k"), _rows(out_v, "out_v")
+    kept = torch.empty((b, heads, keep), dtype=torch.int32, device=device)
+    mass_out = torch.empty((b, heads, keep), dtype=torch.float32, device=device)
+    lengths = torch.empty((b,), dtype=torch.int32, device=device)
+    check(load().uzkv_evict(cache._ref, mass.data_ptr(), sb, sh, mass.shape[2], keep, sink, recent, ctypes.byref(rk),
+                            ctypes.byref(rv), kept.data_ptr(), mass_out.data_ptr(), lengths.data_ptr(),
+                            _sp(cache.index)), "uzkv_evict")
     return Packed(out_k, out_v, mass_out, kept, lengths)
 
 
