@@ -7,13 +7,13 @@
 // eight bits a pass, until the keys of the threshold's bin are all kept or all
 // bits are decided. Of keys equal to the threshold the lowest slots are kept.
 // One thread-block cluster takes one row (sequence, KV head), each of its CTAs
-// a contiguous share of the slots, whose keys it holds in shared memory (rows
-// beyond eight shares of kCached slots are read again each pass). A pass is
-// one barrier: counts, summed over the cluster through distributed shared
-// memory, then every warp finds the threshold's digit by itself. Bound: latency,
-// a few microseconds of barriers and shared-memory rounds. Kept slots
-// are written in slot order: a warp owns consecutive slots, 32 a step, so that
-// ballots give each kept slot its place within the warp's.
+// a contiguous share of the slots, whose keys it holds in shared memory (longer
+// shares are read again each pass). The second pass lists the keys that share
+// the first's digit, and later ones go through that list only. Counts of a
+// pass are summed over the cluster through distributed shared memory (the first
+// pass's spread over copies: masses share few leading bits). Bound: latency, some microseconds of barriers and shared-
+// memory rounds. Kept slots are written in slot order: a warp owns consecutive
+// slots, 32 a step, so that ballots give each kept slot its place.
 //
 // Pack: bound by HBM; each kept row is read and written once, 16 bytes a lane.
 #include <cooperative_groups.h>
@@ -28,7 +28,9 @@ namespace cg = cooperative_groups;
 namespace uzkv {
 namespace {
 
-constexpr uint32_t kCached = 32768;  // keys of a CTA's share in shared memory
+constexpr uint32_t kCached = 23552;  // keys of a CTA's share in shared memory, and as many of the second pass's list
+constexpr uint32_t kMaxRanks = 8;    // CTAs of a row (16 measured slower: the barriers)
+constexpr uint32_t kCopies = 32;     // of the first pass's counts, one a lane
 constexpr int kPackThreads = 256;
 
 struct Params {
@@ -60,20 +62,24 @@ template <int THREADS>
 __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__ Params p, uint32_t cached) {
     constexpr int kWarps = THREADS / 32;
     cg::cluster_group cluster = cg::this_cluster();
-    extern __shared__ uint32_t keys[];  // [cached] of this CTA's share, if it fits
-    __shared__ uint32_t hist[4][256];
-    __shared__ uint32_t totals[4][256];
+    extern __shared__ uint32_t keys[];  // [cached] of this CTA's share, if it fits; [cached] list
+    __shared__ uint32_t first[kCopies][256 + 1];  // a copy's digits one bank on from the last one's
+    __shared__ __align__(16) uint32_t hist[4][256];
+    __shared__ __align__(16) uint32_t hist_all[256];  // of the cluster
+    __shared__ uint4 choice;
     __shared__ uint32_t sums[2][kWarps];
-    __shared__ uint32_t share[2];  // this CTA's keys above and at the threshold
+    __shared__ __align__(8) uint32_t share[2];  // this CTA's keys above and at the threshold
     const uint32_t ranks = cluster.num_blocks(), rank = cluster.block_rank();
     const uint32_t row = blockIdx.y, b = row / p.cache.kv_heads, h = row % p.cache.kv_heads;
     const uint32_t tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     uzip::pdl_launch_dependents();
-    const uint32_t len = row_length(p, b);
-    const uint32_t target = min(len, p.keep);
     const float* mass = p.mass + b * p.mass_b + h * p.mass_h;
     int32_t* kept = p.kept + (uint64_t)row * p.keep;
     float* mass_out = p.mass_out + (uint64_t)row * p.keep;
+    for (uint32_t i = tid; i < kCopies * 257; i += THREADS) first[0][i] = 0;
+    for (uint32_t i = tid; i < 4 * 256; i += THREADS) hist[0][i] = 0;
+    const uint32_t len = row_length(p, b);
+    const uint32_t target = min(len, p.keep);
 
     if (h == 0 && rank == 0 && tid == 0) p.lengths_out[b] = (int32_t)target;
     for (uint32_t r = target + rank * THREADS + tid; r < p.keep; r += ranks * THREADS) {
@@ -94,74 +100,105 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__
     const uint32_t seg = (per / 32 + kWarps - 1) / kWarps * 32;
     const uint32_t w0 = min(end, begin + warp * seg), w1 = min(end, w0 + seg);
     const bool held = per <= cached;
-    for (uint32_t i = tid; i < 4 * 256; i += THREADS) reinterpret_cast<uint32_t*>(hist)[i] = 0;
-    if (held)
-#pragma unroll 4
-        for (uint32_t j = begin + tid; j < end; j += THREADS) keys[j - begin] = key_of(mass[j], j, len, p);
     __syncthreads();
     auto key_at = [&](uint32_t j) { return held ? keys[j - begin] : key_of(mass[j], j, len, p); };
 
+    // First digit, while the keys come in.
+    constexpr int kSteps = 8;  // masses on their way at once
+    for (uint32_t base = w0; base < w1; base += 32 * kSteps) {
+        float m[kSteps];
+#pragma unroll
+        for (int u = 0; u < kSteps; u++) m[u] = base + 32 * u + lane < w1 ? mass[base + 32 * u + lane] : 0.0f;
+#pragma unroll
+        for (int u = 0; u < kSteps; u++) {
+            const uint32_t j = base + 32 * u + lane;
+            if (j >= w1) break;
+            const uint32_t key = key_of(m[u], j, len, p);
+            if (held) keys[j - begin] = key;
+            atomicAdd(&first[lane % kCopies][key >> 24], 1u);
+        }
+    }
+    __syncthreads();
+    for (uint32_t d = tid; d < 256; d += THREADS) {
+        uint32_t n = 0;
+#pragma unroll
+        for (uint32_t c = 0; c < kCopies; c++) n += first[c][d];
+        hist[0][d] = n;
+    }
+
     // Threshold key: its digits from the top; `want` is how many keys are still to be taken at or below the
-    // decided digits. Masses share few leading bits, so lanes with the same first digit add up before they count.
+    // decided digits.
     uint32_t prefix = 0, want = target, threshold = 0;
+    uint32_t* const list = keys + cached + (w0 - begin);  // this warp's part
+    uint32_t listed = 0;
 #pragma unroll 1
     for (int pass = 0; pass < 4; pass++) {
         const uint32_t shift = 24 - 8 * pass;
-        if (pass == 0) {
-            for (uint32_t j0 = w0; j0 < w1; j0 += 32) {
-                const bool in = j0 + lane < w1;
-                const uint32_t digit = in ? key_at(j0 + lane) >> 24 : 256;
-                const uint32_t same = __match_any_sync(0xFFFFFFFFu, digit);
-                if (in && (int)lane == __ffs(same) - 1) atomicAdd(&hist[0][digit], (uint32_t)__popc(same));
+        if (pass == 1 && held) {
+            for (uint32_t base = w0; base < w1; base += 32 * kSteps) {
+                uint32_t key[kSteps];
+#pragma unroll
+                for (int u = 0; u < kSteps; u++) key[u] = base + 32 * u + lane < w1 ? keys[base + 32 * u + lane - begin] : 0;
+#pragma unroll
+                for (int u = 0; u < kSteps; u++) {
+                    const bool in = base + 32 * u + lane < w1 && key[u] >> 24 == prefix;
+                    const uint32_t mine = __ballot_sync(0xFFFFFFFFu, in);
+                    if (in) {
+                        list[listed + __popc(mine & ((1u << lane) - 1))] = key[u];
+                        atomicAdd(&hist[1][(key[u] >> 16) & 255], 1u);
+                    }
+                    listed += __popc(mine);
+                }
             }
-        } else {
-#pragma unroll 4
-            for (uint32_t j = w0 + lane; j < w1; j += 32) {
-                const uint32_t key = key_at(j);
+            __syncwarp();
+        } else if (pass > 0) {
+            for (uint32_t i = held ? lane : w0 + lane; i < (held ? listed : w1); i += 32) {
+                const uint32_t key = held ? list[i] : key_of(mass[i], i, len, p);
                 if ((key >> (shift + 8)) == prefix) atomicAdd(&hist[pass][(key >> shift) & 255], 1u);
             }
         }
-        const uint32_t* count = hist[pass];
         if (ranks > 1) {
             cluster.sync();
             if (tid < 256) {
-                uint32_t n = 0;
-                for (uint32_t r = 0; r < ranks; r++) n += cluster.map_shared_rank(&hist[pass][0], r)[tid];
-                totals[pass][tid] = n;
+                uint32_t n[kMaxRanks] = {}, all = 0;  // all on their way at once
+#pragma unroll
+                for (uint32_t r = 0; r < kMaxRanks; r++)
+                    if (r < ranks) n[r] = cluster.map_shared_rank(&hist[pass][0], r)[tid];
+#pragma unroll
+                for (uint32_t r = 0; r < kMaxRanks; r++) all += n[r];
+                hist_all[tid] = all;
             }
-            count = totals[pass];
         }
         __syncthreads();
-        // Lane l holds digits 255 - 8 l down to 248 - 8 l; the threshold's is where the running count reaches `want`.
-        uint32_t mine[8], n = 0;
+        if (warp == 0) {
+            // Lane l holds digits 255 - 8 l down to 248 - 8 l; the threshold's is where the running count reaches `want`.
+            const uint32_t* count = ranks > 1 ? hist_all : hist[pass];
+            const uint4 hi = *reinterpret_cast<const uint4*>(count + 252 - 8 * lane), lo = *reinterpret_cast<const uint4*>(count + 248 - 8 * lane);
+            const uint32_t mine[8] = {hi.w, hi.z, hi.y, hi.x, lo.w, lo.z, lo.y, lo.x};
+            uint32_t n = 0;
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            mine[i] = count[255 - 8 * lane - i];
-            n += mine[i];
-        }
-        uint32_t upto = n;
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
-            if (lane >= (uint32_t)o) upto += v;
-        }
-        const int owner = __ffs(__ballot_sync(0xFFFFFFFFu, upto >= want)) - 1;
-        uint32_t above = upto - n, digit = 0, at = 0;
-        bool found = false;
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-            if (!found && want <= above + mine[i]) {
-                found = true;
-                digit = 255 - 8 * lane - i;
-                at = mine[i];
+            for (int i = 0; i < 8; i++) n += mine[i];
+            uint32_t upto = n;
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+                if (lane >= (uint32_t)o) upto += v;
             }
-            if (!found) above += mine[i];
+            uint32_t above = upto - n;
+            if (above < want && want <= upto) {
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    if (above < want && want <= above + mine[i])
+                        choice = make_uint4(255 - 8 * lane - i, above, mine[i], 0);
+                    above += mine[i];
+                }
+            }
         }
-        digit = __shfl_sync(0xFFFFFFFFu, digit, owner);
-        want -= __shfl_sync(0xFFFFFFFFu, above, owner);
-        at = __shfl_sync(0xFFFFFFFFu, at, owner);
-        prefix = prefix << 8 | digit;
+        __syncthreads();
+        const uint4 c = choice;  // digit, keys above it, keys of it
+        want -= c.y;
+        prefix = prefix << 8 | c.x;
         threshold = prefix << shift;
-        if (at == want && threshold) {  // all of the bin is kept: every key from its lowest on
+        if (c.z == want && threshold) {  // all of the bin is kept: every key from its lowest on
             threshold -= 1;
             want = 0;
             break;
@@ -170,11 +207,14 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__
     // Keys above the threshold are kept, and the first `want` equal to it.
 
     uint32_t gt = 0, eq = 0;  // of this warp's slots
-    for (uint32_t j0 = w0; j0 < w1; j0 += 32) {
-        const uint32_t key = j0 + lane < w1 ? key_at(j0 + lane) : 0;
-        gt += __popc(__ballot_sync(0xFFFFFFFFu, j0 + lane < w1 && key > threshold));
-        eq += __popc(__ballot_sync(0xFFFFFFFFu, j0 + lane < w1 && key == threshold));
+#pragma unroll 4
+    for (uint32_t j = w0 + lane; j < w1; j += 32) {
+        const uint32_t key = key_at(j);
+        gt += key > threshold;
+        eq += key == threshold;
     }
+    gt = __reduce_add_sync(0xFFFFFFFFu, gt);
+    eq = __reduce_add_sync(0xFFFFFFFFu, eq);
     if (lane == 0) {
         sums[0][warp] = gt;
         sums[1][warp] = eq;
@@ -197,25 +237,40 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const __grid_constant__
     e = __shfl_sync(0xFFFFFFFFu, e - e0, warp);
     if (ranks > 1) {
         cluster.sync();
-        for (uint32_t r = 0; r < rank; r++) {
-            const uint32_t* s = cluster.map_shared_rank(&share[0], r);
-            g += s[0];
-            e += s[1];
+        uint32_t sg = 0, se = 0;  // lane r: CTA r, if it is before this one
+        if (lane < rank) {
+            const uint2 s = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(&share[0], lane));
+            sg = s.x;
+            se = s.y;
         }
+        g += __reduce_add_sync(0xFFFFFFFFu, sg);
+        e += __reduce_add_sync(0xFFFFFFFFu, se);
     }
-    for (uint32_t j0 = w0; j0 < w1; j0 += 32) {
-        const uint32_t j = j0 + lane, below = (1u << lane) - 1;
-        const uint32_t key = j < w1 ? key_at(j) : 0;
-        const uint32_t gs = __ballot_sync(0xFFFFFFFFu, j < w1 && key > threshold);
-        const uint32_t es = __ballot_sync(0xFFFFFFFFu, j < w1 && key == threshold);
-        const uint32_t ge = g + __popc(gs & below), ee = e + __popc(es & below);
-        if (j < w1 && (key > threshold || (key == threshold && ee < want))) {
-            const uint32_t at = ge + min(ee, want);
-            kept[at] = (int32_t)j;
-            mass_out[at] = mass[j];
+    for (uint32_t base = w0; base < w1; base += 32 * kSteps) {
+        float m[kSteps];
+#pragma unroll
+        for (int u = 0; u < kSteps; u++) m[u] = base + 32 * u + lane < w1 ? mass[base + 32 * u + lane] : 0.0f;
+#pragma unroll
+        for (int u = 0; u < kSteps; u++) {
+            const uint32_t j = base + 32 * u + lane, below = (1u << lane) - 1;
+            const bool in = j < w1;
+            const uint32_t key = !in ? 0 : held ? keys[j - begin] : key_of(m[u], j, len, p);
+            const uint32_t gs = __ballot_sync(0xFFFFFFFFu, in && key > threshold);
+            uint32_t at = g + __popc(gs & below);
+            bool keep = in && key > threshold;
+            if (want) {  // the same for all: ties at the threshold to tell apart
+                const uint32_t es = __ballot_sync(0xFFFFFFFFu, in && key == threshold);
+                const uint32_t ee = e + __popc(es & below);
+                keep |= in && key == threshold && ee < want;
+                at += min(ee, want);
+                e += __popc(es);
+            }
+            if (keep) {
+                kept[at] = (int32_t)j;
+                mass_out[at] = m[u];
+            }
+            g += __popc(gs);
         }
-        g += __popc(gs);
-        e += __popc(es);
     }
     if (ranks > 1) cluster.sync();  // no CTA leaves while another reads its shared memory
 }
@@ -239,6 +294,30 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const __grid_constan
         *reinterpret_cast<uint4*>(p.out_k.p + b * p.out_k.b + h * p.out_k.t + r * p.out_k.h + c) = k;
         *reinterpret_cast<uint4*>(p.out_v.p + b * p.out_v.b + h * p.out_v.t + r * p.out_v.h + c) = v;
     }
+}
+
+template <int THREADS>
+int launch_select(const Params& p, uint32_t ranks, uint32_t rows, uint32_t held, cudaStream_t s) {
+    static std::atomic<uint64_t> ready{0};  // a bit for each device whose limit is raised
+    int dev = 0;
+    UZIP_CUDA_TRY(cudaGetDevice(&dev));
+    if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+        UZIP_CUDA_TRY(cudaFuncSetAttribute(select_kernel<THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kCached * 8));
+        if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(ranks, rows);
+    cfg.blockDim = dim3(THREADS);
+    cfg.stream = s;
+    cfg.dynamicSmemBytes = held * 8;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = ranks;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = ranks > 1 ? 1 : 0;
+    UZIP_CUDA_TRY(cudaLaunchKernelEx(&cfg, select_kernel<THREADS>, p, held));
+    return UZIP_OK;
 }
 
 }  // namespace
@@ -276,34 +355,15 @@ extern "C" UZIP_API int uzkv_evict(const uzkv_cache_t* cache, const float* d_mas
     int sms = 0;
     if (int rc = sm_count(&sms)) return rc;
     const uint32_t rows = p.cache.sequences * p.cache.kv_heads;
-    // A row's CTAs: up to eight while the SMs have room and a share keeps 4096 slots.
+    // A row's CTAs: as many as the SMs have room for, up to eight, while a share keeps 4096 slots.
     uint32_t ranks = 1;
-    while (ranks < 8 && rows * ranks * 2 <= (uint32_t)sms && slots / ranks > 4096) ranks *= 2;
+    while (ranks < kMaxRanks && rows * ranks * 2 <= (uint32_t)sms && slots / ranks > 4096) ranks *= 2;
     const uint32_t per = ((slots + ranks - 1) / ranks + 31) / 32 * 32, held = per <= kCached ? per : 0;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(ranks, rows);
-    cfg.stream = s;
-    cfg.dynamicSmemBytes = held * 4;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = ranks;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = ranks > 1 ? 1 : 0;
     if (per <= 4096) {  // short shares: fewer warps meet at the barriers
-        cfg.blockDim = dim3(256);
-        UZIP_CUDA_TRY(cudaLaunchKernelEx(&cfg, select_kernel<256>, p, held));
+        if (int rc = launch_select<256>(p, ranks, rows, held, s)) return rc;
     } else {
-        static std::atomic<uint64_t> ready{0};  // a bit for each device whose limit is raised
-        int dev = 0;
-        UZIP_CUDA_TRY(cudaGetDevice(&dev));
-        if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
-            UZIP_CUDA_TRY(cudaFuncSetAttribute(select_kernel<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kCached * 4));
-            if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
-        }
-        cfg.blockDim = dim3(1024);
-        UZIP_CUDA_TRY(cudaLaunchKernelEx(&cfg, select_kernel<1024>, p, held));
+        if (int rc = launch_select<1024>(p, ranks, rows, held, s)) return rc;
     }
     const uint64_t chunks = (uint64_t)keep * p.row_chunks;
     const uint64_t want = std::max<uint64_t>(1, (uint64_t)sms * 32 / rows);
