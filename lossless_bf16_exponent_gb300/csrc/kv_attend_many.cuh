@@ -63,6 +63,13 @@ __device__ __forceinline__ void tc_ld32(uint32_t* r, uint32_t addr) {
         : "r"(addr)
         : "memory");
 }
+__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
 __device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t* r) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
@@ -305,12 +312,12 @@ __global__ void __launch_bounds__(kManyThreads, 1) attend_many_kernel(const __gr
             const Unit& u = part.u;
             const uint32_t row0 = u.mt * p.m;
             if (part.both)
-                load_queries<QT, T, DP, 128, 1>(
+                load_queries<QT, T, DP, 128>(
                     p, tid % 128, u.b, u.h, row0 + x * 128, 128,
                     [&](uint32_t r, uint32_t ch) { return reinterpret_cast<uint4*>(qs + x * C::kQTile + swizzled(128, r, ch)); },
                     factor + x * 128);
             else  // half of the shared rows each
-                load_queries<QT, T, DP, 128, 1>(
+                load_queries<QT, T, DP, 128>(
                     p, tid % 128, u.b, u.h, row0 + x * 64, 64,
                     [&](uint32_t r, uint32_t ch) { return reinterpret_cast<uint4*>(qs + swizzled(128, x * 64 + r, ch)); },
                     factor + x * 64);
@@ -334,58 +341,72 @@ __global__ void __launch_bounds__(kManyThreads, 1) attend_many_kernel(const __gr
                     seen[0] = seen_bits(p, u.b, u.span, row0 + mine, j0);
                     seen[1] = seen_bits(p, u.b, u.span, row0 + mine, j0 + 64);
                 }
-                uint32_t w[64];
-                float most, add;
-                auto weigh = [&](float r) {  // weights against reference r, their sum, and the largest exponent
-                    most = -INFINITY;
-                    float part_sum[4] = {0.0f, 0.0f, 0.0f, 0.0f}, part_top[2] = {-INFINITY, -INFINITY};
+                // Largest score of the row: 32 columns at a time, the next ones on their way meanwhile.
+                uint32_t v[2][32];
+                float part[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                tc_ld32(v[0], st);
 #pragma unroll
-                    for (int c = 0; c < 4; c++) {
-                        uint32_t v[32];
-                        tc_ld32(v, st + 32 * c);
-                        tc_wait_ld();
+                for (int c = 0; c < 4; c++) {
+                    tc_wait_ld();
+                    tc_ld32(v[(c + 1) & 1], st + (c < 3 ? 32 * (c + 1) : 0));  // after the last, the first again
+                    uint32_t* y = v[c & 1];
+                    if (masked) {
                         const uint32_t bits = (uint32_t)(seen[c / 2] >> (32 * (c & 1)));
 #pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            float a = __uint_as_float(v[i]) * f - r, b = __uint_as_float(v[i + 1]) * f - r;
-                            if (masked) {
-                                if (!(bits >> i & 1)) a = -INFINITY;
-                                if (!(bits >> i & 2)) b = -INFINITY;
-                            }
-                            part_top[0] = fmaxf(part_top[0], a);
-                            part_top[1] = fmaxf(part_top[1], b);
-                            a = exp2_fast(a);
-                            b = exp2_fast(b);
-                            part_sum[i & 2] += a;
-                            part_sum[(i & 2) + 1] += b;
-                            w[16 * c + i / 2] = pack2<T>(a, b);
-                        }
+                        for (int i = 0; i < 32; i++)
+                            if (!(bits >> i & 1)) y[i] = 0xFF800000u;  // -inf
                     }
-                    most = fmaxf(part_top[0], part_top[1]);
-                    add = (part_sum[0] + part_sum[1]) + (part_sum[2] + part_sum[3]);
-                };
-                const float r = ref == -INFINITY ? 0.0f : ref - kLift<T>;
-                weigh(r);
-                const bool rise = ref == -INFINITY ? most > -INFINITY : most > kSlack + kLift<T>;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2)
+                        part[i / 2 % 4] = fmaxf(part[i / 2 % 4], fmaxf(__uint_as_float(y[i]), __uint_as_float(y[i + 1])));
+                }
+                const float most = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+                const float high = most == -INFINITY ? most : most * f;  // f is not negative; 0 * -inf is none
+                const bool rise = high > ref + kSlack;                   // the reference may trail by kSlack
                 if (__any_sync(0xFFFFFFFFu, rise)) {
-                    const float now = fmaxf(ref, most + r);
+                    const float now = fmaxf(ref, high);
                     const float fade = ref == -INFINITY ? 0.0f : exp2_fast(ref - now);  // 0: nothing so far
                     ref = now;
                     sum *= fade;
-                    if (j > 0)  // the stream's products are complete up to its last tile
+                    if (j > 0) {  // the stream's products are complete up to its last tile
+                        tc_wait_ld();
                         for (uint32_t c = 0; c < D; c += 32) {
-                            uint32_t v[32];
-                            tc_ld32(v, ot + c);
+                            uint32_t z[32];
+                            tc_ld32(z, ot + c);
                             tc_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 32; i++) v[i] = __float_as_uint(__uint_as_float(v[i]) * fade);
-                            tc_st32(ot + c, v);
+                            for (int i = 0; i < 32; i++) z[i] = __float_as_uint(__uint_as_float(z[i]) * fade);
+                            tc_st32(ot + c, z);
                         }
-                    weigh(ref == -INFINITY ? 0.0f : ref - kLift<T>);
+                    }
                 }
-                sum += add;
-                tc_st32(st, w);
-                tc_st32(st + 32, w + 32);
+                // Weights: they take the place of scores already read.
+                const float r = ref == -INFINITY ? 0.0f : ref - kLift<T>;
+                const uint64_t f2 = pair(f, f), r2 = pair(-r, -r);
+                uint64_t add[2] = {0, 0};
+#pragma unroll
+                for (int c = 0; c < 4; c++) {
+                    tc_wait_ld();
+                    if (c < 3) tc_ld32(v[(c + 1) & 1], st + 32 * (c + 1));
+                    const uint32_t* y = v[c & 1];
+                    const uint32_t bits = (uint32_t)(seen[c / 2] >> (32 * (c & 1)));
+                    uint32_t w[16];
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        float2 a = unpair(fma2(pair(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), f2, r2));
+                        if (masked) {
+                            if (!(bits >> i & 1)) a.x = -INFINITY;
+                            if (!(bits >> i & 2)) a.y = -INFINITY;
+                        }
+                        a.x = exp2_fast(a.x);
+                        a.y = exp2_fast(a.y);
+                        add[i / 2 & 1] = add2(add[i / 2 & 1], pair(a.x, a.y));
+                        w[i / 2] = pack2<T>(a.x, a.y);
+                    }
+                    tc_st16(st + 16 * c, w);
+                }
+                const float2 total = unpair(add2(add[0], add[1]));
+                sum += total.x + total.y;
                 tc_wait_st();
                 tc_fence_before();
                 __syncwarp();

@@ -306,11 +306,11 @@ template <>
 constexpr float kLift<__half> = 6.0f;
 
 // Queries of rows row0 .. row0 + rows - 1 to shared memory as T (columns past head_dim and rows past p.rows
-// zero), by THREADS threads numbered tid; at(row, c) is where 16-byte chunk c of a row goes. factor[r *
-// STRIDE], where wanted, is what a score of row r is to be multiplied by to have it in units of log2: scale *
-// log2(e), and for BF16 queries that go to an FP16 product the power of two that was taken out of the row to
-// bring its largest element to [1, 2).
-template <typename QT, typename T, int DP, int THREADS, int STRIDE, typename At>
+// zero), by THREADS threads numbered tid; at(row, c) is where 16-byte chunk c of a row goes. factor[r] is what a
+// score of row r is to be multiplied by to have it in units of log2: |scale| * log2(e), and for BF16 queries that
+// go to an FP16 product the power of two that was taken out of the row to bring its largest element to [1, 2).
+// The sign of scale goes to the queries.
+template <typename QT, typename T, int DP, int THREADS, typename At>
 __device__ __forceinline__ void load_queries(const AttParams& p, uint32_t tid, uint32_t b, uint32_t h, uint32_t row0,
                                              uint32_t rows, At at, float* factor) {
     constexpr bool kCast = !std::is_same<QT, T>::value;
@@ -323,7 +323,7 @@ __device__ __forceinline__ void load_queries(const AttParams& p, uint32_t tid, u
             const uint32_t t = row / p.group, g = row - t * p.group;
             x = *reinterpret_cast<const uint4*>(p.q.p + b * p.q.b + t * p.q.t + (uint64_t)(h * p.group + g) * p.q.h + c * 16);
         }
-        float f = p.scale * kLog2e;
+        float f = fabsf(p.scale) * kLog2e;
         if (kCast) {
             const QT* e = reinterpret_cast<const QT*>(&x);
             float v[8], top = 0.0f;
@@ -343,8 +343,14 @@ __device__ __forceinline__ void load_queries(const AttParams& p, uint32_t tid, u
 #pragma unroll
             for (int k = 0; k < 4; k++) w[k] = pack2<__half>(v[2 * k] * down, v[2 * k + 1] * down);
         }
+        if (p.scale < 0.0f) {
+            x.x ^= 0x80008000u;
+            x.y ^= 0x80008000u;
+            x.z ^= 0x80008000u;
+            x.w ^= 0x80008000u;
+        }
         *at(i, c) = x;
-        if (factor && c == 0) factor[i * STRIDE] = f;
+        if (c == 0) factor[i] = f;
     }
 }
 

@@ -75,8 +75,8 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const __grid_cons
     char* const qs = smem;
     char* const tiles = qs + C::kQBytes;
     char* const raws = tiles + C::kTiles * C::kTileBytes;
-    float2* const rowf = reinterpret_cast<float2*>(raws + C::kRaw * C::kRawBytes);  // [2][256]: factor, exponent
-    uint64_t* const bars = reinterpret_cast<uint64_t*>(rowf + 512);
+    float* const rowf = reinterpret_cast<float*>(raws + C::kRaw * C::kRawBytes);  // [2][2][256]: factors; exponents, negative
+    uint64_t* const bars = reinterpret_cast<uint64_t*>(rowf + 1024);
     uint32_t* const tmem_at = reinterpret_cast<uint32_t*>(bars + 32);
     const uint32_t tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const uint32_t D = p.cache.head_dim, N = p.m;
@@ -160,19 +160,19 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const __grid_cons
             if (!ok) break;
             const uint32_t row0 = w.chunk * N;
             char* q = qs + qb * N * DP * 2;
-            float2* f = rowf + fb * 256;
-            load_queries<QT, T, DP, 128, 2>(
+            float* f = rowf + fb * 512;
+            load_queries<QT, T, DP, 128>(
                 p, tid, w.u.b, w.u.h, row0, N, [&](uint32_t r, uint32_t ch) { return reinterpret_cast<uint4*>(q + swizzled(N, r, ch)); },
-                &f[0].x);
+                f);
             for (uint32_t r = tid; r < N; r += 128) {
                 const uint32_t row = row0 + r, t = row / p.group;
-                float e = INFINITY;  // a row that adds nothing
+                float e = -INFINITY;  // a row that adds nothing
                 if (row < p.rows && t < w.u.span.fresh) {
                     const float lse = p.lse[((uint64_t)w.u.b * p.tokens + t) * p.q_heads + w.u.h * p.group + row % p.group];
                     const float wt = p.weights ? p.weights[(uint64_t)w.u.b * p.tokens + t] : 1.0f;
-                    if (lse != -INFINITY && wt != 0.0f) e = p.weights ? lse * kLog2e - log2f(wt) : lse * kLog2e;
+                    if (lse != -INFINITY && wt != 0.0f) e = p.weights ? log2f(wt) - lse * kLog2e : -lse * kLog2e;
                 }
-                f[r].y = e;
+                f[256 + r] = e;
             }
             fence_async_smem();
             __syncwarp();
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const __grid_cons
         uint32_t seg = 0, used = 0;
         for (MassWalk w(first, run.end); w.valid() && ok; w.next(p), seg++) {
             const Span sp = w.u.span;
-            const float2* f = rowf + seg % 2 * 256;
+            const float *f = rowf + seg % 2 * 512, *e = f + 256;
             const int64_t row_at = w.u.b * p.mass_b + w.u.h * p.mass_h;
             ok = warp_wait(q_full + 8 * (seg % 2), (seg / 2) & 1);
             for (uint32_t i = 0; i < w.count && ok; i++) {
@@ -247,38 +247,62 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const __grid_cons
                 float acc = 0.0f;
                 bool guard = j0 + kMassTile > sp.old;
                 if (!guard) {
-                    float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    // 16 columns at a time, the next ones on their way meanwhile.
+                    float v[2][16];
+                    uint64_t part[2] = {0, 0};
+                    tc_ld16(v[0], at);
+                    auto columns = [&](const float* x, uint32_t c0) {
+#pragma unroll
+                        for (int i = 0; i < 16; i += 4) {
+                            const ulonglong2 en = *reinterpret_cast<const ulonglong2*>(e + c0 + i);
+                            ulonglong2 fn = make_ulonglong2(pair(fabsf(p.scale) * kLog2e, fabsf(p.scale) * kLog2e), 0);
+                            fn.y = fn.x;
+                            if (FP8) fn = *reinterpret_cast<const ulonglong2*>(f + c0 + i);  // rows have their own powers of two
+                            const float2 a = unpair(fma2(pair(x[i], x[i + 1]), fn.x, en.x)), b = unpair(fma2(pair(x[i + 2], x[i + 3]), fn.y, en.y));
+                            part[0] = add2(part[0], pair(exp2_fast(a.x), exp2_fast(a.y)));
+                            part[1] = add2(part[1], pair(exp2_fast(b.x), exp2_fast(b.y)));
+                        }
+                    };
+                    for (uint32_t c0 = 0; c0 < N; c0 += 32) {
+                        tc_wait_ld();
+                        if (c0 + 16 < N) tc_ld16(v[1], at + c0 + 16);
+                        columns(v[0], c0);
+                        if (c0 + 16 < N) {
+                            tc_wait_ld();
+                            if (c0 + 32 < N) tc_ld16(v[0], at + c0 + 32);
+                            columns(v[1], c0 + 16);
+                        }
+                    }
+                    const float2 sum = unpair(add2(part[0], part[1]));
+                    acc = sum.x + sum.y;
+                    // A key that is not finite makes NaN of rows that add nothing too: take those rows out.
+                    guard = __any_sync(0xFFFFFFFFu, acc != acc);
+                }
+                if (guard) {
+                    // Which new tokens see this lane's: token by token, its mask word fetched one token ahead.
+                    acc = 0.0f;
+                    const uint32_t row0 = w.chunk * N, u = j - sp.old;
+                    uint32_t t = row0 / p.group, left = p.group - row0 % p.group;  // rows left of token t
+                    const bool in = j < sp.old + sp.fresh;
+                    const int64_t* words = p.mask ? p.mask + w.u.b * p.mask_b + (in && j >= sp.old ? u >> 6 : 0) : nullptr;
+                    auto word_of = [&](uint32_t tok) -> int64_t { return words && tok < sp.fresh ? words[(uint64_t)tok * p.mask_words] : 0; };
+                    auto sees = [&](int64_t word) { return in && (j < sp.old || (words ? (bool)(word >> (u & 63) & 1) : u <= t)); };
+                    int64_t word = word_of(t), ahead = word_of(t + 1);
+                    bool see = sees(word);
                     for (uint32_t c0 = 0; c0 < N; c0 += 16) {
                         float v[16];
                         tc_ld16(v, at + c0);
                         tc_wait_ld();
 #pragma unroll
-                        for (int x = 0; x < 16; x += 2) {
-                            const float4 e = *reinterpret_cast<const float4*>(f + c0 + x);
-                            part[x % 4] += exp2_fast(v[x] * e.x - e.y);
-                            part[x % 4 + 1] += exp2_fast(v[x + 1] * e.z - e.w);
-                        }
-                    }
-                    acc = (part[0] + part[1]) + (part[2] + part[3]);
-                    // A key that is not finite makes NaN of rows that add nothing too: take those rows out.
-                    guard = __any_sync(0xFFFFFFFFu, acc != acc);
-                }
-                if (guard) {
-                    acc = 0.0f;
-                    const uint32_t row0 = w.chunk * N;
-                    for (uint32_t c0 = 0; c0 < N; c0 += 16) {
-                        float v[16];
-                        tc_ld16(v, at + c0);
-                        tc_wait_ld();
                         for (int x = 0; x < 16; x++) {
-                            const float2 e = f[c0 + x];
-                            const uint32_t t = (row0 + c0 + x) / p.group;
-                            bool see = e.y != INFINITY;
-                            if (see && j >= sp.old)
-                                see = j < sp.old + sp.fresh &&
-                                      mask_bit(p.mask ? p.mask + w.u.b * p.mask_b + (uint64_t)t * p.mask_words : nullptr, t, j - sp.old);
-                            const float m = exp2_fast(v[x] * e.x - e.y);
-                            acc += see ? m : 0.0f;
+                            const float m = exp2_fast(v[x] * f[c0 + x] + e[c0 + x]);
+                            acc += see && e[c0 + x] != -INFINITY ? m : 0.0f;
+                            if (--left == 0) {
+                                left = p.group;
+                                t++;
+                                see = sees(ahead);
+                                ahead = word_of(t + 1);
+                            }
                         }
                     }
                 }
