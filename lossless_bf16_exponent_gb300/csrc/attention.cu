@@ -169,11 +169,11 @@ extern "C" UZIP_API int uzkv_tree_attention(const uzkv_rows_t* q, const uzkv_row
     int sms = 0;
     if (int rc = sm_count(&sms)) return rc;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    using Launch = int (*)(AttParams&, int, cudaStream_t);
+    using Launch = int (*)(AttParams&, const uzkv_cache_t*, int, cudaStream_t);
     static constexpr Launch kLaunch[2][2][2] = {  // [many rows][FP16][E5M2 cache]
         {{attend_bf16, attend_bf16_e5m2}, {attend_fp16, attend_fp16_e5m2}},
         {{attend_many_bf16, attend_many_bf16_e5m2}, {attend_many_fp16, attend_many_fp16_e5m2}}};
-    if (int rc = kLaunch[many(p.rows, p.cache.head_dim)][dtype == UZKV_FP16][cache->dtype == UZKV_E5M2](p, sms, s)) return rc;
+    if (int rc = kLaunch[many(p.rows, p.cache.head_dim)][dtype == UZKV_FP16][cache->dtype == UZKV_E5M2](p, cache, sms, s)) return rc;
     return dtype == UZKV_BF16 ? launch_join<__nv_bfloat16>(p, s) : launch_join<__half>(p, s);
 }
 
@@ -201,6 +201,6 @@ extern "C" UZIP_API int uzkv_attention_mass(const uzkv_rows_t* q, const float* d
     if (int rc = sm_count(&sms)) return rc;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const bool fp8 = cache->dtype == UZKV_E5M2;
-    if (dtype == UZKV_BF16) return fp8 ? mass_bf16_e5m2(p, sms, s) : mass_bf16(p, sms, s);
-    return fp8 ? mass_fp16_e5m2(p, sms, s) : mass_fp16(p, sms, s);
+    if (dtype == UZKV_BF16) return fp8 ? mass_bf16_e5m2(p, cache, sms, s) : mass_bf16(p, cache, sms, s);
+    return fp8 ? mass_fp16_e5m2(p, cache, sms, s) : mass_fp16(p, cache, sms, s);
 }

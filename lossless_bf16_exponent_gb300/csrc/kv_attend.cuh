@@ -5,9 +5,10 @@
 // Bound: HBM, as long as the products of a tile take less time than its bytes
 // (4 D flop a row and token against 2 D bytes an element's width: up to about
 // 64 rows at the warp-level product's rate). So the kernel is built to keep
-// copies in flight: one CTA an SM, four warps that only copy, eight that only
-// compute, and a ring of stages between them. Copying warps find their tokens'
-// pages one tile ahead and run on across unit boundaries.
+// copies in flight: one CTA an SM, a warp that only copies (four where pages do
+// not allow bulk copies), eight that only compute, and a ring of stages between
+// them. The copies' pages are looked up one tile ahead, and the ring runs on
+// across unit boundaries.
 //
 // The products have the cached tokens along M: S^T = K Q^T and O^T = V^T P^T,
 // 16 tokens (or 16 columns of V) by 8 rows. Eight rows of a decoding step waste
@@ -28,7 +29,7 @@
 #include <algorithm>
 #include <atomic>
 
-#include "kv_attention.cuh"
+#include "kv_tma.cuh"
 
 namespace uzkv {
 
@@ -52,10 +53,11 @@ struct AttCfg {
     static_assert(kKeys >= 16, "a product's tokens");
 };
 
-constexpr int kAttThreads = 12 * 32;  // 8 warps that compute, 4 that copy
+template <bool TMA>
+constexpr int kAttThreads = (8 + (TMA ? 1 : 4)) * 32;  // 8 warps that compute, the others copy
 
-template <typename QT, bool FP8, int DP, int RN, int WM>
-__global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_constant__ AttParams p) {
+template <typename QT, bool FP8, int DP, int RN, int WM, bool TMA>
+__global__ void __launch_bounds__(kAttThreads<TMA>, 1) attend_kernel(const __grid_constant__ AttParams p, const __grid_constant__ Maps maps) {
     using C = AttCfg<QT, FP8, DP, RN, WM>;
     using T = typename C::T;
     extern __shared__ __align__(1024) char smem[];
@@ -68,14 +70,14 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
     uzip::pdl_launch_dependents();
     if (tid == 0) {
         for (int s = 0; s < C::kStages; s++) {
-            bar_init(full + 8 * s, 128);  // every copying thread
+            bar_init(full + 8 * s, TMA ? 1 : 128);  // every copying thread
             bar_init(freed + 8 * s, 8);   // every computing warp
         }
         bar_init(merge, 8);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (D < DP)  // columns past the head dimension stay zero: no copy writes them
-        for (uint32_t i = tid; i < C::kStages * C::kStage / 16; i += kAttThreads) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
+    if (!TMA && D < DP)  // columns past the head dimension stay zero: no copy writes them
+        for (uint32_t i = tid; i < C::kStages * C::kStage / 16; i += kAttThreads<TMA>) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
     const Split split = split_of(p);
     const Run run = run_of(p, split, p.mtiles);
     Unit cur{};
@@ -84,7 +86,27 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
     __syncthreads();
     bool ok = true;
 
-    if (warp >= 8) {
+    if (TMA && warp == 8) {
+        // ---- copies
+        TmaFeed<C::kTile, C::kRB> feed;
+        feed.find(p, maps, cur, cur.pos < run.end);
+        uint32_t i = 0;
+        for (; cur.pos < run.end && ok; i++) {
+            const TmaFeed<C::kTile, C::kRB> now = feed;
+            const uint32_t h = cur.h, s = i % C::kStages;
+            advance(p, cur, p.mtiles);
+            feed.find(p, maps, cur, cur.pos < run.end);
+            if (i >= C::kStages) ok = warp_wait(freed + 8 * s, (i / C::kStages - 1) & 1);
+            if (!ok) break;
+            if (lane == 0) bar_expect(full + 8 * s, 2 * now.bytes(maps));
+            __syncwarp();
+            const uint32_t ks = smem_u32(smem + s * C::kStage);
+            now.copy(maps, &maps.k, h, ks, full + 8 * s);
+            now.copy(maps, &maps.v, h, ks + C::kTile * C::kRB, full + 8 * s);
+        }
+        for (uint32_t k = i > C::kStages ? i - C::kStages : 0; k < i; k++)  // no copy outlives the CTA
+            ok &= warp_wait(full + 8 * (k % C::kStages), (k / C::kStages) & 1);
+    } else if (!TMA && warp >= 8) {
         // ---- copies: a warp takes a quarter of a tile's tokens
         constexpr uint32_t kMine = C::kTile / 4, kLanes = C::kRB / 16;
         const uint32_t w = warp - 8, c = lane % kLanes, live = D * (FP8 ? 1 : 2) / 16;
@@ -110,7 +132,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
                 const uint32_t r = x * (32 / kLanes) + lane / kLanes;
                 const char* ka = reinterpret_cast<const char*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(krow), r));
                 const char* va = reinterpret_cast<const char*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(vrow), r));
-                const uint32_t dst = ks + chunk_at<C::kRB>(w * kMine + r, c);
+                const uint32_t dst = ks + row_chunk<C::kRB>(C::kTile, w * kMine + r, c);
                 if (c < live) {
                     copy16(dst, ka ? ka + c * 16 : p.cache.k, ka != nullptr);
                     copy16(dst + C::kTile * C::kRB, va ? va + c * 16 : p.cache.v, va != nullptr);
@@ -127,6 +149,8 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
         uint32_t merges = 0, first = 0;  // first: the tile with which this CTA began the unit
         bool begun = false;
         // Column of o[x][.][y]: x * 16 + g + 8 (y / 2), or with the even and odd columns apart.
+        // The address 32 bytes of a row further on, `i` times: blocks of 128 bytes lie a tile's rows apart.
+        auto step_of = [](uint32_t base, uint32_t i) { return (base + (i >> 2) * C::kTile * 128) ^ ((i & 3) << 5); };
         auto column = [&](int x, int y) { return x * 16 + (FP8 ? 2 * g + y / 2 : g + 8 * (y / 2)); };
 
         for (uint32_t i = 0; cur.pos < run.end && ok; i++) {
@@ -207,12 +231,12 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
                             for (int y = 0; y < 4; y++) sc[h][x][t][y] = 0.0f;
 #pragma unroll
                 for (int x = 0; x < kB; x++) {
-                    const uint32_t base = ks + chunk_at<C::kRB>(key0 + x * 16 + lane % 16, lane / 16);
+                    const uint32_t base = ks + row_chunk<C::kRB>(C::kTile, key0 + x * 16 + lane % 16, lane / 16);
                     if (!FP8) {
 #pragma unroll
                         for (int kk = 0; kk < DP / 16; kk++) {
                             uint32_t a[4];
-                            ldsm4(a, base ^ (kk << 5));
+                            ldsm4(a, step_of(base, kk));
 #pragma unroll
                             for (int t = 0; t < RN; t++) mma16816<T>(sc[kk % kChains][x][t], a, q[t][kk][0], q[t][kk][1]);
                         }
@@ -220,7 +244,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
 #pragma unroll
                         for (int kp = 0; kp < DP / 32; kp++) {
                             uint32_t r[4];
-                            ldsm4(r, base ^ (kp << 5));
+                            ldsm4(r, step_of(base, kp));
 #pragma unroll
                             for (int y = 0; y < 2; y++) {
                                 const uint32_t a[4] = {uzip::prmt(r[2 * y], 0, 0x1404), uzip::prmt(r[2 * y + 1], 0, 0x1404),
@@ -297,34 +321,40 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
                 }
                 // A value that a row does not see must not reach it through 0 * NaN: where the tile has new tokens,
                 // non-finite values are taken out of the product and added below to the rows that see them.
+                // (Rows past the last token may hold anything.)
                 uint32_t odd = 0;
 #pragma unroll
                 for (int x = 0; x < kB; x++) {
+                    uint32_t used[2] = {0, 0};  // halves of a pair of tokens 2 l, 2 l + 1 (and 8 on) that are in use
+                    if (masked) {
+                        const int32_t left = (int32_t)(cur.span.old + cur.span.fresh - (j0 + sub * C::kSub + x * 16)) - 2 * (int32_t)l;
+                        for (int y = 0; y < 2; y++) used[y] = left - 8 * y >= 2 ? 0xFFFFFFFFu : left - 8 * y == 1 ? 0xFFFFu : 0;
+                    }
                     if (!FP8) {
-                        const uint32_t base = vs + chunk_at<C::kRB>(key0 + x * 16 + (lane / 16) * 8 + lane % 8, (lane / 8) % 2);
+                        const uint32_t base = vs + row_chunk<C::kRB>(C::kTile, key0 + x * 16 + (lane / 16) * 8 + lane % 8, (lane / 8) % 2);
 #pragma unroll
                         for (int dx = 0; dx < DP / 16; dx++) {
                             uint32_t a[4];
-                            ldsm4_t(a, base ^ (dx << 5));
+                            ldsm4_t(a, step_of(base, dx));
                             if (masked)
 #pragma unroll
-                                for (int y = 0; y < 4; y++) odd |= clean2<T>(a[y]);
+                                for (int y = 0; y < 4; y++) odd |= clean2<T>(a[y]) & used[y / 2];
 #pragma unroll
                             for (int t = 0; t < RN; t++) mma16816<T>(o[dx][t], a, w[x][t][0], w[x][t][1]);
                         }
                     } else {
-                        const uint32_t base = vs + chunk_at<C::kRB>(key0 + x * 16 + ((lane / 8) % 2) * 8 + lane % 8, lane / 16);
+                        const uint32_t base = vs + row_chunk<C::kRB>(C::kTile, key0 + x * 16 + ((lane / 8) % 2) * 8 + lane % 8, lane / 16);
 #pragma unroll
                         for (int dp = 0; dp < DP / 32; dp++) {
                             uint32_t r[4];
-                            ldsm4_t(r, base ^ (dp << 5));
+                            ldsm4_t(r, step_of(base, dp));
 #pragma unroll
                             for (int y = 0; y < 2; y++) {
                                 uint32_t a[4] = {uzip::prmt(r[2 * y], 0, 0x2404), uzip::prmt(r[2 * y], 0, 0x3414),
                                                  uzip::prmt(r[2 * y + 1], 0, 0x2404), uzip::prmt(r[2 * y + 1], 0, 0x3414)};
                                 if (masked)
 #pragma unroll
-                                    for (int z = 0; z < 4; z++) odd |= clean2<T>(a[z]);
+                                    for (int z = 0; z < 4; z++) odd |= clean2<T>(a[z]) & used[z / 2];
 #pragma unroll
                                 for (int t = 0; t < RN; t++) mma16816<T>(o[2 * dp + y][t], a, w[x][t][0], w[x][t][1]);
                             }
@@ -445,47 +475,55 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
     if (!ok && p.cache.status) *p.cache.status = UZIP_ERR_TIMEOUT;
 }
 
-template <typename QT, bool FP8, int DP, int RN, int WM>
-int launch_attend_as(AttParams& p, int sms, cudaStream_t stream) {
+template <typename QT, bool FP8, int DP, int RN, int WM, bool TMA>
+int launch_attend_by(AttParams& p, const Maps& maps, cudaStream_t stream) {
     using C = AttCfg<QT, FP8, DP, RN, WM>;
     static std::atomic<uint64_t> ready{0};  // a bit for each device whose limit is raised
     int dev = 0;
     UZIP_CUDA_TRY(cudaGetDevice(&dev));
     if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
-        UZIP_CUDA_TRY(cudaFuncSetAttribute(attend_kernel<QT, FP8, DP, RN, WM>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem));
+        UZIP_CUDA_TRY(cudaFuncSetAttribute(attend_kernel<QT, FP8, DP, RN, WM, TMA>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem));
         if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
+    attend_kernel<QT, FP8, DP, RN, WM, TMA><<<p.grid, kAttThreads<TMA>, C::kSmem, stream>>>(p, maps);
+    UZIP_CUDA_TRY(cudaGetLastError());
+    return UZIP_OK;
+}
+
+template <typename QT, bool FP8, int DP, int RN, int WM>
+int launch_attend_as(AttParams& p, const uzkv_cache_t* c, int sms, cudaStream_t stream) {
+    using C = AttCfg<QT, FP8, DP, RN, WM>;
     p.m = C::kM;
     p.mtiles = (p.rows + C::kM - 1) / C::kM;
     p.dp = DP;
     p.shift = C::kTile == 128 ? 7 : 6;
     p.unit_cost = 3;
     p.grid = std::min<uint32_t>((uint32_t)sms, kMaxAttGrid);
-    attend_kernel<QT, FP8, DP, RN, WM><<<p.grid, kAttThreads, C::kSmem, stream>>>(p);
-    UZIP_CUDA_TRY(cudaGetLastError());
-    return UZIP_OK;
+    Maps maps{};
+    if (maps_of(p, c, C::kTile, &maps)) return launch_attend_by<QT, FP8, DP, RN, WM, true>(p, maps, stream);
+    return launch_attend_by<QT, FP8, DP, RN, WM, false>(p, maps, stream);
 }
 
 // Rows a CTA takes at once: the fewest of 8 (heads up to 128), 16, 32 and 64 that hold all, else 64.
 template <typename QT, bool FP8, int DP>
-int launch_attend_rows(AttParams& p, int sms, cudaStream_t s) {
+int launch_attend_rows(AttParams& p, const uzkv_cache_t* c, int sms, cudaStream_t s) {
     if constexpr (DP <= 128) {
-        if (p.rows <= 8) return launch_attend_as<QT, FP8, DP, 1, 1>(p, sms, s);
-        if (p.rows <= 16) return launch_attend_as<QT, FP8, DP, 2, 1>(p, sms, s);
-        if (p.rows <= 32) return launch_attend_as<QT, FP8, DP, 2, 2>(p, sms, s);
-        return launch_attend_as<QT, FP8, DP, 2, 4>(p, sms, s);
+        if (p.rows <= 8) return launch_attend_as<QT, FP8, DP, 1, 1>(p, c, sms, s);
+        if (p.rows <= 16) return launch_attend_as<QT, FP8, DP, 2, 1>(p, c, sms, s);
+        if (p.rows <= 32) return launch_attend_as<QT, FP8, DP, 2, 2>(p, c, sms, s);
+        return launch_attend_as<QT, FP8, DP, 2, 4>(p, c, sms, s);
     } else {  // eight rows a warp: 16 would not leave registers for the output
-        if (p.rows <= 16) return launch_attend_as<QT, FP8, DP, 1, 2>(p, sms, s);
-        if (p.rows <= 32) return launch_attend_as<QT, FP8, DP, 1, 4>(p, sms, s);
-        return launch_attend_as<QT, FP8, DP, 1, 8>(p, sms, s);
+        if (p.rows <= 16) return launch_attend_as<QT, FP8, DP, 1, 2>(p, c, sms, s);
+        if (p.rows <= 32) return launch_attend_as<QT, FP8, DP, 1, 4>(p, c, sms, s);
+        return launch_attend_as<QT, FP8, DP, 1, 8>(p, c, sms, s);
     }
 }
 
 template <typename QT, bool FP8>
-int launch_attend(AttParams& p, int sms, cudaStream_t s) {
-    if (p.cache.head_dim <= 64) return launch_attend_rows<QT, FP8, 64>(p, sms, s);
-    if (p.cache.head_dim <= 128) return launch_attend_rows<QT, FP8, 128>(p, sms, s);
-    return launch_attend_rows<QT, FP8, 256>(p, sms, s);
+int launch_attend(AttParams& p, const uzkv_cache_t* c, int sms, cudaStream_t s) {
+    if (p.cache.head_dim <= 64) return launch_attend_rows<QT, FP8, 64>(p, c, sms, s);
+    if (p.cache.head_dim <= 128) return launch_attend_rows<QT, FP8, 128>(p, c, sms, s);
+    return launch_attend_rows<QT, FP8, 256>(p, c, sms, s);
 }
 
 }  // namespace uzkv

@@ -16,9 +16,11 @@
 //   O += P V         P from tensor memory, V from shared memory as it lies in the
 //                    cache (the product's N, the head dimension, contiguous)
 //
-// Warps: 0-3 bring keys and values to a ring of operand tiles (E5M2 as bytes,
-// then widened), 4-7 and 8-11 are the streams' groups, which also load their
-// unit's queries and write its output, 12 issues the products.
+// Warps: 13 brings keys and values to a ring of operand tiles by bulk copies;
+// 0-3 widen E5M2, which lands as bytes, take non-finite values out of tiles
+// with new tokens, and do the copies where pages do not allow bulk ones; 4-7
+// and 8-11 are the streams' groups, which also load their unit's queries and
+// write its output; 12 issues the products.
 #pragma once
 
 #include <algorithm>
@@ -28,7 +30,7 @@
 
 namespace uzkv {
 
-constexpr int kManyThreads = 13 * 32;
+constexpr int kManyThreads = 14 * 32;
 constexpr uint32_t kManyTile = 128;
 
 template <typename QT, bool FP8, int DP>
@@ -37,11 +39,12 @@ struct ManyCfg {
     static constexpr uint32_t kQTile = 128 * DP * 2;                 // queries of a stream
     static constexpr uint32_t kTileBytes = kManyTile * DP * 2;       // keys or values
     static constexpr uint32_t kRawBytes = kManyTile * DP;            // their E5M2 bytes
-    static constexpr uint32_t kOther = 2560 + 256;                   // factors and statistics; barriers
+    static constexpr uint32_t kOther = 2560 + 512;                   // factors and statistics; barriers
     static constexpr uint32_t kRoom = 227 * 1024 - kOther - 2 * kQTile;
     static constexpr uint32_t kRaw = FP8 ? 4 : 0;
     static constexpr uint32_t kFit = (kRoom - kRaw * kRawBytes) / kTileBytes;
     static constexpr uint32_t kTiles = kFit > 8 ? 8 : kFit;
+    static constexpr uint32_t kRing = FP8 ? kRaw : kTiles;           // tiles on their way
     static constexpr uint32_t kSmem = kOther + 2 * kQTile + kTiles * kTileBytes + kRaw * kRawBytes;
     static_assert(kTiles >= 3, "the keys of two tiles and a tile of values");
 };
@@ -111,8 +114,9 @@ struct ManyPart {
     }
 };
 
-template <typename QT, bool FP8, int DP>
-__global__ void __launch_bounds__(kManyThreads, 1) attend_many_kernel(const __grid_constant__ AttParams p) {
+template <typename QT, bool FP8, int DP, bool TMA>
+__global__ void __launch_bounds__(kManyThreads, 1) attend_many_kernel(const __grid_constant__ AttParams p,
+                                                                     const __grid_constant__ Maps maps) {
     using C = ManyCfg<QT, FP8, DP>;
     using T = typename C::T;
     extern __shared__ __align__(1024) char smem[];
@@ -122,18 +126,21 @@ __global__ void __launch_bounds__(kManyThreads, 1) attend_many_kernel(const __gr
     float* const factor = reinterpret_cast<float*>(raws + C::kRaw * C::kRawBytes);  // [256], or [128] of shared rows ...
     float2* const stat = reinterpret_cast<float2*>(factor + 128);  // ... and then [2][128]: each stream's reference and sum
     uint64_t* const bars = reinterpret_cast<uint64_t*>(factor + 640);
-    uint32_t* const dirty = reinterpret_cast<uint32_t*>(bars + 24);  // [8]: a unit's tiles had non-finite values taken out
+    uint32_t* const dirty = reinterpret_cast<uint32_t*>(bars + 40);  // [8]: a unit's tiles had non-finite values taken out
     uint32_t* const tmem_at = dirty + 8;
     const uint32_t tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const uint32_t D = p.cache.head_dim;
     const uint32_t full = smem_u32(bars), freed = full + 8 * 8, s_full = full + 16 * 8, p_full = full + 18 * 8,
-                   q_full = full + 20 * 8, o_full = full + 21 * 8, stat_full = full + 22 * 8, unit_done = full + 23 * 8;
+                   q_full = full + 20 * 8, o_full = full + 21 * 8, stat_full = full + 22 * 8, unit_done = full + 23 * 8,
+                   landed = full + 24 * 8, raw_freed = full + 32 * 8;
 
     uzip::pdl_launch_dependents();
     if (tid == 0) {
         for (uint32_t i = 0; i < 8; i++) {
-            bar_init(full + 8 * i, 4);   // the four copying warps
-            bar_init(freed + 8 * i, 1);  // the products' commit
+            bar_init(full + 8 * i, 4);       // the four warps that bring, widen or clean; bulk copies that need none of it
+            bar_init(freed + 8 * i, 1);      // the products' commit
+            bar_init(landed + 8 * i, 1);     // bulk copies for those warps
+            bar_init(raw_freed + 8 * i, 4);  // E5M2 bytes: widened
             dirty[i] = 0;
         }
         for (uint32_t i = 0; i < 2; i++) {
@@ -147,7 +154,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) attend_many_kernel(const __gr
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 12) tc_alloc(smem_u32(tmem_at), 512);
-    if (D < DP) {  // columns past the head dimension stay zero: no copy writes them
+    if (D < DP && (FP8 || !TMA)) {  // columns past the head dimension stay zero: no copy writes them
         for (uint32_t i = tid; i < C::kTiles * C::kTileBytes / 16; i += kManyThreads) reinterpret_cast<uint4*>(tiles)[i] = make_uint4(0, 0, 0, 0);
         fence_async_smem();
     }
@@ -166,7 +173,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) attend_many_kernel(const __gr
     if (warp < 4) {
         // ---- copies: keys, then values of each tile; a warp takes 32 of its rows
         constexpr uint32_t kES = FP8 ? 1 : 2, kLanes = DP * kES / 16;  // a row's chunks
-        constexpr uint32_t kRing = FP8 ? C::kRaw : C::kTiles;
+        constexpr uint32_t kRing = C::kRing;
         const uint32_t c = lane % kLanes, live = D * kES / 16;
         Unit ahead = unit;     // tile to copy next
         uint32_t copied = 0;   // operand tiles copied: even ones are keys
@@ -177,8 +184,9 @@ __global__ void __launch_bounds__(kManyThreads, 1) attend_many_kernel(const __gr
             if (ahead.pos < run.end && j < ahead.span.old + ahead.span.fresh) pl = place_of(p.cache, ahead.b, j);
             return pl;
         };
-        at = find();
+        if (!TMA) at = find();
         auto copy = [&]() {
+            if (TMA) return;
             if (ok && ahead.pos < run.end) {
                 if (!FP8 && copied >= kRing) ok = warp_wait(freed + 8 * (copied % kRing), (copied / kRing - 1) & 1);
                 __syncwarp();
@@ -190,7 +198,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) attend_many_kernel(const __gr
                     const uint32_t r = i * (32 / kLanes) + lane / kLanes;
                     const char* src = reinterpret_cast<const char*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(row), r));
                     const uint32_t R = warp * 32 + r;
-                    const uint32_t to = FP8 ? chunk_at<DP>(R, c) : swizzled(kManyTile, R, c);
+                    const uint32_t to = FP8 ? row_chunk<DP>(kManyTile, R, c) : swizzled(kManyTile, R, c);
                     if (c < live) copy16(smem_u32(slot) + to, src ? src + c * 16 : p.cache.k, src != nullptr);
                 }
                 copied++;
@@ -203,11 +211,20 @@ __global__ void __launch_bounds__(kManyThreads, 1) attend_many_kernel(const __gr
         };
         for (uint32_t i = 0; i < kRing - 1; i++) copy();
         Unit cur = unit;
-        uint32_t sent = 0, index = 0;  // units so far
+        uint32_t sent = 0, index = 0, turns = 0;  // units so far; phases of `landed`, where only some tiles come through it
         while (cur.pos < run.end && ok) {
             const uint32_t j0 = cur.tile * kManyTile;
             for (uint32_t values = 0; values < 2 && ok; values++, sent++) {
-                copy_wait<kRing - 2>();
+                const bool clean = values && j0 + kManyTile > cur.span.old;
+                if (TMA) {
+                    if (!FP8 && !clean) continue;
+                    const uint32_t s = sent % kRing;
+                    ok = warp_wait(landed + 8 * s, FP8 ? (sent / kRing) & 1 : (turns >> s) & 1);
+                    turns ^= 1u << s;
+                    if (!ok) break;
+                } else {
+                    copy_wait<kRing - 2>();
+                }
                 char* const tile = tiles + (sent % C::kTiles) * C::kTileBytes;
                 if (FP8) {
                     // Widen this warp's rows: 16 bytes to two chunks of eight FP16.
@@ -219,29 +236,33 @@ __global__ void __launch_bounds__(kManyThreads, 1) attend_many_kernel(const __gr
 #pragma unroll 4
                         for (uint32_t x = 0; x < kLanes; x++) {
                             const uint32_t R = warp * 32 + x * (32 / kLanes) + lane / kLanes;
-                            const uint4 v = *reinterpret_cast<const uint4*>(raw + chunk_at<DP>(R, c));
+                            const uint4 v = *reinterpret_cast<const uint4*>(raw + row_chunk<DP>(kManyTile, R, c));
                             *reinterpret_cast<uint4*>(tile + swizzled(kManyTile, R, 2 * c)) =
                                 make_uint4(uzip::prmt(v.x, 0, 0x1404), uzip::prmt(v.x, 0, 0x3424), uzip::prmt(v.y, 0, 0x1404), uzip::prmt(v.y, 0, 0x3424));
                             *reinterpret_cast<uint4*>(tile + swizzled(kManyTile, R, 2 * c + 1)) =
                                 make_uint4(uzip::prmt(v.z, 0, 0x1404), uzip::prmt(v.z, 0, 0x3424), uzip::prmt(v.w, 0, 0x1404), uzip::prmt(v.w, 0, 0x3424));
                         }
                 }
-                if (values && j0 + kManyTile > cur.span.old) {
+                if (clean) {
                     // A value that a row does not see must not reach it through 0 * NaN: non-finite values of a tile
-                    // with new tokens leave it here, and the unit's end adds them to the rows that see them. Each
-                    // thread looks at the chunks it wrote.
+                    // with new tokens leave it here, and the unit's end adds them to the rows that see them. Rows past
+                    // the last token, which a bulk copy may have brought, become zeros. Each thread looks at the
+                    // chunks of its warp's rows that it wrote, or would have.
                     bool bad = false;
+                    const uint32_t end = cur.span.old + cur.span.fresh;
                     if (c < live)
                         for (uint32_t x = 0; x < kLanes; x++) {
                             const uint32_t R = warp * 32 + x * (32 / kLanes) + lane / kLanes;
                             for (uint32_t half = 0; half < (FP8 ? 2 : 1); half++) {
-                                uint32_t* w = reinterpret_cast<uint32_t*>(tile + swizzled(kManyTile, R, FP8 ? 2 * c + half : c));
-                                for (int y = 0; y < 4; y++) {
-                                    uint32_t v = w[y];
-                                    if (clean2<T>(v)) {
-                                        w[y] = v;
-                                        bad = true;
-                                    }
+                                uint4* at16 = reinterpret_cast<uint4*>(tile + swizzled(kManyTile, R, FP8 ? 2 * c + half : c));
+                                if (j0 + R >= end) {
+                                    *at16 = make_uint4(0, 0, 0, 0);
+                                    continue;
+                                }
+                                uint4 v = *at16;
+                                if (clean2<T>(v.x) | clean2<T>(v.y) | clean2<T>(v.z) | clean2<T>(v.w)) {
+                                    *at16 = v;
+                                    bad = true;
                                 }
                             }
                         }
@@ -249,14 +270,50 @@ __global__ void __launch_bounds__(kManyThreads, 1) attend_many_kernel(const __gr
                 }
                 fence_async_smem();
                 __syncwarp();
-                if (lane == 0) bar_arrive(full + 8 * (sent % C::kTiles));
+                if (lane == 0) {
+                    bar_arrive(full + 8 * (sent % C::kTiles));
+                    if (TMA && FP8) bar_arrive(raw_freed + 8 * (sent % kRing));
+                }
                 copy();
             }
             const bool to_end = cur.tile + 1 == cur.tiles;
             advance(p, cur, p.mtiles);
             if (to_end) index++;
         }
-        copy_wait<0>();
+        if (!TMA) copy_wait<0>();
+    } else if (warp == 13) {
+        // ---- bulk copies: keys, then values of each tile
+        if (TMA) {
+            using Feed = TmaFeed<kManyTile, FP8 ? DP : DP * 2>;
+            char* const ring = FP8 ? raws : tiles;
+            const uint32_t again = FP8 ? raw_freed : freed;
+            Feed feed;
+            feed.find(p, maps, unit, unit.pos < run.end);
+            uint32_t n = 0;  // operand tiles
+            while (unit.pos < run.end && ok) {
+                const Feed now = feed;
+                const uint32_t h = unit.h;
+                const bool masked = (unit.tile + 1) * kManyTile > unit.span.old;
+                advance(p, unit, p.mtiles);
+                feed.find(p, maps, unit, unit.pos < run.end);
+                for (uint32_t values = 0; values < 2 && ok; values++, n++) {
+                    const uint32_t s = n % C::kRing;
+                    if (n >= C::kRing) ok = warp_wait(again + 8 * s, (n / C::kRing - 1) & 1);
+                    if (!ok) break;
+                    const bool by = FP8 || (values && masked);  // the warps that widen or clean come first
+                    const uint32_t done = (by ? landed : full) + 8 * s;
+                    if (lane == 0) {
+                        bar_expect(done, now.bytes(maps));
+                        if (!by) bar_arrive(done, 3);
+                    }
+                    __syncwarp();
+                    now.copy(maps, values ? &maps.v : &maps.k, h, smem_u32(ring + s * (FP8 ? C::kRawBytes : C::kTileBytes)), done);
+                }
+            }
+            const uint32_t last = FP8 ? landed : full;
+            for (uint32_t k = n > C::kRing ? n - C::kRing : 0; k < n; k++)  // no copy outlives the CTA
+                ok &= warp_wait(last + 8 * (k % C::kRing), (k / C::kRing) & 1);
+        }
     } else if (warp == 12) {
         // ---- products, by one lane
         if (lane == 0) {
@@ -523,16 +580,23 @@ __global__ void __launch_bounds__(kManyThreads, 1) attend_many_kernel(const __gr
     if (warp == 12) tc_free(tmem, 512);
 }
 
-template <typename QT, bool FP8, int DP>
-int launch_many_as(AttParams& p, int sms, cudaStream_t stream) {
+template <typename QT, bool FP8, int DP, bool TMA>
+int launch_many_by(AttParams& p, const Maps& maps, cudaStream_t stream) {
     using C = ManyCfg<QT, FP8, DP>;
     static std::atomic<uint64_t> ready{0};  // a bit for each device whose limit is raised
     int dev = 0;
     UZIP_CUDA_TRY(cudaGetDevice(&dev));
     if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
-        UZIP_CUDA_TRY(cudaFuncSetAttribute(attend_many_kernel<QT, FP8, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem));
+        UZIP_CUDA_TRY(cudaFuncSetAttribute(attend_many_kernel<QT, FP8, DP, TMA>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem));
         if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
+    attend_many_kernel<QT, FP8, DP, TMA><<<p.grid, kManyThreads, C::kSmem, stream>>>(p, maps);
+    UZIP_CUDA_TRY(cudaGetLastError());
+    return UZIP_OK;
+}
+
+template <typename QT, bool FP8, int DP>
+int launch_many_as(AttParams& p, const uzkv_cache_t* c, int sms, cudaStream_t stream) {
     p.m = p.rows <= 128 ? 128 : 256;
     p.mtiles = (p.rows + p.m - 1) / p.m;
     p.dp = DP;
@@ -540,14 +604,14 @@ int launch_many_as(AttParams& p, int sms, cudaStream_t stream) {
     static_assert(kManyTile == 1u << 7, "tile");
     p.unit_cost = 5;
     p.grid = std::min<uint32_t>((uint32_t)sms, kMaxAttGrid);
-    attend_many_kernel<QT, FP8, DP><<<p.grid, kManyThreads, C::kSmem, stream>>>(p);
-    UZIP_CUDA_TRY(cudaGetLastError());
-    return UZIP_OK;
+    Maps maps{};
+    if (maps_of(p, c, kManyTile, &maps)) return launch_many_by<QT, FP8, DP, true>(p, maps, stream);
+    return launch_many_by<QT, FP8, DP, false>(p, maps, stream);
 }
 
 template <typename QT, bool FP8>
-int launch_many(AttParams& p, int sms, cudaStream_t s) {
-    return p.cache.head_dim <= 64 ? launch_many_as<QT, FP8, 64>(p, sms, s) : launch_many_as<QT, FP8, 128>(p, sms, s);
+int launch_many(AttParams& p, const uzkv_cache_t* c, int sms, cudaStream_t s) {
+    return p.cache.head_dim <= 64 ? launch_many_as<QT, FP8, 64>(p, c, sms, s) : launch_many_as<QT, FP8, 128>(p, c, sms, s);
 }
 
 }  // namespace uzkv

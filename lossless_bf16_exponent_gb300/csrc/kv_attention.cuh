@@ -6,10 +6,6 @@
 // are rows of one product: row r is token r / group, head r % group, so a
 // cached row is read once for all of them.
 //
-// Shared-memory rows are 64, 128, 256 or 512 bytes, in 16-byte chunks whose
-// number is XORed with the row's, so that the eight rows that a matrix load
-// takes at one chunk lie in eight different bank groups.
-//
 // E5M2 rows stay bytes in shared memory. E5M2 is the upper byte of FP16, so a
 // byte permute widens two of them to a pair that the FP16 product takes.
 #pragma once
@@ -257,6 +253,9 @@ __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
 __device__ __forceinline__ void bar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+__device__ __forceinline__ void bar_arrive(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
 // Waits for the phase of the given parity to end. Bounded: false after about a second, which only a fault in the
 // kernel's own counting could bring about; the caller then leaves its loop.
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
@@ -288,11 +287,13 @@ __device__ __forceinline__ uint32_t clean2(uint32_t& v) {
     return bad;
 }
 
-// Byte offset of 16-byte chunk c of a row in a shared-memory tile of RB-byte rows.
+// Byte offset of 16-byte chunk c of row r in a shared-memory tile of `rows` rows of RB bytes: blocks of 128 bytes a
+// row one after the other (or the 64 that a row has), chunks XORed with the row so that the eight rows of a matrix
+// load lie in eight bank groups. This is the accelerator's own 128-byte (64-byte) swizzle, and the tensor core's.
 template <int RB>
-__device__ __forceinline__ uint32_t chunk_at(uint32_t row, uint32_t c) {
+__device__ __forceinline__ uint32_t row_chunk(uint32_t rows, uint32_t r, uint32_t c) {
     static_assert(RB == 64 || RB == 128 || RB == 256 || RB == 512, "row bytes");
-    return row * RB + ((c ^ (RB >= 128 ? row & 7 : (row >> 1) & 3)) << 4);
+    return RB == 64 ? r * 64 + ((c ^ ((r >> 1) & 3)) << 4) : (c >> 3) * rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
 // Weights go to the 16-bit product as exp2(x - reference), and the reference may trail the running maximum by
@@ -316,56 +317,67 @@ __device__ __forceinline__ void load_queries(const AttParams& p, uint32_t tid, u
     constexpr bool kCast = !std::is_same<QT, T>::value;
     constexpr uint32_t kChunks = DP / 8;  // a power of two, at most 32
     const uint32_t c = tid % kChunks, live = p.cache.head_dim / 8;
-    for (uint32_t i = tid / kChunks; i < rows; i += THREADS / kChunks) {
-        const uint32_t row = row0 + i;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (row < p.rows && c < live) {
-            const uint32_t t = row / p.group, g = row - t * p.group;
-            x = *reinterpret_cast<const uint4*>(p.q.p + b * p.q.b + t * p.q.t + (uint64_t)(h * p.group + g) * p.q.h + c * 16);
-        }
-        float f = fabsf(p.scale) * kLog2e;
-        if (kCast) {
-            const QT* e = reinterpret_cast<const QT*>(&x);
-            float v[8], top = 0.0f;
+    constexpr int kBatch = 4;  // rows on their way at once
+    constexpr uint32_t kStep = THREADS / kChunks;
+    for (uint32_t i0 = tid / kChunks; i0 < rows; i0 += kStep * kBatch) {
+        uint4 in[kBatch];
 #pragma unroll
-            for (int k = 0; k < 8; k++) {
-                v[k] = to_f32(e[k]);
-                top = fmaxf(top, fabsf(v[k]));
+        for (int k = 0; k < kBatch; k++) {
+            const uint32_t row = row0 + i0 + k * kStep;
+            in[k] = make_uint4(0, 0, 0, 0);
+            if (i0 + k * kStep < rows && row < p.rows && c < live) {
+                const uint32_t t = row / p.group, g = row - t * p.group;
+                in[k] = *reinterpret_cast<const uint4*>(p.q.p + b * p.q.b + t * p.q.t + (uint64_t)(h * p.group + g) * p.q.h + c * 16);
             }
-            // rows is a multiple of 16 and so of what a pass takes: no lane of a warp has left the loop
-            for (uint32_t o = kChunks / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-            // 2^-e as a float with e the exponent of top; 1 for a row of zeros, subnormals or with an infinity
-            const uint32_t ex = __float_as_uint(top) >> 23;
-            const bool plain = ex > 0 && ex < 254;
-            const float down = plain ? __uint_as_float((254 - ex) << 23) : 1.0f;
-            f *= plain ? __uint_as_float(ex << 23) : 1.0f;
-            uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+        }
 #pragma unroll
-            for (int k = 0; k < 4; k++) w[k] = pack2<__half>(v[2 * k] * down, v[2 * k + 1] * down);
+        for (int k = 0; k < kBatch; k++) {
+            const uint32_t i = i0 + k * kStep;
+            if (i >= rows) break;  // rows is a multiple of 16 and so of what a pass takes: all lanes of a warp alike
+            uint4 x = in[k];
+            float f = fabsf(p.scale) * kLog2e;
+            if (kCast) {
+                const QT* e = reinterpret_cast<const QT*>(&x);
+                float v[8], top = 0.0f;
+#pragma unroll
+                for (int y = 0; y < 8; y++) {
+                    v[y] = to_f32(e[y]);
+                    top = fmaxf(top, fabsf(v[y]));
+                }
+                for (uint32_t o = kChunks / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+                // 2^-e as a float with e the exponent of top; 1 for a row of zeros, subnormals or with an infinity
+                const uint32_t ex = __float_as_uint(top) >> 23;
+                const bool plain = ex > 0 && ex < 254;
+                const float down = plain ? __uint_as_float((254 - ex) << 23) : 1.0f;
+                f *= plain ? __uint_as_float(ex << 23) : 1.0f;
+                uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+                for (int y = 0; y < 4; y++) w[y] = pack2<__half>(v[2 * y] * down, v[2 * y + 1] * down);
+            }
+            if (p.scale < 0.0f) {
+                x.x ^= 0x80008000u;
+                x.y ^= 0x80008000u;
+                x.z ^= 0x80008000u;
+                x.w ^= 0x80008000u;
+            }
+            *at(i, c) = x;
+            if (c == 0) factor[i] = f;
         }
-        if (p.scale < 0.0f) {
-            x.x ^= 0x80008000u;
-            x.y ^= 0x80008000u;
-            x.z ^= 0x80008000u;
-            x.w ^= 0x80008000u;
-        }
-        *at(i, c) = x;
-        if (c == 0) factor[i] = f;
     }
 }
 
 // Attention kernels by types, one translation unit each; they set p.m, p.mtiles, p.dp and p.grid.
-int attend_bf16(AttParams& p, int sms, cudaStream_t s);
-int attend_bf16_e5m2(AttParams& p, int sms, cudaStream_t s);
-int attend_fp16(AttParams& p, int sms, cudaStream_t s);
-int attend_fp16_e5m2(AttParams& p, int sms, cudaStream_t s);
-int attend_many_bf16(AttParams& p, int sms, cudaStream_t s);  // more rows, heads up to 128
-int attend_many_bf16_e5m2(AttParams& p, int sms, cudaStream_t s);
-int attend_many_fp16(AttParams& p, int sms, cudaStream_t s);
-int attend_many_fp16_e5m2(AttParams& p, int sms, cudaStream_t s);
-int mass_bf16(AttParams& p, int sms, cudaStream_t s);
-int mass_bf16_e5m2(AttParams& p, int sms, cudaStream_t s);
-int mass_fp16(AttParams& p, int sms, cudaStream_t s);
-int mass_fp16_e5m2(AttParams& p, int sms, cudaStream_t s);
+int attend_bf16(AttParams& p, const uzkv_cache_t* c, int sms, cudaStream_t s);
+int attend_bf16_e5m2(AttParams& p, const uzkv_cache_t* c, int sms, cudaStream_t s);
+int attend_fp16(AttParams& p, const uzkv_cache_t* c, int sms, cudaStream_t s);
+int attend_fp16_e5m2(AttParams& p, const uzkv_cache_t* c, int sms, cudaStream_t s);
+int attend_many_bf16(AttParams& p, const uzkv_cache_t* c, int sms, cudaStream_t s);  // more rows, heads up to 128
+int attend_many_bf16_e5m2(AttParams& p, const uzkv_cache_t* c, int sms, cudaStream_t s);
+int attend_many_fp16(AttParams& p, const uzkv_cache_t* c, int sms, cudaStream_t s);
+int attend_many_fp16_e5m2(AttParams& p, const uzkv_cache_t* c, int sms, cudaStream_t s);
+int mass_bf16(AttParams& p, const uzkv_cache_t* c, int sms, cudaStream_t s);
+int mass_bf16_e5m2(AttParams& p, const uzkv_cache_t* c, int sms, cudaStream_t s);
+int mass_fp16(AttParams& p, const uzkv_cache_t* c, int sms, cudaStream_t s);
+int mass_fp16_e5m2(AttParams& p, const uzkv_cache_t* c, int sms, cudaStream_t s);
 
 }  // namespace uzkv

@@ -8,12 +8,12 @@
 // is a token and the sum over rows stays within a thread, in one fixed order.
 // Any number of rows costs only its own columns (a multiple of 16).
 //
-// One CTA an SM takes a run of tiles (kv_attention.cuh's split). Its warps:
-// 0-3 bring keys to a ring of operand tiles (16-byte asynchronous copies; E5M2
-// keys land as bytes and are widened to FP16 tiles), and the rows' queries and
-// factors once a unit; 12 issues the products into two buffers of tensor
-// memory; 4-7 and 8-11 take turns at the tiles, sum, add the decayed old mass
-// and store. More than 256 rows (128 for heads above 128) go in chunks: the
+// One CTA an SM takes a run of tiles (kv_attention.cuh's split). Its warps: 13
+// brings keys to a ring of operand tiles by bulk copies; 0-3 load the rows'
+// queries and factors once a unit, widen E5M2 keys, which land as bytes, to
+// FP16 tiles, and do the copies where pages do not allow bulk ones; 12 issues
+// the products into two buffers of tensor memory; 4-7 and 8-11 take turns at
+// the tiles, sum, add the decayed old mass and store. More than 256 rows (128 for heads above 128) go in chunks: the
 // CTA passes over its tiles of the unit once a chunk, adding to what the same
 // thread stored before.
 #pragma once
@@ -25,7 +25,7 @@
 
 namespace uzkv {
 
-constexpr int kMassThreads = 13 * 32;
+constexpr int kMassThreads = 14 * 32;
 constexpr uint32_t kMassTile = 128;
 
 template <typename QT, bool FP8, int DP>
@@ -40,6 +40,7 @@ struct MassCfg {
     static constexpr uint32_t kFit = (kRoom - kQBytes) / kTileBytes;
     static constexpr uint32_t kTiles = FP8 ? (DP <= 128 ? 2 : 1) : (kFit > 8 ? 8 : kFit);
     static constexpr uint32_t kRaw = FP8 ? (DP <= 128 ? 4 : 2) : 0;
+    static constexpr uint32_t kRing = FP8 ? kRaw : kTiles;            // tiles on their way
     static constexpr uint32_t kSmem = kQBytes + kTiles * kTileBytes + kRaw * kRawBytes + 8192;
     static_assert(kSmem <= 227 * 1024, "shared memory");
     static_assert(kTiles >= 1, "operand tiles");
@@ -67,8 +68,8 @@ struct MassWalk {
     __device__ __forceinline__ uint32_t turn(uint32_t i) const { return (i + units) & 1; }
 };
 
-template <typename QT, bool FP8, int DP>
-__global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const __grid_constant__ AttParams p) {
+template <typename QT, bool FP8, int DP, bool TMA>
+__global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const __grid_constant__ AttParams p, const __grid_constant__ Maps maps) {
     using C = MassCfg<QT, FP8, DP>;
     using T = typename C::T;
     extern __shared__ __align__(1024) char smem[];
@@ -77,19 +78,21 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const __grid_cons
     char* const raws = tiles + C::kTiles * C::kTileBytes;
     float* const rowf = reinterpret_cast<float*>(raws + C::kRaw * C::kRawBytes);  // [2][2][256]: factors; exponents, negative
     uint64_t* const bars = reinterpret_cast<uint64_t*>(rowf + 1024);
-    uint32_t* const tmem_at = reinterpret_cast<uint32_t*>(bars + 32);
+    uint32_t* const tmem_at = reinterpret_cast<uint32_t*>(bars + 40);
     const uint32_t tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const uint32_t D = p.cache.head_dim, N = p.m;
     const uint32_t qbuf = 2 * N * DP * 2 <= C::kQBytes ? 2 : 1;  // queries of two units at once where they fit
     const uint32_t full = smem_u32(bars), freed = full + 8 * 8, q_full = full + 16 * 8, q_freed = full + 18 * 8,
-                   s_full = full + 20 * 8, s_freed = full + 22 * 8;
+                   s_full = full + 20 * 8, s_freed = full + 22 * 8, landed = full + 24 * 8, raw_freed = full + 32 * 8;
     uint32_t columns = 32;
     while (columns < 2 * N) columns *= 2;
 
     if (tid == 0) {
         for (uint32_t i = 0; i < 8; i++) {
-            bar_init(full + 8 * i, 4);   // the four copying warps
-            bar_init(freed + 8 * i, 1);  // the products' commit
+            bar_init(full + 8 * i, TMA && !FP8 ? 1 : 4);  // the bulk copies, or the four warps that bring or widen
+            bar_init(freed + 8 * i, 1);                   // the products' commit
+            bar_init(landed + 8 * i, 1);                  // E5M2 bytes: the bulk copies
+            bar_init(raw_freed + 8 * i, 4);               // ... and the four warps that widen
         }
         for (uint32_t i = 0; i < 2; i++) {
             bar_init(q_full + 8 * i, 4);
@@ -100,7 +103,7 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const __grid_cons
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 12) tc_alloc(smem_u32(tmem_at), columns);
-    if (D < DP) {  // columns past the head dimension stay zero: no copy writes them
+    if (D < DP && (FP8 || !TMA)) {  // columns past the head dimension stay zero: no copy writes them
         for (uint32_t i = tid; i < C::kTiles * C::kTileBytes / 16; i += kMassThreads) reinterpret_cast<uint4*>(tiles)[i] = make_uint4(0, 0, 0, 0);
         fence_async_smem();
     }
@@ -119,11 +122,12 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const __grid_cons
     if (warp < 4) {
         // ---- copies
         constexpr uint32_t kES = FP8 ? 1 : 2, kLanes = DP * kES / 16;  // a row's chunks
-        constexpr uint32_t kRing = FP8 ? C::kRaw : C::kTiles;
+        constexpr uint32_t kRing = C::kRing;
         const uint32_t c = lane % kLanes, live = D * kES / 16;
         MassWalk cw(first, run.end);        // of the next tile to copy
         uint32_t cs = 0, copied = 0;  // its place in the run, and how many are copied
         auto copy = [&]() {
+            if (TMA) return;
             if (ok && cw.valid()) {
                 // A warp takes 32 of the tile's rows: each lane finds one, then the warp copies them row by row.
                 if (!FP8 && copied >= kRing) ok = warp_wait(freed + 8 * (copied % kRing), (copied / kRing - 1) & 1);
@@ -140,7 +144,7 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const __grid_cons
                     const uint32_t r = i * (32 / kLanes) + lane / kLanes;
                     const char* src = reinterpret_cast<const char*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(row), r));
                     const uint32_t R = warp * 32 + r;
-                    const uint32_t at = FP8 ? chunk_at<DP>(R, c) : swizzled(kMassTile, R, c);
+                    const uint32_t at = FP8 ? row_chunk<DP>(kMassTile, R, c) : swizzled(kMassTile, R, c);
                     if (c < live) copy16(smem_u32(slot) + at, src ? src + c * 16 : p.cache.k, src != nullptr);
                 }
                 copied++;
@@ -177,8 +181,10 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const __grid_cons
             fence_async_smem();
             __syncwarp();
             if (lane == 0) bar_arrive(q_full + 8 * (seg % 2));
-            for (uint32_t i = 0; i < w.count && ok; i++, sent++) {
-                copy_wait<kRing - 2>();
+            for (uint32_t i = 0; i < w.count && ok && (FP8 || !TMA); i++, sent++) {
+                if (TMA) ok = warp_wait(landed + 8 * (sent % C::kRing), (sent / C::kRing) & 1);
+                else copy_wait<kRing - 2>();
+                if (!ok) break;
                 if (FP8) {
                     // Widen this warp's rows of the tile: 16 bytes to two chunks of eight FP16.
                     if (sent >= C::kTiles) ok = warp_wait(freed + 8 * (sent % C::kTiles), (sent / C::kTiles - 1) & 1);
@@ -189,7 +195,7 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const __grid_cons
 #pragma unroll 4
                         for (uint32_t x = 0; x < kLanes; x++) {
                             const uint32_t R = warp * 32 + x * (32 / kLanes) + lane / kLanes;
-                            const uint4 v = *reinterpret_cast<const uint4*>(raw + chunk_at<DP>(R, c));
+                            const uint4 v = *reinterpret_cast<const uint4*>(raw + row_chunk<DP>(kMassTile, R, c));
                             *reinterpret_cast<uint4*>(tile + swizzled(kMassTile, R, 2 * c)) =
                                 make_uint4(uzip::prmt(v.x, 0, 0x1404), uzip::prmt(v.x, 0, 0x3424), uzip::prmt(v.y, 0, 0x1404), uzip::prmt(v.y, 0, 0x3424));
                             *reinterpret_cast<uint4*>(tile + swizzled(kMassTile, R, 2 * c + 1)) =
@@ -198,11 +204,46 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const __grid_cons
                 }
                 fence_async_smem();
                 __syncwarp();
-                if (lane == 0) bar_arrive(full + 8 * (sent % C::kTiles));
+                if (lane == 0) {
+                    bar_arrive(full + 8 * (sent % C::kTiles));
+                    if (TMA) bar_arrive(raw_freed + 8 * (sent % C::kRing));
+                }
                 copy();
             }
         }
-        copy_wait<0>();
+        if (!TMA) copy_wait<0>();
+    } else if (warp == 13) {
+        // ---- bulk copies
+        if (TMA) {
+            using Feed = TmaFeed<kMassTile, FP8 ? DP : DP * 2>;
+            char* const ring = FP8 ? raws : tiles;
+            const uint32_t done = FP8 ? landed : full, again = FP8 ? raw_freed : freed;
+            MassWalk w(first, run.end);
+            Unit u = first;
+            Feed feed;
+            feed.find(p, maps, u, w.valid());
+            uint32_t i = 0, at = 0;  // tile of the run, and of its unit's part
+            while (w.valid() && ok) {
+                const Feed now = feed;
+                const uint32_t h = u.h, s = i % C::kRing;
+                if (++at == w.count) {
+                    at = 0;
+                    w.next(p);
+                    u = w.u;
+                } else {
+                    u.tile++;
+                }
+                feed.find(p, maps, u, w.valid());
+                if (i >= C::kRing) ok = warp_wait(again + 8 * s, (i / C::kRing - 1) & 1);
+                if (!ok) break;
+                if (lane == 0) bar_expect(done + 8 * s, now.bytes(maps));
+                __syncwarp();
+                now.copy(maps, &maps.k, h, smem_u32(ring + s * (FP8 ? C::kRawBytes : C::kTileBytes)), done + 8 * s);
+                i++;
+            }
+            for (uint32_t k = i > C::kRing ? i - C::kRing : 0; k < i; k++)  // no copy outlives the CTA
+                ok &= warp_wait(done + 8 * (k % C::kRing), (k / C::kRing) & 1);
+        }
     } else if (warp == 12) {
         // ---- products, by one lane
         if (lane == 0) {
@@ -336,16 +377,24 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const __grid_cons
     if (warp == 12) tc_free(tmem, columns);
 }
 
-template <typename QT, bool FP8, int DP>
-int launch_mass_as(AttParams& p, int sms, cudaStream_t stream) {
+template <typename QT, bool FP8, int DP, bool TMA>
+int launch_mass_by(AttParams& p, const Maps& maps, cudaStream_t stream) {
     using C = MassCfg<QT, FP8, DP>;
     static std::atomic<uint64_t> ready{0};  // a bit for each device whose limit is raised
     int dev = 0;
     UZIP_CUDA_TRY(cudaGetDevice(&dev));
     if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
-        UZIP_CUDA_TRY(cudaFuncSetAttribute(mass_kernel<QT, FP8, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem));
+        UZIP_CUDA_TRY(cudaFuncSetAttribute(mass_kernel<QT, FP8, DP, TMA>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem));
         if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
+    mass_kernel<QT, FP8, DP, TMA><<<p.grid, kMassThreads, C::kSmem, stream>>>(p, maps);
+    UZIP_CUDA_TRY(cudaGetLastError());
+    return UZIP_OK;
+}
+
+template <typename QT, bool FP8, int DP>
+int launch_mass_as(AttParams& p, const uzkv_cache_t* c, int sms, cudaStream_t stream) {
+    using C = MassCfg<QT, FP8, DP>;
     const uint32_t chunks = (p.rows + C::kMaxN - 1) / C::kMaxN;
     p.mtiles = chunks;
     p.m = ((p.rows + chunks - 1) / chunks + 15) / 16 * 16;
@@ -353,16 +402,16 @@ int launch_mass_as(AttParams& p, int sms, cudaStream_t stream) {
     p.unit_cost = 3;
     static_assert(kMassTile == 1u << 7, "tile");
     p.grid = (uint32_t)sms;
-    mass_kernel<QT, FP8, DP><<<p.grid, kMassThreads, C::kSmem, stream>>>(p);
-    UZIP_CUDA_TRY(cudaGetLastError());
-    return UZIP_OK;
+    Maps maps{};
+    if (maps_of(p, c, kMassTile, &maps)) return launch_mass_by<QT, FP8, DP, true>(p, maps, stream);
+    return launch_mass_by<QT, FP8, DP, false>(p, maps, stream);
 }
 
 template <typename QT, bool FP8>
-int launch_mass(AttParams& p, int sms, cudaStream_t s) {
-    if (p.cache.head_dim <= 64) return launch_mass_as<QT, FP8, 64>(p, sms, s);
-    if (p.cache.head_dim <= 128) return launch_mass_as<QT, FP8, 128>(p, sms, s);
-    return launch_mass_as<QT, FP8, 256>(p, sms, s);
+int launch_mass(AttParams& p, const uzkv_cache_t* c, int sms, cudaStream_t s) {
+    if (p.cache.head_dim <= 64) return launch_mass_as<QT, FP8, 64>(p, c, sms, s);
+    if (p.cache.head_dim <= 128) return launch_mass_as<QT, FP8, 128>(p, c, sms, s);
+    return launch_mass_as<QT, FP8, 256>(p, c, sms, s);
 }
 
 }  // namespace uzkv

@@ -7,13 +7,11 @@
 // repeats every 8 rows = 1024 bytes. Tiles start on 1024-byte boundaries.
 #pragma once
 
-#include "kv_attention.cuh"
+#include "kv_tma.cuh"
 
 namespace uzkv {
 
-__device__ __forceinline__ uint32_t swizzled(uint32_t rows, uint32_t r, uint32_t c) {
-    return (c >> 3) * rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-}
+__device__ __forceinline__ uint32_t swizzled(uint32_t rows, uint32_t r, uint32_t c) { return row_chunk<128>(rows, r, c); }
 
 // Descriptor of an operand tile at a shared-memory address: stride between groups of 8 rows 1024 bytes,
 // 128-byte swizzle; rows are along the product's M or N and elements along its K.
