@@ -500,7 +500,7 @@ int launch_attend_as(AttParams& p, const uzkv_cache_t* c, int sms, cudaStream_t 
     p.unit_cost = 3;
     p.grid = std::min<uint32_t>((uint32_t)sms, kMaxAttGrid);
     Maps maps{};
-    if (maps_of(p, c, C::kTile, &maps)) return launch_attend_by<QT, FP8, DP, RN, WM, true>(p, maps, stream);
+    if (maps_of(p, c, C::kTile, 4096, &maps)) return launch_attend_by<QT, FP8, DP, RN, WM, true>(p, maps, stream);
     return launch_attend_by<QT, FP8, DP, RN, WM, false>(p, maps, stream);
 }
 

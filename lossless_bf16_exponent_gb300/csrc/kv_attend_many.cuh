@@ -55,17 +55,6 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, ui
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
         : "memory");
 }
-__device__ __forceinline__ void tc_ld32(uint32_t* r, uint32_t addr) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,"
-        "%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
-          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
-          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(addr)
-        : "memory");
-}
 __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t* r) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
@@ -319,6 +308,9 @@ __global__ void __launch_bounds__(kManyThreads, 1) attend_many_kernel(const __gr
         if (lane == 0) {
             const uint32_t n = (D + 15) / 16 * 16;  // columns of the output
             const uint32_t iqk = mma_desc<T>(128, kManyTile), ipv = mma_desc<T>(128, n) | 1u << 16;  // V: N contiguous
+            // Descriptors once; offsets add to their low bits.
+            const uint64_t q_desc = tile_desc(smem_u32(qs)), k_desc = tile_desc(smem_u32(tiles)),
+                           v_desc = rows_desc(smem_u32(tiles), kManyTile * 128);
             uint32_t base = 0, index = 0, weights[2] = {0, 0};  // operand tiles of earlier units; units; jobs of each stream
             while (unit.pos < run.end && ok) {
                 const ManyPart part(p, unit, run.end);
@@ -328,10 +320,9 @@ __global__ void __launch_bounds__(kManyThreads, 1) attend_many_kernel(const __gr
                     if (!part.both || !x) ok = bar_wait(full + 8 * s, (t / C::kTiles) & 1);
                     if (!ok) return;
                     tc_fence_after();
-                    const uint32_t q = smem_u32(qs) + (part.both ? x * C::kQTile : 0), k = smem_u32(tiles) + s * C::kTileBytes;
-                    for (uint32_t i = 0; i < n / 16; i++)
-                        tc_mma(tmem + x * 256, tile_desc(q + (i >> 2) * 128 * 128 + (i & 3) * 32),
-                               tile_desc(k + (i >> 2) * kManyTile * 128 + (i & 3) * 32), iqk, i != 0);
+                    const uint64_t q = q_desc + (part.both ? x * (C::kQTile >> 4) : 0), k = k_desc + s * (C::kTileBytes >> 4);
+                    if (D > DP * 3 / 4) tc_mma_steps<DP / 16>(tmem + x * 256, q, 128 * 128 >> 4, k, kManyTile * 128 >> 4, iqk);
+                    else tc_mma_steps<DP * 3 / 64>(tmem + x * 256, q, 128 * 128 >> 4, k, kManyTile * 128 >> 4, iqk);
                     tc_commit(s_full + 8 * x);
                     if (!part.both || x) tc_commit(freed + 8 * s);
                 };
@@ -345,10 +336,10 @@ __global__ void __launch_bounds__(kManyThreads, 1) attend_many_kernel(const __gr
                     if (ok) ok = bar_wait(p_full + 8 * x, done & 1);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t v = smem_u32(tiles) + s * C::kTileBytes;
+                    const uint64_t v = v_desc + s * (C::kTileBytes >> 4);
+#pragma unroll
                     for (uint32_t i = 0; i < kManyTile / 16; i++)
-                        tc_mma_ts(tmem + x * 256 + 128, tmem + x * 256 + i * 8, rows_desc(v + i * 2048, kManyTile * 128), ipv,
-                                  j > 1 || i != 0);
+                        tc_mma_ts(tmem + x * 256 + 128, tmem + x * 256 + i * 8, v + i * (2048 >> 4), ipv, j > 1 || i != 0);
                     if (!part.both || x) tc_commit(freed + 8 * s);
                     if (j + 2 < jobs) score(j + 2);
                 }
@@ -605,7 +596,7 @@ int launch_many_as(AttParams& p, const uzkv_cache_t* c, int sms, cudaStream_t st
     p.unit_cost = 5;
     p.grid = std::min<uint32_t>((uint32_t)sms, kMaxAttGrid);
     Maps maps{};
-    if (maps_of(p, c, kManyTile, &maps)) return launch_many_by<QT, FP8, DP, true>(p, maps, stream);
+    if (maps_of(p, c, kManyTile, 2048, &maps)) return launch_many_by<QT, FP8, DP, true>(p, maps, stream);
     return launch_many_by<QT, FP8, DP, false>(p, maps, stream);
 }
 

@@ -247,21 +247,21 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const __grid_cons
     } else if (warp == 12) {
         // ---- products, by one lane
         if (lane == 0) {
-            const uint32_t idesc = mma_desc<T>(kMassTile, N), steps = (D + 15) / 16;
+            const uint32_t idesc = mma_desc<T>(kMassTile, N), q_block = N * 128 >> 4;
+            const uint64_t tiles_desc = tile_desc(smem_u32(tiles));
             uint32_t seg = 0, k = 0, uses[2] = {0, 0};
             for (MassWalk w(first, run.end); w.valid() && ok; w.next(p), seg++) {
                 ok = bar_wait(q_full + 8 * (seg % 2), (seg / 2) & 1);
-                const uint32_t q = smem_u32(qs) + seg % qbuf * N * DP * 2;
+                const uint64_t q_desc = tile_desc(smem_u32(qs) + seg % qbuf * N * DP * 2);  // offsets add to its low bits
                 for (uint32_t i = 0; i < w.count && ok; i++, k++) {
                     const uint32_t s = k % C::kTiles, side = w.turn(i), used = side ? uses[1]++ : uses[0]++;
                     ok = bar_wait(full + 8 * s, (k / C::kTiles) & 1);
                     if (ok && used) ok = bar_wait(s_freed + 8 * side, (used - 1) & 1);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t a = smem_u32(tiles) + s * C::kTileBytes;
-                    for (uint32_t x = 0; x < steps; x++)
-                        tc_mma(tmem + side * N, tile_desc(a + (x >> 2) * kMassTile * 128 + (x & 3) * 32),
-                               tile_desc(q + (x >> 2) * N * 128 + (x & 3) * 32), idesc, x != 0);
+                    const uint64_t a = tiles_desc + s * (C::kTileBytes >> 4);
+                    if (D > DP * 3 / 4) tc_mma_steps<DP / 16>(tmem + side * N, a, kMassTile * 128 >> 4, q_desc, q_block, idesc);
+                    else tc_mma_steps<DP * 3 / 64>(tmem + side * N, a, kMassTile * 128 >> 4, q_desc, q_block, idesc);
                     tc_commit(freed + 8 * s);
                     tc_commit(s_full + 8 * side);
                 }
@@ -288,32 +288,41 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const __grid_cons
                 float acc = 0.0f;
                 bool guard = j0 + kMassTile > sp.old;
                 if (!guard) {
-                    // 16 columns at a time, the next ones on their way meanwhile.
-                    float v[2][16];
-                    uint64_t part[2] = {0, 0};
-                    tc_ld16(v[0], at);
-                    auto columns = [&](const float* x, uint32_t c0) {
+                    // 32 columns at a time, the next ones on their way meanwhile.
+                    uint32_t v[2][32];
+                    uint64_t part[4] = {0, 0, 0, 0};
+                    const uint64_t f1 = pair(fabsf(p.scale) * kLog2e, fabsf(p.scale) * kLog2e);
+                    auto columns = [&](const uint32_t* x, uint32_t c0, auto count) {
 #pragma unroll
-                        for (int i = 0; i < 16; i += 4) {
+                        for (int i = 0; i < decltype(count)::value; i += 4) {
                             const ulonglong2 en = *reinterpret_cast<const ulonglong2*>(e + c0 + i);
-                            ulonglong2 fn = make_ulonglong2(pair(fabsf(p.scale) * kLog2e, fabsf(p.scale) * kLog2e), 0);
-                            fn.y = fn.x;
+                            ulonglong2 fn = make_ulonglong2(f1, f1);
                             if (FP8) fn = *reinterpret_cast<const ulonglong2*>(f + c0 + i);  // rows have their own powers of two
-                            const float2 a = unpair(fma2(pair(x[i], x[i + 1]), fn.x, en.x)), b = unpair(fma2(pair(x[i + 2], x[i + 3]), fn.y, en.y));
-                            part[0] = add2(part[0], pair(exp2_fast(a.x), exp2_fast(a.y)));
-                            part[1] = add2(part[1], pair(exp2_fast(b.x), exp2_fast(b.y)));
+                            const float2 a = unpair(fma2(pair(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), fn.x, en.x));
+                            const float2 b = unpair(fma2(pair(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), fn.y, en.y));
+                            part[i / 2 % 4] = add2(part[i / 2 % 4], pair(exp2_fast(a.x), exp2_fast(a.y)));
+                            part[i / 2 % 4 + 1] = add2(part[i / 2 % 4 + 1], pair(exp2_fast(b.x), exp2_fast(b.y)));
                         }
                     };
-                    for (uint32_t c0 = 0; c0 < N; c0 += 32) {
+                    const uint32_t whole = N / 32 * 32;
+                    if (whole) tc_ld32(v[0], at);
+                    for (uint32_t c0 = 0; c0 < whole; c0 += 64) {
                         tc_wait_ld();
-                        if (c0 + 16 < N) tc_ld16(v[1], at + c0 + 16);
-                        columns(v[0], c0);
-                        if (c0 + 16 < N) {
+                        if (c0 + 32 < whole) tc_ld32(v[1], at + c0 + 32);
+                        columns(v[0], c0, std::integral_constant<int, 32>{});
+                        if (c0 + 32 < whole) {
                             tc_wait_ld();
-                            if (c0 + 32 < N) tc_ld16(v[0], at + c0 + 32);
-                            columns(v[1], c0 + 16);
+                            if (c0 + 64 < whole) tc_ld32(v[0], at + c0 + 64);
+                            columns(v[1], c0 + 32, std::integral_constant<int, 32>{});
                         }
                     }
+                    if (whole < N) {
+                        tc_ld16(reinterpret_cast<float*>(v[0]), at + whole);
+                        tc_wait_ld();
+                        columns(v[0], whole, std::integral_constant<int, 16>{});
+                    }
+                    part[0] = add2(part[0], part[2]);
+                    part[1] = add2(part[1], part[3]);
                     const float2 sum = unpair(add2(part[0], part[1]));
                     acc = sum.x + sum.y;
                     // A key that is not finite makes NaN of rows that add nothing too: take those rows out.
@@ -403,7 +412,7 @@ int launch_mass_as(AttParams& p, const uzkv_cache_t* c, int sms, cudaStream_t st
     static_assert(kMassTile == 1u << 7, "tile");
     p.grid = (uint32_t)sms;
     Maps maps{};
-    if (maps_of(p, c, kMassTile, &maps)) return launch_mass_by<QT, FP8, DP, true>(p, maps, stream);
+    if (maps_of(p, c, kMassTile, 2048, &maps)) return launch_mass_by<QT, FP8, DP, true>(p, maps, stream);
     return launch_mass_by<QT, FP8, DP, false>(p, maps, stream);
 }
 

@@ -32,6 +32,13 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint3
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
         : "memory");
 }
+// A product over 16 STEPS elements of K of two operand tiles; a_block and b_block are the descriptors' distance between
+// blocks of 64 elements. Straight-line: a descriptor computed between two products is what their issue then waits for.
+template <int STEPS>
+__device__ __forceinline__ void tc_mma_steps(uint32_t d, uint64_t a, uint32_t a_block, uint64_t b, uint32_t b_block, uint32_t idesc) {
+#pragma unroll
+    for (uint32_t i = 0; i < STEPS; i++) tc_mma(d, a + (i >> 2) * a_block + (i & 3) * 2, b + (i >> 2) * b_block + (i & 3) * 2, idesc, i != 0);
+}
 // The barrier gets one arrival once the thread's products so far are complete.
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
@@ -59,6 +66,17 @@ __device__ __forceinline__ void tc_ld16(float* v, uint32_t addr) {
         : "memory");
 }
 
+__device__ __forceinline__ void tc_ld32(uint32_t* r, uint32_t addr) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,"
+        "%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr)
+        : "memory");
+}
 // Two FP32 operations at once.
 __device__ __forceinline__ uint64_t pair(float lo, float hi) {
     uint64_t d;

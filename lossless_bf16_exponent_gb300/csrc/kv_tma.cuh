@@ -24,8 +24,12 @@ struct Maps {
     uint32_t box;  // tokens of a copy
 };
 
-// Maps of a cache for tiles of `tile` tokens; false where its pages do not allow them.
-bool maps_of(const AttParams& p, const uzkv_cache_t* c, uint32_t tile, Maps* m);
+// Maps of a cache for tiles of `tile` tokens; false where its pages do not allow them, or copies of at least `least`
+// bytes. A copy costs the accelerator about as much time as 2 KB take, so small ones fall behind the threads' copies.
+// Measured, bulk / threads, 16-bit heads of 128: attention of a decoding batch, 2 KB copies (pages of 16) 328 / 267 us,
+// 4 KB 252 / 266; many rows, 2 KB 297 / 399 us; mass, 2 KB 99 / 107 us; mass of E5M2 heads of 64, 1 KB 27.1 / 24.9,
+// 2 KB 23.7 / 24.9 us.
+bool maps_of(const AttParams& p, const uzkv_cache_t* c, uint32_t tile, uint32_t least, Maps* m);
 
 __device__ __forceinline__ void tma_fetch_map(const CUtensorMap* m) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
