@@ -3,13 +3,14 @@
 // generation tensor cores.
 //
 // Bound: the tensor cores, 4 D flop a row and token. Two streams of work share
-// a CTA: each has 128 rows of queries, a 128 x 128 score tile and an output in
-// tensor memory, and a group of four warps in which a thread is a row, so the
-// running reference and sum of its softmax are a thread's own. While one
-// stream's group turns scores into weights, the other's products run. A unit
-// of more than 128 rows gives each stream 128 of them, and both go through
-// every tile of 128 cached tokens; one of up to 128 rows gives both streams
-// the same rows, and they take the tiles in turn and are merged at its end.
+// a CTA: each has 128 rows of queries, two 128 x 64 score tiles and an output in
+// tensor memory, a thread that issues its products, and a group of four warps
+// in which a thread is a row, so the running reference and sum of its softmax
+// are a thread's own. While the group turns one score tile into weights, the
+// other one's product runs. A unit of more than 128 rows gives each stream 128
+// of them, and both go through every tile of 128 cached tokens, half a tile at a
+// time; one of up to 128 rows gives both streams the same rows, and they take
+// the tiles in turn and are merged at its end.
 //
 //   S = Q K^T        Q and K tiles in shared memory, S in tensor memory
 //   P = exp2(S - r)  by the stream's group; P, 16-bit, replaces S in tensor memory
@@ -20,7 +21,7 @@
 // 0-3 widen E5M2, which lands as bytes, take non-finite values out of tiles
 // with new tokens, and do the copies where pages do not allow bulk ones; 4-7
 // and 8-11 are the streams' groups, which also load their unit's queries and
-// write its output; 12 issues the products.
+// write its output; 12 and 14 issue the streams' products.
 #pragma once
 
 #include <algorithm>
@@ -30,7 +31,7 @@
 
 namespace uzkv {
 
-constexpr int kManyThreads = 14 * 32;
+constexpr int kManyThreads = 15 * 32;
 constexpr uint32_t kManyTile = 128;
 
 template <typename QT, bool FP8, int DP>
@@ -41,12 +42,14 @@ struct ManyCfg {
     static constexpr uint32_t kRawBytes = kManyTile * DP;            // their E5M2 bytes
     static constexpr uint32_t kOther = 2560 + 512;                   // factors and statistics; barriers
     static constexpr uint32_t kRoom = 227 * 1024 - kOther - 2 * kQTile;
-    static constexpr uint32_t kRaw = FP8 ? 4 : 0;
+    static constexpr uint32_t kRaw = FP8 ? (DP == 64 ? 4 : 2) : 0;
     static constexpr uint32_t kFit = (kRoom - kRaw * kRawBytes) / kTileBytes;
     static constexpr uint32_t kTiles = kFit > 8 ? 8 : kFit;
     static constexpr uint32_t kRing = FP8 ? kRaw : kTiles;           // tiles on their way
     static constexpr uint32_t kSmem = kOther + 2 * kQTile + kTiles * kTileBytes + kRaw * kRawBytes;
-    static_assert(kTiles >= 3, "the keys of two tiles and a tile of values");
+    // A stream asks for its next tile's keys, two tiles on where the streams take turns, before it has given back the
+    // values of its last: four operand tiles are the fewest that have room for that.
+    static_assert(kTiles >= 4, "operand tiles");
 };
 
 __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
@@ -62,17 +65,6 @@ __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t* r) {
         "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
-__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t* r) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
-        "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
-        "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
-        "r"(r[31])
-        : "memory");
-}
-
 // Descriptor of a tile whose contiguous dimension is the product's N: blocks of 64 elements `block` bytes apart,
 // groups of 8 rows 1024 bytes apart, 128-byte swizzle.
 __device__ __forceinline__ uint64_t rows_desc(uint32_t addr, uint32_t block) {
@@ -80,8 +72,7 @@ __device__ __forceinline__ uint64_t rows_desc(uint32_t addr, uint32_t block) {
            (uint64_t)2 << 61;
 }
 
-// One CTA's share of a unit: its tiles as jobs of the two streams. With up to 128 rows the streams take tiles in
-// turn, else both take each; either way jobs alternate between them.
+// One CTA's share of a unit. With up to 128 rows the streams take its tiles in turn, else both take each.
 struct ManyPart {
     Unit u;
     uint32_t count, rows;  // tiles in this run; rows of the unit that exist
@@ -91,9 +82,13 @@ struct ManyPart {
         rows = min(p.m, p.rows - u.mt * p.m);
         both = rows > 128;
     }
-    __device__ __forceinline__ uint32_t jobs() const { return both ? 2 * count : count; }
-    __device__ __forceinline__ uint32_t tile_of(uint32_t job) const { return both ? job / 2 : job; }
-    __device__ __forceinline__ uint32_t jobs_of(uint32_t stream) const { return both ? count : (count + 1 - stream) / 2; }
+    // Half tiles of a stream, and the tile of one. The unit's last tile has one half where its tokens end in it.
+    __device__ __forceinline__ uint32_t halves(uint32_t stream) const {
+        const uint32_t tiles = both ? count : (count + 1 - stream) / 2;
+        const bool last = u.tile + count == u.tiles && (both || (count - 1) % 2 == stream);
+        return 2 * tiles - (last && (u.span.old + u.span.fresh - 1) % kManyTile < kManyTile / 2 ? 1 : 0);
+    }
+    __device__ __forceinline__ uint32_t tile_of(uint32_t stream, uint32_t half) const { return both ? half / 2 : half / 2 * 2 + stream; }
     __device__ __forceinline__ Unit next(const AttParams& p) const {
         Unit n = u;
         n.tile += count - 1;
@@ -115,29 +110,29 @@ __global__ void __launch_bounds__(kManyThreads, 1) attend_many_kernel(const __gr
     float* const factor = reinterpret_cast<float*>(raws + C::kRaw * C::kRawBytes);  // [256], or [128] of shared rows ...
     float2* const stat = reinterpret_cast<float2*>(factor + 128);  // ... and then [2][128]: each stream's reference and sum
     uint64_t* const bars = reinterpret_cast<uint64_t*>(factor + 640);
-    uint32_t* const dirty = reinterpret_cast<uint32_t*>(bars + 40);  // [8]: a unit's tiles had non-finite values taken out
+    uint32_t* const dirty = reinterpret_cast<uint32_t*>(bars + 48);  // [8]: a unit's tiles had non-finite values taken out
     uint32_t* const tmem_at = dirty + 8;
     const uint32_t tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const uint32_t D = p.cache.head_dim;
-    const uint32_t full = smem_u32(bars), freed = full + 8 * 8, s_full = full + 16 * 8, p_full = full + 18 * 8,
-                   q_full = full + 20 * 8, o_full = full + 21 * 8, stat_full = full + 22 * 8, unit_done = full + 23 * 8,
-                   landed = full + 24 * 8, raw_freed = full + 32 * 8;
+    const uint32_t full = smem_u32(bars), freed = full + 8 * 8, s_full = full + 16 * 8, p_full = full + 20 * 8,
+                   o_ready = full + 24 * 8, q_full = full + 28 * 8, stat_full = full + 29 * 8, unit_done = full + 30 * 8,
+                   landed = full + 32 * 8, raw_freed = full + 40 * 8;
 
     uzip::pdl_launch_dependents();
     if (tid == 0) {
         for (uint32_t i = 0; i < 8; i++) {
             bar_init(full + 8 * i, 4);       // the four warps that bring, widen or clean; bulk copies that need none of it
-            bar_init(freed + 8 * i, 1);      // the products' commit
+            bar_init(freed + 8 * i, 2);      // both streams
             bar_init(landed + 8 * i, 1);     // bulk copies for those warps
             bar_init(raw_freed + 8 * i, 4);  // E5M2 bytes: widened
             dirty[i] = 0;
         }
-        for (uint32_t i = 0; i < 2; i++) {
+        for (uint32_t i = 0; i < 4; i++) {  // of a stream's two score tiles
             bar_init(s_full + 8 * i, 1);
-            bar_init(p_full + 8 * i, 4);  // the four warps of the stream's group
+            bar_init(p_full + 8 * i, 4);   // the four warps of the stream's group
+            bar_init(o_ready + 8 * i, 1);  // the products with values of every other half tile
         }
         bar_init(q_full, 8);
-        bar_init(o_full, 1);
         bar_init(stat_full, 8);
         bar_init(unit_done, 8);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -303,47 +298,61 @@ __global__ void __launch_bounds__(kManyThreads, 1) attend_many_kernel(const __gr
             for (uint32_t k = n > C::kRing ? n - C::kRing : 0; k < n; k++)  // no copy outlives the CTA
                 ok &= warp_wait(last + 8 * (k % C::kRing), (k / C::kRing) & 1);
         }
-    } else if (warp == 12) {
-        // ---- products, by one lane
+    } else if (warp == 12 || warp == 14) {
+        // ---- a stream's products, by one lane
         if (lane == 0) {
+            const uint32_t x = warp == 12 ? 0 : 1;
             const uint32_t n = (D + 15) / 16 * 16;  // columns of the output
-            const uint32_t iqk = mma_desc<T>(128, kManyTile), ipv = mma_desc<T>(128, n) | 1u << 16;  // V: N contiguous
+            const uint32_t iqk = mma_desc<T>(128, 64), ipv = mma_desc<T>(128, n) | 1u << 16;  // V: N contiguous
             // Descriptors once; offsets add to their low bits.
-            const uint64_t q_desc = tile_desc(smem_u32(qs)), k_desc = tile_desc(smem_u32(tiles)),
-                           v_desc = rows_desc(smem_u32(tiles), kManyTile * 128);
-            uint32_t base = 0, index = 0, weights[2] = {0, 0};  // operand tiles of earlier units; units; jobs of each stream
+            const uint64_t q0 = tile_desc(smem_u32(qs)), k0 = tile_desc(smem_u32(tiles)), v0 = rows_desc(smem_u32(tiles), kManyTile * 128);
+            uint32_t base = 0, index = 0, turns = 0;  // operand tiles of earlier units; units; phases of the two p_full
             while (unit.pos < run.end && ok) {
                 const ManyPart part(p, unit, run.end);
-                const uint32_t jobs = part.jobs();
-                auto score = [&](uint32_t j) {
-                    const uint32_t t = base + 2 * part.tile_of(j), s = t % C::kTiles, x = j & 1;
-                    if (!part.both || !x) ok = bar_wait(full + 8 * s, (t / C::kTiles) & 1);
-                    if (!ok) return;
+                const uint32_t halves = part.halves(x);
+                const uint64_t q = q0 + (part.both ? x * (C::kQTile >> 4) : 0);
+                auto wait_full = [&](uint32_t t) { return bar_wait(full + 8 * (t % C::kTiles), (t / C::kTiles) & 1); };
+                auto pass = [&](uint32_t tile) {  // a tile of the other stream's: give it back as soon as it is there
+                    for (uint32_t t = base + 2 * tile; ok && t < base + 2 * tile + 2; t++) {
+                        ok = wait_full(t);
+                        if (ok) bar_arrive(freed + 8 * (t % C::kTiles));
+                    }
+                };
+                auto score = [&](uint32_t h) {
+                    const uint32_t tile = part.tile_of(x, h), t = base + 2 * tile, s = t % C::kTiles;
+                    if (!(h & 1)) {
+                        if (!part.both && tile) pass(tile - 1);
+                        if (ok) ok = wait_full(t);
+                        if (!ok) return;
+                    }
                     tc_fence_after();
-                    const uint64_t q = q_desc + (part.both ? x * (C::kQTile >> 4) : 0), k = k_desc + s * (C::kTileBytes >> 4);
-                    if (D > DP * 3 / 4) tc_mma_steps<DP / 16>(tmem + x * 256, q, 128 * 128 >> 4, k, kManyTile * 128 >> 4, iqk);
-                    else tc_mma_steps<DP * 3 / 64>(tmem + x * 256, q, 128 * 128 >> 4, k, kManyTile * 128 >> 4, iqk);
-                    tc_commit(s_full + 8 * x);
-                    if (!part.both || x) tc_commit(freed + 8 * s);
+                    const uint64_t k = k0 + s * (C::kTileBytes >> 4) + (h & 1) * (64 * 128 >> 4);
+                    tc_mma_steps<DP / 16>(tmem + x * 256 + (h & 1) * 64, q, 128 * 128 >> 4, k, kManyTile * 128 >> 4, iqk);
+                    tc_commit(s_full + 8 * (2 * x + (h & 1)));
+                    if ((h & 1) || h + 1 == halves) tc_commit(freed + 8 * s);
                 };
                 ok = bar_wait(q_full, index & 1);
-                if (ok) score(0);
-                if (ok && jobs > 1) score(1);
-                for (uint32_t j = 0; j < jobs && ok; j++) {
-                    const uint32_t t = base + 2 * part.tile_of(j) + 1, s = t % C::kTiles, x = j & 1;
-                    ok = bar_wait(full + 8 * s, (t / C::kTiles) & 1);
-                    const uint32_t done = x ? weights[1]++ : weights[0]++;
-                    if (ok) ok = bar_wait(p_full + 8 * x, done & 1);
+                if (ok && halves) score(0);
+                if (ok && halves > 1) score(1);
+                for (uint32_t h = 0; h < halves && ok; h++) {
+                    const uint32_t t = base + 2 * part.tile_of(x, h) + 1, s = t % C::kTiles, b = h & 1;
+                    if (!b) ok = wait_full(t);
+                    if (ok) ok = bar_wait(p_full + 8 * (2 * x + b), (turns >> b) & 1);
+                    turns ^= 1u << b;
                     if (!ok) break;
                     tc_fence_after();
-                    const uint64_t v = v_desc + s * (C::kTileBytes >> 4);
+                    const uint64_t v = v0 + s * (C::kTileBytes >> 4) + b * (64 * 128 >> 4);
 #pragma unroll
-                    for (uint32_t i = 0; i < kManyTile / 16; i++)
-                        tc_mma_ts(tmem + x * 256 + 128, tmem + x * 256 + i * 8, v + i * (2048 >> 4), ipv, j > 1 || i != 0);
-                    if (!part.both || x) tc_commit(freed + 8 * s);
-                    if (j + 2 < jobs) score(j + 2);
+                    for (uint32_t i = 0; i < 4; i++)
+                        tc_mma_ts(tmem + x * 256 + 128, tmem + x * 256 + b * 64 + i * 8, v + i * (2048 >> 4), ipv, h != 0 || i != 0);
+                    tc_commit(o_ready + 8 * (2 * x + b));
+                    if (b || h + 1 == halves) tc_commit(freed + 8 * s);
+                    if (h + 2 < halves) score(h + 2);
                 }
-                if (ok) tc_commit(o_full);
+                if (!part.both) {  // tiles of the other stream's after this one's last
+                    const uint32_t mine = (halves + 1) / 2, next = mine ? 2 * (mine - 1) + x + 1 : 0;
+                    for (uint32_t tile = next; tile < part.count && ok; tile++) pass(tile);
+                }
                 base += 2 * part.count;
                 index++;
                 unit = part.next(p);
@@ -354,7 +363,10 @@ __global__ void __launch_bounds__(kManyThreads, 1) attend_many_kernel(const __gr
         // ---- a stream's softmax, queries and output: thread `row` of 128
         const uint32_t x = warp < 8 ? 0 : 1, row = (warp % 4) * 32 + lane;
         const uint32_t lanes = warp % 4 * 32 << 16, st = tmem + x * 256 + lanes, ot = st + 128;
-        uint32_t index = 0, scored = 0;
+        uint32_t index = 0, turns = 0;          // units; phases of the two s_full
+        // Products with values of this stream in earlier units, by half. When a half tile's scores are there, the
+        // products of the last one but one are complete, so of a barrier's phases at most one is open.
+        uint32_t products[2] = {0, 0};
         while (unit.pos < run.end && ok) {
             const ManyPart part(p, unit, run.end);
             const Unit& u = part.u;
@@ -375,105 +387,98 @@ __global__ void __launch_bounds__(kManyThreads, 1) attend_many_kernel(const __gr
             ok = warp_wait(q_full, index & 1);  // factors of the other warps too
             if (!ok) break;
             const uint32_t mine = part.both ? x * 128 + row : row;  // row of the unit
-            const float f = factor[mine];
+            float f = factor[mine];
+            if (f == 0.0f) f = 1.17549435e-38f;  // the smallest normal number: 0 * -inf would be no number
             float ref = -INFINITY, sum = 0.0f;
-            const uint32_t jobs = part.jobs_of(x);
-            for (uint32_t j = 0; j < jobs; j++) {
-                const uint32_t j0 = (u.tile + (part.both ? j : 2 * j + x)) * kManyTile;
-                ok = warp_wait(s_full + 8 * x, scored++ & 1);
+            const uint32_t halves = part.halves(x);
+            for (uint32_t h = 0; h < halves; h++) {
+                const uint32_t b = h & 1, at = st + b * 64, j0 = (u.tile + part.tile_of(x, h)) * kManyTile + b * 64;
+                ok = warp_wait(s_full + 8 * (2 * x + b), (turns >> b) & 1);
+                turns ^= 1u << b;
                 if (!ok) break;
                 tc_fence_after();
-                const bool masked = j0 + kManyTile > u.span.old;
-                uint64_t seen[2] = {~0ull, ~0ull};
-                if (masked) {
-                    seen[0] = seen_bits(p, u.b, u.span, row0 + mine, j0);
-                    seen[1] = seen_bits(p, u.b, u.span, row0 + mine, j0 + 64);
+                uint32_t v[64];
+                tc_ld32(v, at);
+                tc_ld32(v + 32, at + 32);
+                uint64_t seen = ~0ull;
+                if (j0 + 64 > u.span.old) seen = seen_bits(p, u.b, u.span, row0 + mine, j0);
+                tc_wait_ld();
+                if (j0 + 64 > u.span.old) {
+#pragma unroll
+                    for (int i = 0; i < 64; i++)
+                        if (!((uint32_t)(seen >> (i & 32)) >> (i & 31) & 1)) v[i] = 0xFF800000u;  // -inf
                 }
-                // Largest score of the row: 32 columns at a time, the next ones on their way meanwhile.
-                uint32_t v[2][32];
-                float part[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                tc_ld32(v[0], st);
+                float most[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int c = 0; c < 4; c++) {
-                    tc_wait_ld();
-                    tc_ld32(v[(c + 1) & 1], st + (c < 3 ? 32 * (c + 1) : 0));  // after the last, the first again
-                    uint32_t* y = v[c & 1];
-                    if (masked) {
-                        const uint32_t bits = (uint32_t)(seen[c / 2] >> (32 * (c & 1)));
-#pragma unroll
-                        for (int i = 0; i < 32; i++)
-                            if (!(bits >> i & 1)) y[i] = 0xFF800000u;  // -inf
-                    }
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2)
-                        part[i / 2 % 4] = fmaxf(part[i / 2 % 4], fmaxf(__uint_as_float(y[i]), __uint_as_float(y[i + 1])));
-                }
-                const float most = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
-                const float high = most == -INFINITY ? most : most * f;  // f is not negative; 0 * -inf is none
-                const bool rise = high > ref + kSlack;                   // the reference may trail by kSlack
-                if (__any_sync(0xFFFFFFFFu, rise)) {
+                for (int i = 0; i < 64; i += 2)
+                    most[i / 2 % 4] = fmaxf(most[i / 2 % 4], fmaxf(__uint_as_float(v[i]), __uint_as_float(v[i + 1])));
+                float high = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
+                high *= f;  // f is positive
+                if (__any_sync(0xFFFFFFFFu, high > ref + kSlack)) {  // the reference may trail by kSlack
                     const float now = fmaxf(ref, high);
                     const float fade = ref == -INFINITY ? 0.0f : exp2_fast(ref - now);  // 0: nothing so far
                     ref = now;
                     sum *= fade;
-                    if (j > 0) {  // the stream's products are complete up to its last tile
-                        tc_wait_ld();
-                        for (uint32_t c = 0; c < D; c += 32) {
-                            uint32_t z[32];
-                            tc_ld32(z, ot + c);
+                    if (h > 0) {  // the last product with values may still run
+                        ok = warp_wait(o_ready + 8 * (2 * x + 1 - b), ((b ? products[0] : products[1]) + (h - 1) / 2) & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        for (uint32_t c = 0; c < D; c += 16) {
+                            float z[16];
+                            tc_ld16(z, ot + c);
                             tc_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 32; i++) z[i] = __float_as_uint(__uint_as_float(z[i]) * fade);
-                            tc_st32(ot + c, z);
+                            for (int i = 0; i < 16; i++) z[i] *= fade;
+                            tc_st16(ot + c, reinterpret_cast<const uint32_t*>(z));
                         }
                     }
                 }
-                // Weights: they take the place of scores already read.
+                // Weights take the scores' place, 32 columns for 64.
                 const float r = ref == -INFINITY ? 0.0f : ref - kLift<T>;
                 const uint64_t f2 = pair(f, f), r2 = pair(-r, -r);
                 uint64_t add[2] = {0, 0};
 #pragma unroll
-                for (int c = 0; c < 4; c++) {
-                    tc_wait_ld();
-                    if (c < 3) tc_ld32(v[(c + 1) & 1], st + 32 * (c + 1));
-                    const uint32_t* y = v[c & 1];
-                    const uint32_t bits = (uint32_t)(seen[c / 2] >> (32 * (c & 1)));
+                for (int c = 0; c < 2; c++) {
                     uint32_t w[16];
 #pragma unroll
                     for (int i = 0; i < 32; i += 2) {
-                        float2 a = unpair(fma2(pair(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), f2, r2));
-                        if (masked) {
-                            if (!(bits >> i & 1)) a.x = -INFINITY;
-                            if (!(bits >> i & 2)) a.y = -INFINITY;
-                        }
+                        const uint32_t *y = v + 32 * c + i;
+                        float2 a = unpair(fma2(pair(__uint_as_float(y[0]), __uint_as_float(y[1])), f2, r2));
                         a.x = exp2_fast(a.x);
                         a.y = exp2_fast(a.y);
                         add[i / 2 & 1] = add2(add[i / 2 & 1], pair(a.x, a.y));
                         w[i / 2] = pack2<T>(a.x, a.y);
                     }
-                    tc_st16(st + 16 * c, w);
+                    tc_st16(at + 16 * c, w);
                 }
                 const float2 total = unpair(add2(add[0], add[1]));
                 sum += total.x + total.y;
                 tc_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) bar_arrive(p_full + 8 * x);
+                if (lane == 0) bar_arrive(p_full + 8 * (2 * x + b));
             }
             if (!ok) break;
             // ---- output
-            ok = warp_wait(o_full, index & 1);
+            if (halves) {
+                const uint32_t b = (halves - 1) & 1;
+                ok = warp_wait(o_ready + 8 * (2 * x + b), ((b ? products[1] : products[0]) + (halves - 1) / 2) & 1);
+            }
+            products[0] += (halves + 1) / 2;
+            products[1] += halves / 2;
             if (!ok) break;
             tc_fence_after();
-            const bool odd = *reinterpret_cast<volatile uint32_t*>(dirty + index % 8) != 0;
             float mref = ref == -INFINITY ? 0.0f : ref - kLift<T>;
             // Streams that took the tiles of the same rows in turn: each merges half of the columns.
             float2 other = make_float2(0.0f, 0.0f);
             if (!part.both) stat[x * 128 + row] = make_float2(mref, sum);
+            tc_fence_before();
             __syncwarp();
             if (lane == 0) bar_arrive(stat_full);
-            ok = warp_wait(stat_full, index & 1);
+            ok = warp_wait(stat_full, index & 1);  // the other stream's output is complete too
             if (!ok) break;
+            tc_fence_after();
+            const bool odd = *reinterpret_cast<volatile uint32_t*>(dirty + index % 8) != 0;
             float keep = 1.0f, give = 0.0f;
             if (!part.both) {
                 other = stat[(1 - x) * 128 + row];
