@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) attend_many_kernel(const __gr
         for (uint32_t i = 0; i < 8; i++) {
             bar_init(full + 8 * i, 4);       // the four warps that bring, widen or clean; bulk copies that need none of it
             bar_init(freed + 8 * i, 2);      // both streams
-            bar_init(landed + 8 * i, 1);     // bulk copies for those warps
+            bar_init(landed + 8 * i, TMA ? 1 : 128);  // copies for those warps
             bar_init(raw_freed + 8 * i, 4);  // E5M2 bytes: widened
             dirty[i] = 0;
         }
@@ -169,46 +169,52 @@ __global__ void __launch_bounds__(kManyThreads, 1) attend_many_kernel(const __gr
             return pl;
         };
         if (!TMA) at = find();
-        auto copy = [&]() {
-            if (TMA) return;
-            if (ok && ahead.pos < run.end) {
-                if (!FP8 && copied >= kRing) ok = warp_wait(freed + 8 * (copied % kRing), (copied / kRing - 1) & 1);
-                __syncwarp();
-                const bool values = copied & 1;
-                const char* row = at.page < 0 ? nullptr : values ? v_row(p.cache, at, ahead.h) : k_row(p.cache, at, ahead.h);
-                char* slot = (FP8 ? raws : tiles) + (copied % kRing) * (FP8 ? C::kRawBytes : C::kTileBytes);
+        auto copy = [&]() {  // the next operand tile's rows of this warp, to a slot that is free
+            __syncwarp();
+            const bool values = copied & 1;
+            const char* row = at.page < 0 ? nullptr : values ? v_row(p.cache, at, ahead.h) : k_row(p.cache, at, ahead.h);
+            const uint32_t s = copied % kRing;
+            char* slot = (FP8 ? raws : tiles) + s * (FP8 ? C::kRawBytes : C::kTileBytes);
 #pragma unroll 8
-                for (uint32_t i = 0; i < kLanes; i++) {
-                    const uint32_t r = i * (32 / kLanes) + lane / kLanes;
-                    const char* src = reinterpret_cast<const char*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(row), r));
-                    const uint32_t R = warp * 32 + r;
-                    const uint32_t to = FP8 ? row_chunk<DP>(kManyTile, R, c) : swizzled(kManyTile, R, c);
-                    if (c < live) copy16(smem_u32(slot) + to, src ? src + c * 16 : p.cache.k, src != nullptr);
-                }
-                copied++;
-                if (values) {
-                    advance(p, ahead, p.mtiles);
-                    at = find();
-                }
+            for (uint32_t i = 0; i < kLanes; i++) {
+                const uint32_t r = i * (32 / kLanes) + lane / kLanes;
+                const char* src = reinterpret_cast<const char*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<uint64_t>(row), r));
+                const uint32_t R = warp * 32 + r;
+                const uint32_t to = FP8 ? row_chunk<DP>(kManyTile, R, c) : swizzled(kManyTile, R, c);
+                if (c < live) copy16(smem_u32(slot) + to, src ? src + c * 16 : p.cache.k, src != nullptr);
             }
-            copy_commit();
+            bar_arrive_copies(landed + 8 * s);
+            copied++;
+            if (values) {
+                advance(p, ahead, p.mtiles);
+                at = find();
+            }
         };
-        for (uint32_t i = 0; i < kRing - 1; i++) copy();
+        // As many copies as there is room for; waits for room only where nothing is left to hand on, because what frees
+        // a slot may need the tiles that are already here.
+        auto fill = [&](uint32_t sent) {
+            while (ok && ahead.pos < run.end && copied < sent + kRing) {
+                if (!FP8 && copied >= kRing) {
+                    const uint32_t bar = freed + 8 * (copied % kRing), phase = (copied / kRing - 1) & 1;
+                    if (copied > sent && !__all_sync(0xFFFFFFFFu, bar_test(bar, phase))) return;
+                    ok = warp_wait(bar, phase);
+                    if (!ok) return;
+                }
+                copy();
+            }
+        };
         Unit cur = unit;
         uint32_t sent = 0, index = 0, turns = 0;  // units so far; phases of `landed`, where only some tiles come through it
         while (cur.pos < run.end && ok) {
             const uint32_t j0 = cur.tile * kManyTile;
             for (uint32_t values = 0; values < 2 && ok; values++, sent++) {
                 const bool clean = values && j0 + kManyTile > cur.span.old;
-                if (TMA) {
-                    if (!FP8 && !clean) continue;
-                    const uint32_t s = sent % kRing;
-                    ok = warp_wait(landed + 8 * s, FP8 ? (sent / kRing) & 1 : (turns >> s) & 1);
-                    turns ^= 1u << s;
-                    if (!ok) break;
-                } else {
-                    copy_wait<kRing - 2>();
-                }
+                if (!TMA) fill(sent);
+                if (TMA && !FP8 && !clean) continue;
+                const uint32_t at_slot = sent % kRing;
+                if (ok) ok = warp_wait(landed + 8 * at_slot, FP8 || !TMA ? (sent / kRing) & 1 : (turns >> at_slot) & 1);
+                turns ^= 1u << at_slot;
+                if (!ok) break;
                 char* const tile = tiles + (sent % C::kTiles) * C::kTileBytes;
                 if (FP8) {
                     // Widen this warp's rows: 16 bytes to two chunks of eight FP16.
@@ -258,13 +264,12 @@ __global__ void __launch_bounds__(kManyThreads, 1) attend_many_kernel(const __gr
                     bar_arrive(full + 8 * (sent % C::kTiles));
                     if (TMA && FP8) bar_arrive(raw_freed + 8 * (sent % kRing));
                 }
-                copy();
             }
             const bool to_end = cur.tile + 1 == cur.tiles;
             advance(p, cur, p.mtiles);
             if (to_end) index++;
         }
-        if (!TMA) copy_wait<0>();
+        if (!TMA) asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp == 13) {
         // ---- bulk copies: keys, then values of each tile
         if (TMA) {

@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import threading
 from dataclasses import dataclass
 
 import torch
@@ -344,6 +345,23 @@ def tree_attention_workspace_bytes(cache: KVCache, tokens: int, heads: int) -> i
     return size
 
 
+_scratch = threading.local()
+
+
+def _workspace(cache: KVCache, size: int) -> torch.Tensor:
+    """Scratch of at least ``size`` bytes for a call on the current stream: one
+    buffer a host thread and stream, which its calls use one after the other. A
+    call under graph capture gets its own, which the graph then holds."""
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(size, dtype=torch.uint8, device=cache.device)
+    buffers = _scratch.__dict__
+    key = (cache.index, _sp(cache.index))
+    buffer = buffers.get(key)
+    if buffer is None or buffer.numel() < size:
+        buffer = buffers[key] = torch.empty(size, dtype=torch.uint8, device=cache.device)
+    return buffer
+
+
 def tree_attention(q: torch.Tensor, cache: KVCache, mask: torch.Tensor | None = None,
                    counts: torch.Tensor | None = None, scale: float | None = None, out: torch.Tensor | None = None,
                    lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
@@ -353,7 +371,10 @@ def tree_attention(q: torch.Tensor, cache: KVCache, mask: torch.Tensor | None = 
     its mask row (:func:`tree_mask`; one tree for all when the mask has one
     sequence; None: a chain, each token and those before it). Returns ``(out,
     lse)``: the output, and the float32 log-sum-exp [sequences, tokens, heads].
-    Rows that see nothing, and tokens at or past ``counts``, give 0 and -inf."""
+    Rows that see nothing, and tokens at or past ``counts``, give 0 and -inf.
+    ``workspace``: :func:`tree_attention_workspace_bytes` of uint8 that no call
+    on another stream uses meanwhile; None takes a buffer that is kept for the
+    calling thread's work on this stream (up to 43 MB)."""
     rq = _query(q, cache)
     b, t, heads, d = q.shape
     address, stride = _mask(mask, cache, t) if mask is not None else (None, 0)
@@ -364,7 +385,7 @@ def tree_attention(q: torch.Tensor, cache: KVCache, mask: torch.Tensor | None = 
     else:
         at_lse = _floats(lse, "lse", (b, t, heads), cache)
     if workspace is None:
-        workspace = torch.empty(tree_attention_workspace_bytes(cache, t, heads), dtype=torch.uint8, device=cache.device)
+        workspace = _workspace(cache, tree_attention_workspace_bytes(cache, t, heads))
     elif not _tensor(workspace, "workspace", torch.uint8, None, cache.device).is_contiguous():
         raise ValueError("workspace: expected a contiguous tensor")
     check(load().uzkv_tree_attention(ctypes.byref(rq), ctypes.byref(ro), at_lse, _DTYPES[q.dtype], t, heads, address,
