@@ -115,7 +115,8 @@ def load(path: str | None = None):
               "uzip_e5m2_calibrate", "uzip_e5m2_encode", "uzip_e5m2_decode", "uzip_codebook_make_sentinel",
               "uzip_sentinel_encode", "uzip_sentinel_decode"):
         getattr(L, f).restype = i
-    f32, i64, cache, rows = ctypes.c_float, ctypes.c_int64, ctypes.POINTER(KvCache), ctypes.POINTER(KvRows)
+    f32, i64, cache = ctypes.c_float, ctypes.c_int64, ctypes.POINTER(KvCache)
+    rows = vp  # a KvRows, or its packed bytes
     L.uzkv_rotary.argtypes = [rows, rows, u32, u32, u32, u32, u32, vp, i64, vp, u32, u32, f32, i, vp]
     L.uzkv_rotary_append.argtypes = [rows, rows, rows, rows, u32, u32, u32, vp, i64, vp, u32, u32, f32, vp, cache, vp]
     L.uzkv_tree_attention_workspace_bytes.argtypes = [u32, u32, u32, u32, u32]

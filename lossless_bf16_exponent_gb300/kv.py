@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 import threading
 from dataclasses import dataclass
 
@@ -22,9 +23,14 @@ from . import _lib
 from ._lib import check
 from .codec import _sp, load
 
+# Calls of a few microseconds on the GPU are bound by the host: each call looks
+# every attribute up once, and tensors go to the C ABI as packed structures.
+_pack_rows = struct.Struct("@Pqqq").pack  # uzkv_rows_t
+
 MAX_HEAD_DIM = 256
 MAX_NEW_TOKENS = 256
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.float8_e5m2: 3}
+_FLOATS = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _LAYOUTS = {"half": 0, "interleaved": 1}
 
 
@@ -46,12 +52,12 @@ def _dense(t: torch.Tensor, what: str, dtype, shape, device) -> torch.Tensor:
     return t
 
 
-def _rows(x: torch.Tensor, what: str) -> _lib.KvRows:
-    """A [sequences, tokens, heads, dim] or [tokens, heads, dim] tensor as the C ABI takes it."""
-    *outer, st, sh, sd = x.stride()
-    if sd != 1 and x.shape[-1] != 1:
+def _rows(x: torch.Tensor, what: str) -> bytes:
+    """A [sequences, tokens, heads, dim] tensor as the C ABI takes it."""
+    sb, st, sh, sd = x.stride()
+    if sd != 1 and x.shape[3] != 1:
         raise ValueError(f"{what}: elements of a row must be contiguous")
-    return _lib.KvRows(x.data_ptr(), outer[0] if outer else 0, st, sh)
+    return _pack_rows(x.data_ptr(), sb, st, sh)
 
 
 def _writable(x: torch.Tensor, what: str) -> torch.Tensor:
@@ -82,6 +88,7 @@ class RotaryPlan:
             raise ValueError("turns: expected a contiguous int64 tensor of rotary_dim / 2")
         # What each call passes on, looked up once.
         object.__setattr__(self, "index", self.turns.get_device())
+        object.__setattr__(self, "device", self.turns.device)
         object.__setattr__(self, "args", (self.turns.data_ptr(), self.rotary_dim, _LAYOUTS[self.layout], self.magnitude))
 
 
@@ -133,35 +140,46 @@ def rotary_plan(rotary_dim: int, base: float = 10000.0, layout: str = "half", sc
     return RotaryPlan(turns, rotary_dim, layout, magnitude)
 
 
-def _positions(positions, shape, index) -> int:
-    """Check int32 positions of tokens; the stride between their rows."""
-    if positions.dtype != torch.int32 or positions.shape != shape or positions.get_device() != index:
-        raise ValueError(f"positions: expected int32 {tuple(shape)} on the tensors' device")
-    if shape[-1] > 1 and positions.stride(-1) != 1:
+def _positions(positions, b, t, index) -> int:
+    """Check int32 positions [b, t]; the stride between their rows."""
+    shape = positions.shape
+    if positions.dtype is not torch.int32 or len(shape) != 2 or shape[0] != b or shape[1] != t or positions.get_device() != index:
+        raise ValueError(f"positions: expected int32 of the tensor's {b} x {t} tokens on its device")
+    sb, st = positions.stride()
+    if st != 1 and t > 1:
         raise ValueError("positions: expected contiguous rows")
-    return positions.stride(0) if len(shape) == 2 else 0
+    return sb
 
 
 def _rotate(x, positions, plan, out, backward):
-    index, dims = x.get_device(), x.dim()
-    if x.dtype not in _DTYPES or x.dtype == torch.float8_e5m2:
+    kind, shape, index = _FLOATS.get(x.dtype), x.shape, x.get_device()
+    if kind is None:
         raise ValueError(f"expected bfloat16, float16 or float32 values, got {x.dtype}")
-    if dims not in (3, 4) or index < 0:
+    if len(shape) == 3:  # [tokens, heads, dim]
+        if positions.dim() != 1:
+            raise ValueError("positions: expected one for each token")
+        got = _rotate(x[None], positions[None], plan, None if out is None else out[None], backward)
+        return got[0] if out is None else out
+    if len(shape) != 4 or index < 0:
         raise ValueError("expected a CUDA tensor [tokens, heads, dim] or [sequences, tokens, heads, dim]")
     if plan.index != index:
         raise ValueError("plan: on another device")
-    shape = x.shape
-    step = _positions(positions, shape[:-2], index)
+    b, t, heads, d = shape
+    step = _positions(positions, b, t, index)
+    rx = _rows(x, "x")
     if out is None:
-        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+        out = torch.empty((b, t, heads, d), dtype=x.dtype, device=plan.device)
+        ro = _pack_rows(out.data_ptr(), t * heads * d, heads * d, d)
     else:
         _writable(_tensor(out, "out", x.dtype, shape, x.device), "out")
-    if x.numel() == 0:
+        ro = _rows(out, "out")
+    if b * t * heads * d == 0:
         return out
-    t, heads, d = shape[-3:]
-    check(load().uzkv_rotary(ctypes.byref(_rows(x, "x")), ctypes.byref(_rows(out, "out")), _DTYPES[x.dtype],
-                             shape[0] if dims == 4 else 1, t, heads, d, positions.data_ptr(), step, *plan.args,
-                             backward, _sp(index)), "uzkv_rotary")
+    turns, rotary_dim, layout, magnitude = plan.args
+    rc = load().uzkv_rotary(rx, ro, kind, b, t, heads, d, positions.data_ptr(), step, turns, rotary_dim, layout,
+                            magnitude, backward, _sp(index))
+    if rc:
+        check(rc, "uzkv_rotary")
     return out
 
 
@@ -228,7 +246,7 @@ class KVCache:
         self._workspace_bytes: dict[tuple[int, int], int] = {}  # by (tokens, heads)
 
 
-def _new_rows(x: torch.Tensor, what: str, cache: KVCache, heads: int | None = None) -> _lib.KvRows:
+def _new_rows(x: torch.Tensor, what: str, cache: KVCache, heads: int | None = None) -> bytes:
     """Check new tokens' rows [sequences, tokens, heads, head dim] of a cache."""
     shape = x.shape
     if len(shape) != 4 or shape[0] != cache.sequences or shape[3] != cache.head_dim or x.get_device() != cache.index \
@@ -237,16 +255,18 @@ def _new_rows(x: torch.Tensor, what: str, cache: KVCache, heads: int | None = No
                          f"on {cache.device}, got {tuple(shape)} on {x.device}")
     if x.dtype not in cache.takes:
         raise ValueError(f"{what}: {x.dtype} does not go with a cache of {cache.dtype}")
-    return _rows(x, what)
+    sb, st, sh, sd = x.stride()
+    if sd != 1 and shape[3] != 1:
+        raise ValueError(f"{what}: elements of a row must be contiguous")
+    return _pack_rows(x.data_ptr(), sb, st, sh)
 
 
-def _new_out(out: torch.Tensor | None, q: torch.Tensor):
+def _new_out(out: torch.Tensor | None, q: torch.Tensor, b: int, t: int, heads: int, d: int, device):
     """The output of q's shape (a new one where None), and its rows."""
     if out is None:
-        b, t, heads, d = q.shape
-        out = torch.empty((b, t, heads, d), dtype=q.dtype, device=q.device)
-        return out, _lib.KvRows(out.data_ptr(), t * heads * d, heads * d, d)
-    _writable(_tensor(out, "out", q.dtype, q.shape, q.device), "out")
+        out = torch.empty((b, t, heads, d), dtype=q.dtype, device=device)
+        return out, _pack_rows(out.data_ptr(), t * heads * d, heads * d, d)
+    _writable(_tensor(out, "out", q.dtype, q.shape, device), "out")
     return out, _rows(out, "out")
 
 
@@ -268,21 +288,23 @@ def rotary_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: 
     projection are fine), ``positions`` int32 [sequences, tokens]. Tokens at or
     past ``counts`` give zero queries and are not stored. ``out`` may be ``q``.
     Advancing ``cache.lengths`` is the caller's, once the tokens are accepted."""
-    rq = _new_rows(q, "q", cache)
-    rk, rv = _new_rows(k, "k", cache, cache.kv_heads), _new_rows(v, "v", cache, cache.kv_heads)
-    _, t, heads, _ = q.shape
-    if k.shape[1] != t or v.shape[1] != t or k.dtype != q.dtype or v.dtype != q.dtype:
+    kv_heads, index = cache.kv_heads, cache.index
+    rq, rk, rv = _new_rows(q, "q", cache), _new_rows(k, "k", cache, kv_heads), _new_rows(v, "v", cache, kv_heads)
+    b, t, heads, d = q.shape
+    dtype = q.dtype
+    if k.shape[1] != t or v.shape[1] != t or k.dtype is not dtype or v.dtype is not dtype:
         raise ValueError("k, v: type or tokens differ from q's")
-    if plan.index != cache.index:
+    if plan.index != index:
         raise ValueError("plan: on another device")
-    step = _positions(positions, q.shape[:2], cache.index)
-    out, ro = _new_out(out, q)
-    if q.numel() == 0:
+    step = _positions(positions, b, t, index)
+    out, ro = _new_out(out, q, b, t, heads, d, cache.device)
+    if t * heads == 0:
         return out
-    ref = ctypes.byref
-    check(load().uzkv_rotary_append(ref(rq), ref(rk), ref(rv), ref(ro), _DTYPES[q.dtype], t, heads, positions.data_ptr(),
-                                    step, *plan.args, _counts(counts, cache), cache._ref, _sp(cache.index)),
-          "uzkv_rotary_append")
+    turns, rotary_dim, layout, magnitude = plan.args
+    rc = load().uzkv_rotary_append(rq, rk, rv, ro, _FLOATS[dtype], t, heads, positions.data_ptr(), step, turns, rotary_dim,
+                                   layout, magnitude, _counts(counts, cache), cache._ref, _sp(index))
+    if rc:
+        check(rc, "uzkv_rotary_append")
     return out
 
 
@@ -320,13 +342,15 @@ def _mask(mask, cache, t):
     return mask.data_ptr(), 0 if mask.shape[0] == 1 else t * words
 
 
-def _query(q: torch.Tensor, cache: KVCache) -> _lib.KvRows:
+def _query(q: torch.Tensor, cache: KVCache):
+    """Check queries of new tokens; their rows and shape."""
     rows = _new_rows(q, "q", cache)
-    if not 1 <= q.shape[1] <= MAX_NEW_TOKENS:
-        raise ValueError(f"q: {q.shape[1]} new tokens, expected 1 to {MAX_NEW_TOKENS}")
-    if q.shape[2] == 0 or q.shape[2] % cache.kv_heads:
-        raise ValueError(f"q: {q.shape[2]} heads over {cache.kv_heads} kv heads")
-    return rows
+    b, t, heads, d = q.shape
+    if not 1 <= t <= MAX_NEW_TOKENS:
+        raise ValueError(f"q: {t} new tokens, expected 1 to {MAX_NEW_TOKENS}")
+    if heads == 0 or heads % cache.kv_heads:
+        raise ValueError(f"q: {heads} heads over {cache.kv_heads} kv heads")
+    return rows, b, t, heads, d
 
 
 def _floats(x: torch.Tensor, what: str, shape, cache: KVCache) -> int:
@@ -375,10 +399,9 @@ def tree_attention(q: torch.Tensor, cache: KVCache, mask: torch.Tensor | None = 
     ``workspace``: :func:`tree_attention_workspace_bytes` of uint8 that no call
     on another stream uses meanwhile; None takes a buffer that is kept for the
     calling thread's work on this stream (up to 43 MB)."""
-    rq = _query(q, cache)
-    b, t, heads, d = q.shape
+    rq, b, t, heads, d = _query(q, cache)
     address, stride = _mask(mask, cache, t) if mask is not None else (None, 0)
-    out, ro = _new_out(out, q)
+    out, ro = _new_out(out, q, b, t, heads, d, cache.device)
     if lse is None:
         lse = torch.empty((b, t, heads), dtype=torch.float32, device=cache.device)
         at_lse = lse.data_ptr()
@@ -388,9 +411,11 @@ def tree_attention(q: torch.Tensor, cache: KVCache, mask: torch.Tensor | None = 
         workspace = _workspace(cache, tree_attention_workspace_bytes(cache, t, heads))
     elif not _tensor(workspace, "workspace", torch.uint8, None, cache.device).is_contiguous():
         raise ValueError("workspace: expected a contiguous tensor")
-    check(load().uzkv_tree_attention(ctypes.byref(rq), ctypes.byref(ro), at_lse, _DTYPES[q.dtype], t, heads, address,
-                                     stride, _counts(counts, cache), d ** -0.5 if scale is None else scale, cache._ref,
-                                     workspace.data_ptr(), workspace.numel(), _sp(cache.index)), "uzkv_tree_attention")
+    rc = load().uzkv_tree_attention(rq, ro, at_lse, _FLOATS[q.dtype], t, heads, address, stride, _counts(counts, cache),
+                                    d ** -0.5 if scale is None else scale, cache._ref, workspace.data_ptr(),
+                                    workspace.numel(), _sp(cache.index))
+    if rc:
+        check(rc, "uzkv_tree_attention")
     return out, lse
 
 
@@ -406,8 +431,7 @@ def attention_mass(q: torch.Tensor, cache: KVCache, lse: torch.Tensor, mask: tor
     float32 [sequences, tokens] (1 for accepted tokens, 0 for the others; None:
     ones). ``out`` may be ``mass``; its width (default: the cache's capacity) says
     how many slots are weighed."""
-    rq = _query(q, cache)
-    b, t, heads, d = q.shape
+    rq, b, t, heads, d = _query(q, cache)
     address, stride = _mask(mask, cache, t) if mask is not None else (None, 0)
     at_lse = _floats(lse, "lse", (b, t, heads), cache)
     at_weights = _floats(weights, "weights", (b, t), cache) if weights is not None else None
@@ -430,10 +454,11 @@ def attention_mass(q: torch.Tensor, cache: KVCache, lse: torch.Tensor, mask: tor
         if mass.stride() != (sb, sh, sn):
             raise ValueError("mass: expected the strides of out")
         at_mass = mass.data_ptr()
-    check(load().uzkv_attention_mass(ctypes.byref(rq), at_lse, _DTYPES[q.dtype], t, heads, address, stride,
-                                     _counts(counts, cache), at_weights, d ** -0.5 if scale is None else scale,
-                                     cache._ref, at_mass, decay, out.data_ptr(), sb, sh, shape[2], _sp(cache.index)),
-          "uzkv_attention_mass")
+    rc = load().uzkv_attention_mass(rq, at_lse, _FLOATS[q.dtype], t, heads, address, stride, _counts(counts, cache),
+                                    at_weights, d ** -0.5 if scale is None else scale, cache._ref, at_mass, decay,
+                                    out.data_ptr(), sb, sh, shape[2], _sp(cache.index))
+    if rc:
+        check(rc, "uzkv_attention_mass")
     return out
 
 
@@ -457,26 +482,25 @@ def evict(cache: KVCache, mass: torch.Tensor, keep: int, sink: int = 0, recent: 
     """Keep ``keep`` tokens of each sequence and head and pack them: the first
     ``sink``, the last ``recent`` and those of the largest ``mass`` (float32
     [sequences, kv heads, slots]; equal masses: the lowest slot first). A sequence
-    of at most ``keep`` tokens keeps them all. ``out_k`` and ``out_v`` default to
-    two halves of one contiguous buffer, ready for :func:`encode`; given ones may
-    be views with room behind for tokens to come, but no part of the cache."""
+    of at most ``keep`` tokens keeps them all. ``out_k`` and ``out_v`` default to new
+    contiguous tensors, ready for :func:`encode`; given ones may be the halves of
+    one buffer or views with room behind for tokens to come, but no part of the
+    cache."""
     b, heads, d = cache.sequences, cache.kv_heads, cache.head_dim
-    if mass.dtype != torch.float32 or mass.get_device() != cache.index or mass.dim() != 3 \
-            or mass.shape[0] != b or mass.shape[1] != heads or mass.shape[2] < 1:
+    shape = mass.shape
+    if mass.dtype is not torch.float32 or mass.get_device() != cache.index or len(shape) != 3 or shape[0] != b \
+            or shape[1] != heads or shape[2] < 1:
         raise ValueError(f"mass: expected float32 [{b}, {heads}, slots] on {cache.device}, got {mass.dtype} "
-                         f"{tuple(mass.shape)} on {mass.device}")
+                         f"{tuple(shape)} on {mass.device}")
     sb, sh, sn = mass.stride()
-    if mass.shape[2] > 1 and sn != 1:
+    if shape[2] > 1 and sn != 1:
         raise ValueError("mass: expected contiguous rows")
     if keep < 1 or sink < 0 or recent < 0 or sink + recent > keep:
         raise ValueError("expected keep >= 1 and 0 <= sink + recent <= keep")
     device = cache.device
     if out_k is None and out_v is None:
-        both = torch.empty((2, b, heads, keep, d), dtype=cache.dtype, device=device)
-        out_k, out_v = both.unbind()
-        rows = heads * keep * d
-        rk = _lib.KvRows(both.data_ptr(), rows, keep * d, d)
-        rv = _lib.KvRows(both.data_ptr() + b * rows * both.element_size(), rows, keep * d, d)
+        out_k, out_v = (torch.empty((b, heads, keep, d), dtype=cache.dtype, device=device) for _ in range(2))
+        rk, rv = (_pack_rows(x.data_ptr(), heads * keep * d, keep * d, d) for x in (out_k, out_v))
     elif out_k is None or out_v is None:
         raise ValueError("give both out_k and out_v or neither")
     else:
@@ -486,9 +510,10 @@ def evict(cache: KVCache, mass: torch.Tensor, keep: int, sink: int = 0, recent: 
     kept = torch.empty((b, heads, keep), dtype=torch.int32, device=device)
     mass_out = torch.empty((b, heads, keep), dtype=torch.float32, device=device)
     lengths = torch.empty((b,), dtype=torch.int32, device=device)
-    check(load().uzkv_evict(cache._ref, mass.data_ptr(), sb, sh, mass.shape[2], keep, sink, recent, ctypes.byref(rk),
-                            ctypes.byref(rv), kept.data_ptr(), mass_out.data_ptr(), lengths.data_ptr(),
-                            _sp(cache.index)), "uzkv_evict")
+    rc = load().uzkv_evict(cache._ref, mass.data_ptr(), sb, sh, shape[2], keep, sink, recent, rk, rv, kept.data_ptr(),
+                           mass_out.data_ptr(), lengths.data_ptr(), _sp(cache.index))
+    if rc:
+        check(rc, "uzkv_evict")
     return Packed(out_k, out_v, mass_out, kept, lengths)
 
 
