@@ -324,7 +324,7 @@ __device__ __forceinline__ void load_queries(const AttParams& p, uint32_t tid, u
     constexpr bool kCast = !std::is_same<QT, T>::value;
     constexpr uint32_t kChunks = DP / 8;  // a power of two, at most 32
     const uint32_t c = tid % kChunks, live = p.cache.head_dim / 8;
-    constexpr int kBatch = 4;  // rows on their way at once
+    constexpr int kBatch = 8;  // rows on their way at once
     constexpr uint32_t kStep = THREADS / kChunks;
     for (uint32_t i0 = tid / kChunks; i0 < rows; i0 += kStep * kBatch) {
         uint4 in[kBatch];

@@ -281,12 +281,17 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const __grid_cons
             for (uint32_t i = 0; i < w.count && ok; i++) {
                 if (w.turn(i) != group) continue;
                 const uint32_t j0 = (w.u.tile + i) * kMassTile, j = j0 + quarter * 32 + lane;
+                // What the sum is added to: on its way meanwhile.
+                const bool decayed = w.chunk == 0;
+                float before = 0.0f;
+                if (j < p.slots && !decayed) before = p.mass_out[row_at + j];
+                else if (j < p.slots && p.mass_in && j < sp.old) before = p.mass_in[row_at + j];
                 ok = warp_wait(s_full + 8 * group, used++ & 1);
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t at = tmem + group * N + (quarter * 32 << 16);
                 float acc = 0.0f;
-                bool guard = j0 + kMassTile > sp.old;
+                bool guard = j0 + quarter * 32 + 32 > sp.old;
                 if (!guard) {
                     // 32 columns at a time, the next ones on their way meanwhile.
                     uint32_t v[2][32];
@@ -329,41 +334,53 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const __grid_cons
                     guard = __any_sync(0xFFFFFFFFu, acc != acc);
                 }
                 if (guard) {
-                    // Which new tokens see this lane's: token by token, its mask word fetched one token ahead.
+                    // Which new tokens see this lane's: 32 tokens' bits at a time, for the rows that are theirs.
                     acc = 0.0f;
                     const uint32_t row0 = w.chunk * N, u = j - sp.old;
                     uint32_t t = row0 / p.group, left = p.group - row0 % p.group;  // rows left of token t
-                    const bool in = j < sp.old + sp.fresh;
-                    const int64_t* words = p.mask ? p.mask + w.u.b * p.mask_b + (in && j >= sp.old ? u >> 6 : 0) : nullptr;
-                    auto word_of = [&](uint32_t tok) -> int64_t { return words && tok < sp.fresh ? words[(uint64_t)tok * p.mask_words] : 0; };
-                    auto sees = [&](int64_t word) { return in && (j < sp.old || (words ? (bool)(word >> (u & 63) & 1) : u <= t)); };
-                    int64_t word = word_of(t), ahead = word_of(t + 1);
-                    bool see = sees(word);
+                    const bool in = j < sp.old + sp.fresh, old = j < sp.old;
+                    const int64_t* words = p.mask && in && !old ? p.mask + w.u.b * p.mask_b + (u >> 6) : nullptr;
+                    auto bits_from = [&](uint32_t first) {
+                        uint32_t bits = !in ? 0 : old ? 0xFFFFFFFFu : 0;
+                        if (in && !old)
+#pragma unroll 8
+                            for (uint32_t i = 0; i < 32; i++) {
+                                const uint32_t tok = first + i;
+                                if (tok < sp.fresh && (p.mask ? (bool)(words[(uint64_t)tok * p.mask_words] >> (u & 63) & 1) : u <= tok)) bits |= 1u << i;
+                            }
+                        return bits;
+                    };
+                    uint32_t first_bit = t, bits = bits_from(t);
                     for (uint32_t c0 = 0; c0 < N; c0 += 16) {
                         float v[16];
                         tc_ld16(v, at + c0);
+                        uint32_t see = 0;  // of these 16 rows, a token's at once
+                        for (uint32_t x = 0; x < 16;) {
+                            const uint32_t n = min(left, 16 - x);
+                            see |= (bits & 1) ? ((1u << n) - 1) << x : 0;
+                            x += n;
+                            left -= n;
+                            if (left == 0) {  // the same for all lanes
+                                left = p.group;
+                                bits >>= 1;
+                                if (++t == first_bit + 32) {
+                                    first_bit = t;
+                                    bits = bits_from(t);
+                                }
+                            }
+                        }
                         tc_wait_ld();
 #pragma unroll
                         for (int x = 0; x < 16; x++) {
-                            const float m = exp2_fast(v[x] * f[c0 + x] + e[c0 + x]);
-                            acc += see && e[c0 + x] != -INFINITY ? m : 0.0f;
-                            if (--left == 0) {
-                                left = p.group;
-                                t++;
-                                see = sees(ahead);
-                                ahead = word_of(t + 1);
-                            }
+                            const float en = e[c0 + x], m = exp2_fast(v[x] * f[c0 + x] + en);
+                            acc += (see >> x & 1) && en != -INFINITY ? m : 0.0f;
                         }
                     }
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) bar_arrive(s_freed + 8 * group);
-                if (j < p.slots) {
-                    if (w.chunk) acc += p.mass_out[row_at + j];
-                    else if (p.mass_in && j < sp.old) acc += p.decay * p.mass_in[row_at + j];
-                    p.mass_out[row_at + j] = acc;
-                }
+                if (j < p.slots) p.mass_out[row_at + j] = acc + (decayed ? p.decay * before : before);
             }
             // This warp's last read of the unit's factors is behind it.
             __syncwarp();
@@ -408,7 +425,7 @@ int launch_mass_as(AttParams& p, const uzkv_cache_t* c, int sms, cudaStream_t st
     p.mtiles = chunks;
     p.m = ((p.rows + chunks - 1) / chunks + 15) / 16 * 16;
     p.shift = 7;
-    p.unit_cost = 3;
+    p.unit_cost = 5;
     static_assert(kMassTile == 1u << 7, "tile");
     p.grid = (uint32_t)sms;
     Maps maps{};
