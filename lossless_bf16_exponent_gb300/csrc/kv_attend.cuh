@@ -101,8 +101,8 @@ __global__ void __launch_bounds__(kAttThreads<TMA>, 1) attend_kernel(const __gri
             if (lane == 0) bar_expect(full + 8 * s, 2 * now.bytes(maps));
             __syncwarp();
             const uint32_t ks = smem_u32(smem + s * C::kStage);
-            now.copy(maps, &maps.k, h, ks, full + 8 * s);
-            now.copy(maps, &maps.v, h, ks + C::kTile * C::kRB, full + 8 * s);
+            now.copy(p, maps, &maps.k, h, ks, full + 8 * s);
+            now.copy(p, maps, &maps.v, h, ks + C::kTile * C::kRB, full + 8 * s);
         }
         for (uint32_t k = i > C::kStages ? i - C::kStages : 0; k < i; k++)  // no copy outlives the CTA
             ok &= warp_wait(full + 8 * (k % C::kStages), (k / C::kStages) & 1);
@@ -110,17 +110,20 @@ __global__ void __launch_bounds__(kAttThreads<TMA>, 1) attend_kernel(const __gri
         // ---- copies: a warp takes a quarter of a tile's tokens
         constexpr uint32_t kMine = C::kTile / 4, kLanes = C::kRB / 16;
         const uint32_t w = warp - 8, c = lane % kLanes, live = D * (FP8 ? 1 : 2) / 16;
-        Place at{-1, 0};
+        Place at{0, 0};
+        bool used = false;  // whether there is such a token
         auto find = [&]() {  // this lane's token of the tile under `cur`
-            Place pl{-1, 0};
+            Place pl{0, 0};
             const uint32_t j = cur.tile * C::kTile + w * kMine + lane;
-            if (cur.pos < run.end && lane < kMine && j < cur.span.old + cur.span.fresh) pl = place_of(p.cache, cur.b, j);
+            used = cur.pos < run.end && lane < kMine && j < cur.span.old + cur.span.fresh;
+            if (used) pl = look_up(p.cache, cur.b, j);
             return pl;
         };
         at = find();
         for (uint32_t i = 0; cur.pos < run.end && ok; i++) {
-            const char* krow = at.page >= 0 ? k_row(p.cache, at, cur.h) : nullptr;
-            const char* vrow = at.page >= 0 ? v_row(p.cache, at, cur.h) : nullptr;
+            const Place now = used ? checked(p.cache, at) : Place{-1, 0};
+            const char* krow = now.page >= 0 ? k_row(p.cache, now, cur.h) : nullptr;
+            const char* vrow = now.page >= 0 ? v_row(p.cache, now, cur.h) : nullptr;
             advance(p, cur, p.mtiles);
             at = find();
             const uint32_t s = i % C::kStages;

@@ -161,18 +161,21 @@ __global__ void __launch_bounds__(kManyThreads, 1) attend_many_kernel(const __gr
         const uint32_t c = lane % kLanes, live = D * kES / 16;
         Unit ahead = unit;     // tile to copy next
         uint32_t copied = 0;   // operand tiles copied: even ones are keys
-        Place at{-1, 0};
+        Place at{0, 0};
+        bool used = false;  // whether there is a token for this lane
         auto find = [&]() {
-            Place pl{-1, 0};
+            Place pl{0, 0};
             const uint32_t j = ahead.tile * kManyTile + warp * 32 + lane;
-            if (ahead.pos < run.end && j < ahead.span.old + ahead.span.fresh) pl = place_of(p.cache, ahead.b, j);
+            used = ahead.pos < run.end && j < ahead.span.old + ahead.span.fresh;
+            if (used) pl = look_up(p.cache, ahead.b, j);
             return pl;
         };
         if (!TMA) at = find();
         auto copy = [&]() {  // the next operand tile's rows of this warp, to a slot that is free
             __syncwarp();
             const bool values = copied & 1;
-            const char* row = at.page < 0 ? nullptr : values ? v_row(p.cache, at, ahead.h) : k_row(p.cache, at, ahead.h);
+            const Place now = used ? checked(p.cache, at) : Place{-1, 0};
+            const char* row = now.page < 0 ? nullptr : values ? v_row(p.cache, now, ahead.h) : k_row(p.cache, now, ahead.h);
             const uint32_t s = copied % kRing;
             char* slot = (FP8 ? raws : tiles) + s * (FP8 ? C::kRawBytes : C::kTileBytes);
 #pragma unroll 8
@@ -296,7 +299,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) attend_many_kernel(const __gr
                         if (!by) bar_arrive(done, 3);
                     }
                     __syncwarp();
-                    now.copy(maps, values ? &maps.v : &maps.k, h, smem_u32(ring + s * (FP8 ? C::kRawBytes : C::kTileBytes)), done);
+                    now.copy(p, maps, values ? &maps.v : &maps.k, h, smem_u32(ring + s * (FP8 ? C::kRawBytes : C::kTileBytes)), done);
                 }
             }
             const uint32_t last = FP8 ? landed : full;

@@ -88,16 +88,20 @@ struct Place {
     int32_t page;
     uint32_t row;
 };
-__device__ __forceinline__ Place place_of(const Cache& c, uint32_t b, uint32_t j) {
+// Looked up only: what looks ahead passes it through checked() where it is used, so that the load is not waited for
+// before.
+__device__ __forceinline__ Place look_up(const Cache& c, uint32_t b, uint32_t j) {
     const uint32_t q = c.page_tokens.div(j);
-    const int32_t page = c.table[b * c.table_stride + q];
-    Place p{page, j - q * c.page_tokens.d};
-    if ((uint32_t)page >= c.pages) {
+    return Place{c.table[b * c.table_stride + q], j - q * c.page_tokens.d};
+}
+__device__ __forceinline__ Place checked(const Cache& c, Place p) {
+    if ((uint32_t)p.page >= c.pages) {
         corrupt(c);
         p.page = -1;
     }
     return p;
 }
+__device__ __forceinline__ Place place_of(const Cache& c, uint32_t b, uint32_t j) { return checked(c, look_up(c, b, j)); }
 __device__ __forceinline__ char* k_row(const Cache& c, Place p, uint32_t h) {
     return c.k + p.page * c.k_page + h * c.k_head + p.row * c.k_token;
 }

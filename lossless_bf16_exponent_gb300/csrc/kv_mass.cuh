@@ -124,20 +124,24 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const __grid_cons
         constexpr uint32_t kES = FP8 ? 1 : 2, kLanes = DP * kES / 16;  // a row's chunks
         constexpr uint32_t kRing = C::kRing;
         const uint32_t c = lane % kLanes, live = D * kES / 16;
-        MassWalk cw(first, run.end);        // of the next tile to copy
+        MassWalk cw(first, run.end);  // of the next tile to copy
         uint32_t cs = 0, copied = 0;  // its place in the run, and how many are copied
+        Place ahead{0, 0};
+        bool used = false;  // whether the next tile has a token for this lane
+        auto find = [&]() {
+            const uint32_t j = (cw.u.tile + cs) * kMassTile + warp * 32 + lane;
+            used = cw.valid() && j < cw.u.span.old + cw.u.span.fresh;
+            if (used) ahead = look_up(p.cache, cw.u.b, j);
+        };
+        if (!TMA) find();
         auto copy = [&]() {
             if (TMA) return;
             if (ok && cw.valid()) {
                 // A warp takes 32 of the tile's rows: each lane finds one, then the warp copies them row by row.
                 if (!FP8 && copied >= kRing) ok = warp_wait(freed + 8 * (copied % kRing), (copied / kRing - 1) & 1);
                 if (FP8) __syncwarp();  // this warp has widened what the slot held: it copies only its own rows
-                const uint32_t j = (cw.u.tile + cs) * kMassTile + warp * 32 + lane;
-                const char* row = nullptr;
-                if (j < cw.u.span.old + cw.u.span.fresh) {
-                    const Place pl = place_of(p.cache, cw.u.b, j);
-                    if (pl.page >= 0) row = k_row(p.cache, pl, cw.u.h);
-                }
+                const Place now = used ? checked(p.cache, ahead) : Place{-1, 0};
+                const char* row = now.page >= 0 ? k_row(p.cache, now, cw.u.h) : nullptr;
                 char* slot = (FP8 ? raws : tiles) + (copied % kRing) * (FP8 ? C::kRawBytes : C::kTileBytes);
 #pragma unroll 8
                 for (uint32_t i = 0; i < kLanes; i++) {
@@ -152,6 +156,7 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const __grid_cons
                     cs = 0;
                     cw.next(p);
                 }
+                find();
             }
             copy_commit();
         };
@@ -238,7 +243,7 @@ __global__ void __launch_bounds__(kMassThreads, 1) mass_kernel(const __grid_cons
                 if (!ok) break;
                 if (lane == 0) bar_expect(done + 8 * s, now.bytes(maps));
                 __syncwarp();
-                now.copy(maps, &maps.k, h, smem_u32(ring + s * (FP8 ? C::kRawBytes : C::kTileBytes)), done + 8 * s);
+                now.copy(p, maps, &maps.k, h, smem_u32(ring + s * (FP8 ? C::kRawBytes : C::kTileBytes)), done + 8 * s);
                 i++;
             }
             for (uint32_t k = i > C::kRing ? i - C::kRing : 0; k < i; k++)  // no copy outlives the CTA

@@ -51,29 +51,26 @@ __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
 template <uint32_t TILE, uint32_t RB>
 struct TmaFeed {
     static constexpr uint32_t kWide = RB < 128 ? RB : 128, kBlocks = RB / kWide;
-    uint32_t page, row, live;  // of box `lane`; boxes of the tile that hold tokens in use
+    Place at;       // of box `lane`
+    uint32_t live;  // boxes of the tile that hold tokens in use
 
     __device__ __forceinline__ void find(const AttParams& p, const Maps& m, const Unit& u, bool any) {
         const uint32_t lane = threadIdx.x % 32, j0 = u.tile * TILE, end = u.span.old + u.span.fresh;
         live = any ? (min(TILE, end - j0) + m.box - 1) / m.box : 0;
-        page = p.cache.pages;  // not there: zeros
-        row = 0;
-        if (lane < live) {
-            const Place pl = place_of(p.cache, u.b, j0 + lane * m.box);
-            if (pl.page >= 0) {
-                page = (uint32_t)pl.page;
-                row = pl.row;
-            }
-        }
+        at = Place{0, 0};
+        if (lane < live) at = look_up(p.cache, u.b, j0 + lane * m.box);
     }
     __device__ __forceinline__ uint32_t bytes(const Maps& m) const { return live * m.box * RB; }
     // All lanes, after the barrier expects bytes(): boxes by blocks over the lanes.
-    __device__ __forceinline__ void copy(const Maps& m, const CUtensorMap* map, uint32_t head, uint32_t dst, uint32_t bar) const {
+    __device__ __forceinline__ void copy(const AttParams& p, const Maps& m, const CUtensorMap* map, uint32_t head, uint32_t dst,
+                                         uint32_t bar) const {
         const uint32_t lane = threadIdx.x % 32;
+        const Place here = lane < live ? checked(p.cache, at) : Place{-1, 0};
+        const uint32_t page = here.page < 0 ? p.cache.pages : (uint32_t)here.page, row = here.row;  // not there: zeros
         for (uint32_t i0 = 0; i0 < live * kBlocks; i0 += 32) {
-            const uint32_t i = i0 + lane, block = i % kBlocks, at = i / kBlocks;
-            const uint32_t pg = __shfl_sync(0xFFFFFFFFu, page, at % 32), rw = __shfl_sync(0xFFFFFFFFu, row, at % 32);
-            if (i < live * kBlocks) tma_box(dst + block * TILE * kWide + at * m.box * kWide, map, block * kWide, rw, head, pg, bar);
+            const uint32_t i = i0 + lane, block = i % kBlocks, n = i / kBlocks;
+            const uint32_t pg = __shfl_sync(0xFFFFFFFFu, page, n % 32), rw = __shfl_sync(0xFFFFFFFFu, row, n % 32);
+            if (i < live * kBlocks) tma_box(dst + block * TILE * kWide + n * m.box * kWide, map, block * kWide, rw, head, pg, bar);
         }
     }
 };
