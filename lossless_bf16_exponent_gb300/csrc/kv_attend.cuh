@@ -5,10 +5,11 @@
 // Bound: HBM, as long as the products of a tile take less time than its bytes
 // (4 D flop a row and token against 2 D bytes an element's width: up to about
 // 64 rows at the warp-level product's rate). So the kernel is built to keep
-// copies in flight: one CTA an SM, a warp that only copies (four where pages do
-// not allow bulk copies), eight that only compute, and a ring of stages between
-// them. The copies' pages are looked up one tile ahead, and the ring runs on
-// across unit boundaries.
+// copies in flight: one CTA an SM, four warps that only copy, 16 bytes a thread
+// and instruction (bulk tensor copies measured no better here: 241 / 242 us at
+// pages of 64 tokens, 159 / 120 us for E5M2 heads of 64), eight that only compute,
+// and a ring of stages between them. The copies' pages are looked up one tile
+// ahead, and the ring runs on across unit boundaries.
 //
 // The products have the cached tokens along M: S^T = K Q^T and O^T = V^T P^T,
 // 16 tokens (or 16 columns of V) by 8 rows. Eight rows of a decoding step waste
@@ -29,7 +30,7 @@
 #include <algorithm>
 #include <atomic>
 
-#include "kv_tma.cuh"
+#include "kv_attention.cuh"
 
 namespace uzkv {
 
@@ -53,11 +54,17 @@ struct AttCfg {
     static_assert(kKeys >= 16, "a product's tokens");
 };
 
-template <bool TMA>
-constexpr int kAttThreads = (8 + (TMA ? 1 : 4)) * 32;  // 8 warps that compute, the others copy
+constexpr int kAttThreads = 12 * 32;  // 8 warps that compute, 4 that copy
 
-template <typename QT, bool FP8, int DP, int RN, int WM, bool TMA>
-__global__ void __launch_bounds__(kAttThreads<TMA>, 1) attend_kernel(const __grid_constant__ AttParams p, const __grid_constant__ Maps maps) {
+// The launch's 384 x 168 registers, shared out anew: 4 warps x 32 x 72 + 8 x 32 x 216 are as many.
+template <bool COMPUTES>
+__device__ __forceinline__ void registers() {
+    if (COMPUTES) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+}
+
+template <typename QT, bool FP8, int DP, int RN, int WM>
+__global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_constant__ AttParams p) {
     using C = AttCfg<QT, FP8, DP, RN, WM>;
     using T = typename C::T;
     extern __shared__ __align__(1024) char smem[];
@@ -70,14 +77,14 @@ __global__ void __launch_bounds__(kAttThreads<TMA>, 1) attend_kernel(const __gri
     uzip::pdl_launch_dependents();
     if (tid == 0) {
         for (int s = 0; s < C::kStages; s++) {
-            bar_init(full + 8 * s, TMA ? 1 : 128);  // every copying thread
+            bar_init(full + 8 * s, 128);  // every copying thread
             bar_init(freed + 8 * s, 8);   // every computing warp
         }
         bar_init(merge, 8);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (!TMA && D < DP)  // columns past the head dimension stay zero: no copy writes them
-        for (uint32_t i = tid; i < C::kStages * C::kStage / 16; i += kAttThreads<TMA>) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
+    if (D < DP)  // columns past the head dimension stay zero: no copy writes them
+        for (uint32_t i = tid; i < C::kStages * C::kStage / 16; i += kAttThreads) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
     const Split split = split_of(p);
     const Run run = run_of(p, split, p.mtiles);
     Unit cur{};
@@ -86,27 +93,8 @@ __global__ void __launch_bounds__(kAttThreads<TMA>, 1) attend_kernel(const __gri
     __syncthreads();
     bool ok = true;
 
-    if (TMA && warp == 8) {
-        // ---- copies
-        TmaFeed<C::kTile, C::kRB> feed;
-        feed.find(p, maps, cur, cur.pos < run.end);
-        uint32_t i = 0;
-        for (; cur.pos < run.end && ok; i++) {
-            const TmaFeed<C::kTile, C::kRB> now = feed;
-            const uint32_t h = cur.h, s = i % C::kStages;
-            advance(p, cur, p.mtiles);
-            feed.find(p, maps, cur, cur.pos < run.end);
-            if (i >= C::kStages) ok = warp_wait(freed + 8 * s, (i / C::kStages - 1) & 1);
-            if (!ok) break;
-            if (lane == 0) bar_expect(full + 8 * s, 2 * now.bytes(maps));
-            __syncwarp();
-            const uint32_t ks = smem_u32(smem + s * C::kStage);
-            now.copy(p, maps, &maps.k, h, ks, full + 8 * s);
-            now.copy(p, maps, &maps.v, h, ks + C::kTile * C::kRB, full + 8 * s);
-        }
-        for (uint32_t k = i > C::kStages ? i - C::kStages : 0; k < i; k++)  // no copy outlives the CTA
-            ok &= warp_wait(full + 8 * (k % C::kStages), (k / C::kStages) & 1);
-    } else if (!TMA && warp >= 8) {
+    if (warp >= 8) {
+        registers<false>();
         // ---- copies: a warp takes a quarter of a tile's tokens
         constexpr uint32_t kMine = C::kTile / 4, kLanes = C::kRB / 16;
         const uint32_t w = warp - 8, c = lane % kLanes, live = D * (FP8 ? 1 : 2) / 16;
@@ -146,6 +134,7 @@ __global__ void __launch_bounds__(kAttThreads<TMA>, 1) attend_kernel(const __gri
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
         // ---- products
+        registers<true>();
         const uint32_t wm = warp % WM, wn = warp / WM, mykey = wn * C::kKeys;
         uint32_t q[RN][DP / 16][2];
         float o[DP / 16][RN][4], f[RN][2], ref[RN][2], sum[RN][2];  // rows 2 l and 2 l + 1 of each tile of eight
@@ -478,55 +467,47 @@ __global__ void __launch_bounds__(kAttThreads<TMA>, 1) attend_kernel(const __gri
     if (!ok && p.cache.status) *p.cache.status = UZIP_ERR_TIMEOUT;
 }
 
-template <typename QT, bool FP8, int DP, int RN, int WM, bool TMA>
-int launch_attend_by(AttParams& p, const Maps& maps, cudaStream_t stream) {
+template <typename QT, bool FP8, int DP, int RN, int WM>
+int launch_attend_as(AttParams& p, int sms, cudaStream_t stream) {
     using C = AttCfg<QT, FP8, DP, RN, WM>;
     static std::atomic<uint64_t> ready{0};  // a bit for each device whose limit is raised
     int dev = 0;
     UZIP_CUDA_TRY(cudaGetDevice(&dev));
     if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
-        UZIP_CUDA_TRY(cudaFuncSetAttribute(attend_kernel<QT, FP8, DP, RN, WM, TMA>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem));
+        UZIP_CUDA_TRY(cudaFuncSetAttribute(attend_kernel<QT, FP8, DP, RN, WM>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem));
         if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
-    attend_kernel<QT, FP8, DP, RN, WM, TMA><<<p.grid, kAttThreads<TMA>, C::kSmem, stream>>>(p, maps);
-    UZIP_CUDA_TRY(cudaGetLastError());
-    return UZIP_OK;
-}
-
-template <typename QT, bool FP8, int DP, int RN, int WM>
-int launch_attend_as(AttParams& p, const uzkv_cache_t* c, int sms, cudaStream_t stream) {
-    using C = AttCfg<QT, FP8, DP, RN, WM>;
     p.m = C::kM;
     p.mtiles = (p.rows + C::kM - 1) / C::kM;
     p.dp = DP;
     p.shift = C::kTile == 128 ? 7 : 6;
     p.unit_cost = 3;
     p.grid = std::min<uint32_t>((uint32_t)sms, kMaxAttGrid);
-    Maps maps{};
-    if (maps_of(p, c, C::kTile, 4096, &maps)) return launch_attend_by<QT, FP8, DP, RN, WM, true>(p, maps, stream);
-    return launch_attend_by<QT, FP8, DP, RN, WM, false>(p, maps, stream);
+    attend_kernel<QT, FP8, DP, RN, WM><<<p.grid, kAttThreads, C::kSmem, stream>>>(p);
+    UZIP_CUDA_TRY(cudaGetLastError());
+    return UZIP_OK;
 }
 
 // Rows a CTA takes at once: the fewest of 8 (heads up to 128), 16, 32 and 64 that hold all, else 64.
 template <typename QT, bool FP8, int DP>
-int launch_attend_rows(AttParams& p, const uzkv_cache_t* c, int sms, cudaStream_t s) {
+int launch_attend_rows(AttParams& p, int sms, cudaStream_t s) {
     if constexpr (DP <= 128) {
-        if (p.rows <= 8) return launch_attend_as<QT, FP8, DP, 1, 1>(p, c, sms, s);
-        if (p.rows <= 16) return launch_attend_as<QT, FP8, DP, 2, 1>(p, c, sms, s);
-        if (p.rows <= 32) return launch_attend_as<QT, FP8, DP, 2, 2>(p, c, sms, s);
-        return launch_attend_as<QT, FP8, DP, 2, 4>(p, c, sms, s);
+        if (p.rows <= 8) return launch_attend_as<QT, FP8, DP, 1, 1>(p, sms, s);
+        if (p.rows <= 16) return launch_attend_as<QT, FP8, DP, 2, 1>(p, sms, s);
+        if (p.rows <= 32) return launch_attend_as<QT, FP8, DP, 2, 2>(p, sms, s);
+        return launch_attend_as<QT, FP8, DP, 2, 4>(p, sms, s);
     } else {  // eight rows a warp: 16 would not leave registers for the output
-        if (p.rows <= 16) return launch_attend_as<QT, FP8, DP, 1, 2>(p, c, sms, s);
-        if (p.rows <= 32) return launch_attend_as<QT, FP8, DP, 1, 4>(p, c, sms, s);
-        return launch_attend_as<QT, FP8, DP, 1, 8>(p, c, sms, s);
+        if (p.rows <= 16) return launch_attend_as<QT, FP8, DP, 1, 2>(p, sms, s);
+        if (p.rows <= 32) return launch_attend_as<QT, FP8, DP, 1, 4>(p, sms, s);
+        return launch_attend_as<QT, FP8, DP, 1, 8>(p, sms, s);
     }
 }
 
 template <typename QT, bool FP8>
-int launch_attend(AttParams& p, const uzkv_cache_t* c, int sms, cudaStream_t s) {
-    if (p.cache.head_dim <= 64) return launch_attend_rows<QT, FP8, 64>(p, c, sms, s);
-    if (p.cache.head_dim <= 128) return launch_attend_rows<QT, FP8, 128>(p, c, sms, s);
-    return launch_attend_rows<QT, FP8, 256>(p, c, sms, s);
+int launch_attend(AttParams& p, int sms, cudaStream_t s) {
+    if (p.cache.head_dim <= 64) return launch_attend_rows<QT, FP8, 64>(p, sms, s);
+    if (p.cache.head_dim <= 128) return launch_attend_rows<QT, FP8, 128>(p, sms, s);
+    return launch_attend_rows<QT, FP8, 256>(p, sms, s);
 }
 
 }  // namespace uzkv

@@ -25,10 +25,9 @@ struct Maps {
 };
 
 // Maps of a cache for tiles of `tile` tokens; false where its pages do not allow them, or copies of at least `least`
-// bytes. A copy costs the accelerator about as much time as 2 KB take, so small ones fall behind the threads' copies.
-// Measured, bulk / threads, 16-bit heads of 128: attention of a decoding batch, 2 KB copies (pages of 16) 328 / 267 us,
-// 4 KB 252 / 266; many rows, 2 KB 297 / 399 us; mass, 2 KB 99 / 107 us; mass of E5M2 heads of 64, 1 KB 27.1 / 24.9,
-// 2 KB 23.7 / 24.9 us.
+// bytes: a copy costs the accelerator about as much time as 1 to 2 KB take, so smaller ones fall behind the threads'
+// copies. Measured, bulk / threads: many rows of 128, 2 KB copies 238 / 316 us; E5M2 of 64, 4 KB 39.7 / 48.3, 1 KB 54 / 47;
+// mass, rows of 128, 8 KB 90 / 96 us; E5M2 of 64, 4 KB 21.9 / 24.5, 1 KB 27.1 / 24.9 us.
 bool maps_of(const AttParams& p, const uzkv_cache_t* c, uint32_t tile, uint32_t least, Maps* m);
 
 __device__ __forceinline__ void tma_fetch_map(const CUtensorMap* m) {
