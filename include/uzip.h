@@ -78,7 +78,7 @@ enum uzip_status {
     UZIP_ERR_CHUNK = 3,     /* chunk not a multiple of 8 in [8, 65536]         */
     UZIP_ERR_CAPACITY = 4,  /* output or workspace buffer too small            */
     UZIP_ERR_CORRUPT = 5,   /* stream header or escape data inconsistent       */
-    UZIP_ERR_TIMEOUT = 6,   /* reserved: no entry point waits on the device    */
+    UZIP_ERR_TIMEOUT = 6,   /* a bounded wait in a kernel ran out (uzip_kv.h) */
     UZIP_ERR_CUDA = 7       /* a CUDA runtime call failed                      */
 };
 

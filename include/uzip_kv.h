@@ -23,8 +23,9 @@
  * page numbers of tokens in use below `pages`. A cache that breaks one is read
  * and written as far as it is in bounds (lengths and counts are clamped, a
  * page that does not exist reads as zeros and is not written), its outputs are
- * not trustworthy, and *d_status, if given, is set to UZIP_ERR_CORRUPT; no call
- * sets it to anything else.
+ * not trustworthy, and *d_status, if given, is set to UZIP_ERR_CORRUPT. Waits
+ * inside a kernel are bounded; if one ran out, which no input brings about, it
+ * is set to UZIP_ERR_TIMEOUT. No call sets it to anything else, or clears it.
  */
 #ifndef UZIP_KV_H
 #define UZIP_KV_H

@@ -58,7 +58,7 @@ extern "C" UZIP_API const char* uzip_status_string(int status) {
         case UZIP_ERR_CHUNK: return "chunk must be a multiple of 8 in [8, 65536]";
         case UZIP_ERR_CAPACITY: return "output or workspace buffer too small";
         case UZIP_ERR_CORRUPT: return "corrupt or inconsistent stream";
-        case UZIP_ERR_TIMEOUT: return "device-side wait timed out (not produced by this version)";
+        case UZIP_ERR_TIMEOUT: return "device-side wait timed out";
         case UZIP_ERR_CUDA: return "CUDA runtime error";
         default: return "unknown status";
     }

@@ -17,6 +17,11 @@
 //   O += P V         P from tensor memory, V from shared memory as it lies in the
 //                    cache (the product's N, the head dimension, contiguous)
 //
+// Measured: 512 rows of 128 over two contexts of 65,536 tokens (252 GFLOP): 239 us, 1.05 PFLOP/s, 55 % of the measured
+// cuBLAS rate; 85 rows of 64 over 12 E5M2 contexts of up to 5,001 tokens in pages of 48: 48 us, of 64: 40 us. One product
+// thread for both streams and score tiles of 128 columns, one a stream, took 297 us: each stream's products then wait
+// for its own softmax.
+//
 // Warps: 13 brings keys and values to a ring of operand tiles by bulk copies;
 // 0-3 widen E5M2, which lands as bytes, take non-finite values out of tiles
 // with new tokens, and do the copies where pages do not allow bulk ones; 4-7

@@ -17,6 +17,8 @@
 // loaded before the first is stored, the first of them before the angles are
 // computed. V is the widest of 16 bytes, 8 bytes and one element that the
 // rotary dimension, strides and addresses allow.
+// Measured: 16,388 tokens of 72 heads of 128, BF16: 98 us, 6.2 TB/s, 91 % of the measured copy rate; 4,095 new
+// tokens of 32 + 16 heads, half of each turned, to an E5M2 cache: 17 us (77 MB, floor 11).
 #include <algorithm>
 #include <type_traits>
 

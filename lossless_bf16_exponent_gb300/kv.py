@@ -211,7 +211,7 @@ class KVCache:
     of each sequence before the new ones of a call; the tensor is read on the
     device by each call, so advance it in place. ``status``: None or one int32
     CUDA element that a call sets to 5 (corrupt) when a length or page number is
-    out of range. A contiguous cache [sequences, heads, tokens, dim] is the
+    out of range (6 if a bounded wait inside a kernel ran out; never cleared). A contiguous cache [sequences, heads, tokens, dim] is the
     pool of whole-sequence pages with ``page_table = arange(sequences)[:, None]``."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, lengths: torch.Tensor,
