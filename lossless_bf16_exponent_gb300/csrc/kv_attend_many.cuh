@@ -230,15 +230,20 @@ __global__ void __launch_bounds__(kManyThreads, 1) attend_many_kernel(const __gr
                     if (!ok) break;
                     __syncwarp();
                     const char* raw = raws + (sent % kRing) * C::kRawBytes;
+                    constexpr uint32_t kBatch = kLanes < 8 ? kLanes : 8;  // all read before the first is written
                     if (c < live)
-#pragma unroll 4
-                        for (uint32_t x = 0; x < kLanes; x++) {
-                            const uint32_t R = warp * 32 + x * (32 / kLanes) + lane / kLanes;
-                            const uint4 v = *reinterpret_cast<const uint4*>(raw + row_chunk<DP>(kManyTile, R, c));
-                            *reinterpret_cast<uint4*>(tile + swizzled(kManyTile, R, 2 * c)) =
-                                make_uint4(uzip::prmt(v.x, 0, 0x1404), uzip::prmt(v.x, 0, 0x3424), uzip::prmt(v.y, 0, 0x1404), uzip::prmt(v.y, 0, 0x3424));
-                            *reinterpret_cast<uint4*>(tile + swizzled(kManyTile, R, 2 * c + 1)) =
-                                make_uint4(uzip::prmt(v.z, 0, 0x1404), uzip::prmt(v.z, 0, 0x3424), uzip::prmt(v.w, 0, 0x1404), uzip::prmt(v.w, 0, 0x3424));
+#pragma unroll
+                        for (uint32_t x0 = 0; x0 < kLanes; x0 += kBatch) {
+                            uint4 v[kBatch];
+#pragma unroll
+                            for (uint32_t x = 0; x < kBatch; x++)
+                                v[x] = *reinterpret_cast<const uint4*>(raw + row_chunk<DP>(kManyTile, warp * 32 + (x0 + x) * (32 / kLanes) + lane / kLanes, c));
+#pragma unroll
+                            for (uint32_t x = 0; x < kBatch; x++) {
+                                const uint32_t R = warp * 32 + (x0 + x) * (32 / kLanes) + lane / kLanes;
+                                *reinterpret_cast<uint4*>(tile + swizzled(kManyTile, R, 2 * c)) = widen(v[x].x, v[x].y);
+                                *reinterpret_cast<uint4*>(tile + swizzled(kManyTile, R, 2 * c + 1)) = widen(v[x].z, v[x].w);
+                            }
                         }
                 }
                 if (clean) {

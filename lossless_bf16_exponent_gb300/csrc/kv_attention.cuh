@@ -154,6 +154,10 @@ struct Run {
 __device__ __forceinline__ Run run_of(const AttParams& p, const Split& s, uint32_t mtiles) {
     const uint64_t total = s.all * p.cache.kv_heads * mtiles, shares = min(total, (uint64_t)p.grid);  // no share is empty
     if (blockIdx.x >= shares) return Run{0, 0};
+    if (total * shares >> 32 == 0) {  // the common case, without 64-bit division
+        const uint32_t t = (uint32_t)total, n = (uint32_t)shares;
+        return Run{t * blockIdx.x / n, t * (blockIdx.x + 1) / n};
+    }
     return Run{total * blockIdx.x / shares, total * (blockIdx.x + 1) / shares};
 }
 
@@ -281,6 +285,11 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) { retur
 // One arrival once this thread's copies so far have landed; counted among the barrier's own.
 __device__ __forceinline__ void bar_arrive_copies(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// Eight E5M2 bytes to FP16.
+__device__ __forceinline__ uint4 widen(uint32_t a, uint32_t b) {
+    return make_uint4(uzip::prmt(a, 0, 0x1404), uzip::prmt(a, 0, 0x3424), uzip::prmt(b, 0, 0x1404), uzip::prmt(b, 0, 0x3424));
 }
 
 // NaN and infinities of a pair of values (FP16 or BF16 patterns) become zero; whether there were any.
