@@ -18,7 +18,7 @@
 //                    cache (the product's N, the head dimension, contiguous)
 //
 // Measured: 512 rows of 128 over two contexts of 65,536 tokens (252 GFLOP): 239 us, 1.05 PFLOP/s, 55 % of the measured
-// cuBLAS rate; 85 rows of 64 over 12 E5M2 contexts of up to 5,001 tokens in pages of 48: 48 us, of 64: 40 us. One product
+// cuBLAS rate; 85 rows of 64 over 12 E5M2 contexts of up to 5,001 tokens in pages of 48: 46 us, of 64: 40 us. One product
 // thread for both streams and score tiles of 128 columns, one a stream, took 297 us: each stream's products then wait
 // for its own softmax.
 //

@@ -10,7 +10,7 @@
 //
 // Bound: HBM for few rows, else the sums: an exponential a row and token (32 a clock on an SM) and what surrounds it.
 // Measured: 256 rows of 128 over 131,072 tokens of 8 heads: 90 us (floor 41 by bytes, 36 by products); 20 rows of 64 over 24
-// E5M2 sequences of up to 3,001 tokens: 25 us, most of it startup and the units' ends.
+// E5M2 sequences of up to 3,001 tokens: 23 us, most of it startup and the units' ends.
 //
 // One CTA an SM takes a run of tiles (kv_attention.cuh's split). Its warps: 13
 // brings keys to a ring of operand tiles by bulk copies; 0-3 load the rows'
