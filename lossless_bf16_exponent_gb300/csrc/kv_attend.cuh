@@ -479,6 +479,10 @@ int launch_attend_as(AttParams& p, int sms, cudaStream_t stream) {
     UZIP_CUDA_TRY(cudaGetDevice(&dev));
     if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
         UZIP_CUDA_TRY(cudaFuncSetAttribute(attend_kernel<QT, FP8, DP, RN, WM>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem));
+        // The shares that registers() hands out must be what the kernel is launched with, or it would wait forever.
+        cudaFuncAttributes have;
+        UZIP_CUDA_TRY(cudaFuncGetAttributes(&have, attend_kernel<QT, FP8, DP, RN, WM>));
+        if (have.numRegs * kAttThreads < 4 * 32 * 72 + 8 * 32 * 216) return UZIP_ERR_CUDA;
         if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
     p.m = C::kM;
