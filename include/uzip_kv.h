@@ -154,8 +154,8 @@ UZIP_API int uzkv_attention_mass(const uzkv_rows_t *q, const float *d_lse, uint3
  *   d_kept         [sequences][kv_heads][keep] int32 slots, contiguous, -1 past the kept.
  *   d_mass_out     [sequences][kv_heads][keep] floats, contiguous, 0 past the kept.
  *   d_lengths_out  [sequences] int32: min(lengths[b], keep).
- *   keep           at least max(1, sink + recent).
- * Async. */
+ *   keep           at least max(1, sink + recent), below 2^27.
+ * sequences * kv_heads is at most 65,535. Async. */
 UZIP_API int uzkv_evict(const uzkv_cache_t *cache, const float *d_mass, int64_t mass_stride_b, int64_t mass_stride_h,
                         uint32_t slots, uint32_t keep, uint32_t sink, uint32_t recent, const uzkv_rows_t *out_k,
                         const uzkv_rows_t *out_v, int32_t *d_kept, float *d_mass_out, int32_t *d_lengths_out,
