@@ -24,6 +24,7 @@
 #include <algorithm>
 #include <atomic>
 
+#include "kv_index.cuh"
 #include "kv_internal.cuh"
 
 namespace cg = cooperative_groups;
@@ -283,7 +284,8 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const __grid_constan
     const uint32_t total = p.keep * p.row_chunks;
     const int32_t* kept = p.kept + (uint64_t)row * p.keep;
     uzip::pdl_wait();
-    for (uint32_t i = blockIdx.x * kPackThreads + threadIdx.x; i < total; i += gridDim.x * kPackThreads) {
+    // total goes up to 2^32 - 32 (host check), so an index one step further may pass 2^32
+    for (uint32_t i = blockIdx.x * kPackThreads + threadIdx.x; i < total; i = next_below(i, gridDim.x * kPackThreads, total)) {
         const uint32_t r = i / p.row_chunks, c = i % p.row_chunks * 16;
         const int32_t j = kept[r];
         uint4 k = make_uint4(0, 0, 0, 0), v = k;
