@@ -28,6 +28,24 @@ def _sp(device=None) -> int:
     return torch.cuda.current_stream(device).cuda_stream
 
 
+# Index of the current device, without torch's wrapper where it is there.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _call(index: int, f, *args) -> None:
+    """Call the library's ``f(*args, stream)`` for tensors of device ``index``,
+    on that device's current stream and with that device current: the library
+    launches on, and asks about, the current device, and the handle of a default
+    stream is the same for every device."""
+    if index == _current_device():
+        rc = f(*args, _sp(index))
+    else:
+        with torch.cuda.device(index):
+            rc = f(*args, _sp(index))
+    if rc:
+        check(rc, f.__name__)
+
+
 def _p(t: torch.Tensor | None):
     return t.data_ptr() if t is not None else None
 

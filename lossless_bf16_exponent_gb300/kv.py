@@ -19,9 +19,8 @@ from dataclasses import dataclass
 
 import torch
 
-from . import _lib
-from ._lib import check
-from .codec import _sp, load
+from . import _lib, codec
+from .codec import _call, _sp, load
 
 # Calls of a few microseconds on the GPU are bound by the host: each call looks
 # every attribute up once, and tensors go to the C ABI as packed structures.
@@ -176,10 +175,8 @@ def _rotate(x, positions, plan, out, backward):
     if b * t * heads * d == 0:
         return out
     turns, rotary_dim, layout, magnitude = plan.args
-    rc = load().uzkv_rotary(rx, ro, kind, b, t, heads, d, positions.data_ptr(), step, turns, rotary_dim, layout,
-                            magnitude, backward, _sp(index))
-    if rc:
-        check(rc, "uzkv_rotary")
+    _call(index, load().uzkv_rotary, rx, ro, kind, b, t, heads, d, positions.data_ptr(), step, turns, rotary_dim, layout,
+          magnitude, backward)
     return out
 
 
@@ -301,10 +298,8 @@ def rotary_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: 
     if t * heads == 0:
         return out
     turns, rotary_dim, layout, magnitude = plan.args
-    rc = load().uzkv_rotary_append(rq, rk, rv, ro, _FLOATS[dtype], t, heads, positions.data_ptr(), step, turns, rotary_dim,
-                                   layout, magnitude, _counts(counts, cache), cache._ref, _sp(index))
-    if rc:
-        check(rc, "uzkv_rotary_append")
+    _call(index, load().uzkv_rotary_append, rq, rk, rv, ro, _FLOATS[dtype], t, heads, positions.data_ptr(), step, turns,
+          rotary_dim, layout, magnitude, _counts(counts, cache), cache._ref)
     return out
 
 
@@ -372,11 +367,19 @@ def tree_attention_workspace_bytes(cache: KVCache, tokens: int, heads: int) -> i
 _scratch = threading.local()
 
 
+def _capturing(index: int) -> bool:
+    """Whether the current stream of device ``index`` is being captured in a graph."""
+    if index == codec._current_device():
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.device(index):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _workspace(cache: KVCache, size: int) -> torch.Tensor:
     """Scratch of at least ``size`` bytes for a call on the current stream: one
     buffer a host thread and stream, which its calls use one after the other. A
     call under graph capture gets its own, which the graph then holds."""
-    if torch.cuda.is_current_stream_capturing():
+    if _capturing(cache.index):
         return torch.empty(size, dtype=torch.uint8, device=cache.device)
     buffers = _scratch.__dict__
     key = (cache.index, _sp(cache.index))
@@ -411,11 +414,8 @@ def tree_attention(q: torch.Tensor, cache: KVCache, mask: torch.Tensor | None = 
         workspace = _workspace(cache, tree_attention_workspace_bytes(cache, t, heads))
     elif not _tensor(workspace, "workspace", torch.uint8, None, cache.device).is_contiguous():
         raise ValueError("workspace: expected a contiguous tensor")
-    rc = load().uzkv_tree_attention(rq, ro, at_lse, _FLOATS[q.dtype], t, heads, address, stride, _counts(counts, cache),
-                                    d ** -0.5 if scale is None else scale, cache._ref, workspace.data_ptr(),
-                                    workspace.numel(), _sp(cache.index))
-    if rc:
-        check(rc, "uzkv_tree_attention")
+    _call(cache.index, load().uzkv_tree_attention, rq, ro, at_lse, _FLOATS[q.dtype], t, heads, address, stride,
+          _counts(counts, cache), d ** -0.5 if scale is None else scale, cache._ref, workspace.data_ptr(), workspace.numel())
     return out, lse
 
 
@@ -454,11 +454,9 @@ def attention_mass(q: torch.Tensor, cache: KVCache, lse: torch.Tensor, mask: tor
         if mass.stride() != (sb, sh, sn):
             raise ValueError("mass: expected the strides of out")
         at_mass = mass.data_ptr()
-    rc = load().uzkv_attention_mass(rq, at_lse, _FLOATS[q.dtype], t, heads, address, stride, _counts(counts, cache),
-                                    at_weights, d ** -0.5 if scale is None else scale, cache._ref, at_mass, decay,
-                                    out.data_ptr(), sb, sh, shape[2], _sp(cache.index))
-    if rc:
-        check(rc, "uzkv_attention_mass")
+    _call(cache.index, load().uzkv_attention_mass, rq, at_lse, _FLOATS[q.dtype], t, heads, address, stride,
+          _counts(counts, cache), at_weights, d ** -0.5 if scale is None else scale, cache._ref, at_mass, decay,
+          out.data_ptr(), sb, sh, shape[2])
     return out
 
 
@@ -510,10 +508,8 @@ def evict(cache: KVCache, mass: torch.Tensor, keep: int, sink: int = 0, recent: 
     kept = torch.empty((b, heads, keep), dtype=torch.int32, device=device)
     mass_out = torch.empty((b, heads, keep), dtype=torch.float32, device=device)
     lengths = torch.empty((b,), dtype=torch.int32, device=device)
-    rc = load().uzkv_evict(cache._ref, mass.data_ptr(), sb, sh, shape[2], keep, sink, recent, rk, rv, kept.data_ptr(),
-                           mass_out.data_ptr(), lengths.data_ptr(), _sp(cache.index))
-    if rc:
-        check(rc, "uzkv_evict")
+    _call(cache.index, load().uzkv_evict, cache._ref, mass.data_ptr(), sb, sh, shape[2], keep, sink, recent, rk, rv,
+          kept.data_ptr(), mass_out.data_ptr(), lengths.data_ptr())
     return Packed(out_k, out_v, mass_out, kept, lengths)
 
 
