@@ -206,10 +206,14 @@ class KVCache:
     strides multiples of 16 bytes). ``page_table`` int32 [sequences, pages of a
     sequence], read for tokens in use only. ``lengths`` int32 [sequences]: tokens
     of each sequence before the new ones of a call; the tensor is read on the
-    device by each call, so advance it in place. ``status``: None or one int32
-    CUDA element that a call sets to 5 (corrupt) when a length or page number is
-    out of range (6 if a bounded wait inside a kernel ran out; never cleared). A contiguous cache [sequences, heads, tokens, dim] is the
-    pool of whole-sequence pages with ``page_table = arange(sequences)[:, None]``."""
+    device by each call, so advance it in place (``cache.lengths += n``). Every
+    call passes on the addresses taken here, so the attributes cannot be set to
+    other tensors, nor may a tensor's storage be exchanged: make a new KVCache.
+    ``status``: None or one int32 CUDA element that a call sets to 5 (corrupt)
+    when a length or page number is out of range (6 if a bounded wait inside a
+    kernel ran out; never cleared). A contiguous cache [sequences, heads, tokens,
+    dim] is the pool of whole-sequence pages with
+    ``page_table = arange(sequences)[:, None]``."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, lengths: torch.Tensor,
                  status: torch.Tensor | None = None):
@@ -241,6 +245,15 @@ class KVCache:
             k.shape[3], page_table.shape[0], page_table.shape[1], _DTYPES[k.dtype], 0)
         self._ref = ctypes.byref(self._c)
         self._workspace_bytes: dict[tuple[int, int], int] = {}  # by (tokens, heads)
+
+    def __setattr__(self, name, value):
+        # The same object again is what `cache.lengths += n` assigns.
+        if self.__dict__.get(name, value) is not value:
+            raise AttributeError(f"{name}: a cache keeps its tensors; change them in place or make a new KVCache")
+        self.__dict__[name] = value
+
+    def __delattr__(self, name):
+        raise AttributeError(f"{name}: a cache keeps its tensors")
 
 
 def _new_rows(x: torch.Tensor, what: str, cache: KVCache, heads: int | None = None) -> bytes:

@@ -127,3 +127,22 @@ def test_calls_run_on_the_tensors_device(bench, index):
             assert [(n, d) for n, d, _ in bench.calls] == [(name, index)]
             assert bench.calls[0][2][-1] == 1000 + index and bench.current == current
             assert all(d == index for d in bench.asked)
+
+
+def test_a_cache_keeps_its_tensors(bench):
+    """What a call passes on are the addresses taken when the cache was made: its tensors cannot be exchanged under it,
+    and advancing them in place goes on to work."""
+    cache = make()
+    for name in ("k", "v", "page_table", "lengths", "status", "dtype", "capacity", "_c"):
+        before = getattr(cache, name)
+        with pytest.raises(AttributeError):
+            setattr(cache, name, zeros(2, dtype=I32))
+        assert getattr(cache, name) is before
+    with pytest.raises(AttributeError):
+        del cache.lengths
+    lengths = torch.zeros(2, dtype=I32)
+    cache.lengths.host.copy_(lengths)
+    cache.lengths = cache.lengths  # what an in-place operator assigns
+    uz.evict(cache, zeros(2, 2, 32, dtype=F32), 8)
+    reached = ctypes.cast(bench.calls[0][2][0], ctypes.POINTER(uz._lib.KvCache)).contents
+    assert reached.d_lengths == cache.lengths.data_ptr()
