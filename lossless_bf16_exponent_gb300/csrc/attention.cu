@@ -38,17 +38,10 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
     total *= units;
     const uint64_t start = before * units + ((uint64_t)h * p.mtiles + mt) * width_of(p, tiles) + p.unit_cost;  // of its tiles
     const uint64_t shares = min(total, (uint64_t)p.grid);
-    // CTA c has the positions from total * c / shares on
     uint32_t c0 = 0, c1 = 0;
     if (tiles) {
-        const uint64_t first = (start + 1) * shares - 1, last = (start + tiles) * shares - 1;
-        if (last >> 32) {
-            c0 = (uint32_t)(first / total);
-            c1 = (uint32_t)(last / total);
-        } else {  // the common case, without 64-bit division
-            c0 = (uint32_t)first / (uint32_t)total;
-            c1 = (uint32_t)last / (uint32_t)total;
-        }
+        c0 = share_of(start, shares, total);
+        c1 = share_of(start + tiles - 1, shares, total);
     }
     uzip::pdl_wait();
     if (tiles && c0 == c1) return;

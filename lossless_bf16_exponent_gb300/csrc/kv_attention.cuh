@@ -12,6 +12,7 @@
 
 #include <type_traits>
 
+#include "kv_index.cuh"
 #include "kv_internal.cuh"
 
 namespace uzkv {
@@ -112,8 +113,8 @@ __device__ __forceinline__ Unit unit_at(const AttParams& p, const Split& s, uint
             const uint32_t width = (uint32_t)__shfl_sync(0xFFFFFFFFu, mine, l);
             u.b = b0 + l;
             u.tiles = width - p.unit_cost;
-            const uint32_t in = (uint32_t)(at - start);  // within one sequence
-            const uint32_t unit = in / width, off = in - unit * width;
+            const uint64_t in = at - start;  // within one sequence
+            const uint32_t unit = (uint32_t)divide(in, width), off = (uint32_t)(in - (uint64_t)unit * width);
             u.tile = off > p.unit_cost ? off - p.unit_cost : 0;
             u.pos = at + (off < p.unit_cost ? p.unit_cost - off : 0);
             u.h = unit / mtiles;
