@@ -107,7 +107,7 @@ UZIP_API int uzkv_rotary_append(const uzkv_rows_t *q, const uzkv_rows_t *k, cons
  *   q, out         [sequences][tokens][q_heads][head_dim], dtype BF16 or FP16;
  *                  16-byte aligned rows.
  *   d_lse          NULL or [sequences][tokens][q_heads] floats, contiguous.
- *   tokens         1 .. UZKV_MAX_NEW_TOKENS.
+ *   tokens         1 .. UZKV_MAX_NEW_TOKENS; sequences * tokens * q_heads below 2^31.
  *   d_mask         NULL or [sequences][tokens][ceil(tokens / 64)] words, a
  *                  sequence's rows mask_stride_b words apart (0: one tree for all).
  *   cache          dtype of q or E5M2; head_dim a multiple of 16 bytes' worth of

@@ -94,7 +94,6 @@ template <typename QT>
 int launch_join(const Params& p, cudaStream_t s) {
     const uint64_t warps = (uint64_t)p.cache.sequences * p.cache.kv_heads * p.rows;
     const uint64_t grid = (warps + kThreads / 32 - 1) / (kThreads / 32);
-    if (warps > 0x7FFFFFFFull) return UZIP_ERR_ARG;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(kThreads);
@@ -165,6 +164,8 @@ extern "C" UZIP_API int uzkv_tree_attention(const uzkv_rows_t* q, const uzkv_row
     if (!rows_aligned16(p.out) || !aligned16(d_workspace) || (reinterpret_cast<uintptr_t>(d_lse) & 3)) return UZIP_ERR_ALIGN;
     if (workspace_bytes < uzkv_tree_attention_workspace_bytes(p.cache.sequences, tokens, q_heads, p.cache.kv_heads, p.cache.head_dim))
         return UZIP_ERR_CAPACITY;
+    // The join's grid: a warp a query row. Refused before anything is enqueued.
+    if ((uint64_t)p.cache.sequences * p.cache.kv_heads * p.rows > 0x7FFFFFFFull) return UZIP_ERR_ARG;
     p.lse = d_lse;
     p.partial = static_cast<float*>(d_workspace);
     int sms = 0;
