@@ -8,6 +8,11 @@ the C ABI cannot see (devices, types, shapes, strides); a refusal is a
 ``ValueError`` raised before anything is enqueued, a status of the library an
 :class:`UzipError`. Work goes to the current CUDA stream of the tensors'
 device and nothing synchronises.
+
+:func:`rotary` and :func:`rotary_backward` take part in autograd. The other
+operators have no gradient and refuse inputs whose gradient is being recorded
+(``torch.no_grad()`` or ``detach()``), as every operator does where ``out`` is
+given.
 """
 from __future__ import annotations
 
@@ -18,6 +23,7 @@ import threading
 from dataclasses import dataclass
 
 import torch
+from torch.autograd.graph import increment_version
 
 from . import _lib, codec
 from .codec import _call, _sp, load
@@ -68,6 +74,21 @@ def _writable(x: torch.Tensor, what: str) -> torch.Tensor:
         if n > 1:
             expect = s * (n - 1) + expect
     return x
+
+
+def _no_gradient(what: str, *tensors) -> None:
+    """Refuse tensors whose gradient would be cut without a word."""
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        raise ValueError(f"{what}: has no gradient; call it under torch.no_grad() or on detached tensors")
+
+
+def _given(out: torch.Tensor, what: str) -> torch.Tensor:
+    """Check a caller's output, which is written past autograd's knowledge: what was saved of it is no longer valid."""
+    _writable(out, what)
+    if out.requires_grad:
+        _no_gradient(what, out)
+    increment_version(out)
+    return out
 
 
 # ----------------------------------------------------------------- rotary
@@ -150,7 +171,28 @@ def _positions(positions, b, t, index) -> int:
     return sb
 
 
+class _Rotary(torch.autograd.Function):
+    """The turn (or, backward, the turn back), whose gradient is the other one."""
+
+    @staticmethod
+    def forward(ctx, x, positions, plan, backward):
+        ctx.save_for_backward(positions)
+        ctx.plan, ctx.backward_ = plan, backward
+        return _rotate(x, positions, plan, None, backward)
+
+    @staticmethod
+    def backward(ctx, grad):
+        (positions,) = ctx.saved_tensors
+        if grad.stride(-1) != 1:  # a sum's gradient is one element expanded
+            grad = grad.contiguous()
+        return _rotate(grad, positions, ctx.plan, None, 1 - ctx.backward_), None, None, None
+
+
 def _rotate(x, positions, plan, out, backward):
+    if x.requires_grad and torch.is_grad_enabled():
+        if out is not None:
+            _no_gradient("out", x)
+        return _Rotary.apply(x, positions, plan, backward)
     kind, shape, index = _FLOATS.get(x.dtype), x.shape, x.get_device()
     if kind is None:
         raise ValueError(f"expected bfloat16, float16 or float32 values, got {x.dtype}")
@@ -165,14 +207,15 @@ def _rotate(x, positions, plan, out, backward):
         raise ValueError("plan: on another device")
     b, t, heads, d = shape
     step = _positions(positions, b, t, index)
-    rx = _rows(x, "x")
+    empty = b * t * heads * d == 0
+    rx = None if empty else _rows(x, "x")  # no rule for the strides of nothing
     if out is None:
         out = torch.empty((b, t, heads, d), dtype=x.dtype, device=plan.device)
         ro = _pack_rows(out.data_ptr(), t * heads * d, heads * d, d)
     else:
-        _writable(_tensor(out, "out", x.dtype, shape, x.device), "out")
+        _given(_tensor(out, "out", x.dtype, shape, x.device), "out")
         ro = _rows(out, "out")
-    if b * t * heads * d == 0:
+    if empty:
         return out
     turns, rotary_dim, layout, magnitude = plan.args
     _call(index, load().uzkv_rotary, rx, ro, kind, b, t, heads, d, positions.data_ptr(), step, turns, rotary_dim, layout,
@@ -185,14 +228,16 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, plan: RotaryPlan,
     """Turn the pairs of each head of ``x`` ([tokens, heads, dim] or
     [sequences, tokens, heads, dim], bfloat16, float16 or float32, rows
     contiguous) by its token's position (int32). Elements past the plan's
-    rotary_dim are copied. ``out`` may be ``x``."""
+    rotary_dim are copied. ``out`` may be ``x``. Differentiable in ``x`` where
+    ``out`` is not given."""
     return _rotate(x, positions, plan, out, 0)
 
 
 def rotary_backward(grad: torch.Tensor, positions: torch.Tensor, plan: RotaryPlan,
                     out: torch.Tensor | None = None) -> torch.Tensor:
     """Gradient of :func:`rotary`'s input from that of its output: the same
-    turn, backwards."""
+    turn, backwards. What autograd calls for :func:`rotary`; for training loops
+    that keep their own tape. Differentiable like it."""
     return _rotate(grad, positions, plan, out, 1)
 
 
@@ -231,6 +276,8 @@ class KVCache:
             _dense(status, "status", torch.int32, torch.Size([1]), k.device)
         for t, what in ((k, "k"), (v, "v")):
             _writable(t, what)
+            if t.requires_grad:
+                raise ValueError(f"{what}: a cache is written past autograd's knowledge; give detached tensors")
             if t.shape[3] > 1 and t.stride(3) != 1:
                 raise ValueError(f"{what}: elements of a row must be contiguous")
         self.k, self.v, self.page_table, self.lengths, self.status = k, v, page_table, lengths, status
@@ -276,7 +323,7 @@ def _new_out(out: torch.Tensor | None, q: torch.Tensor, b: int, t: int, heads: i
     if out is None:
         out = torch.empty((b, t, heads, d), dtype=q.dtype, device=device)
         return out, _pack_rows(out.data_ptr(), t * heads * d, heads * d, d)
-    _writable(_tensor(out, "out", q.dtype, q.shape, device), "out")
+    _given(_tensor(out, "out", q.dtype, q.shape, device), "out")
     return out, _rows(out, "out")
 
 
@@ -299,6 +346,8 @@ def rotary_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: 
     past ``counts`` give zero queries and are not stored. ``out`` may be ``q``.
     Advancing ``cache.lengths`` is the caller's, once the tokens are accepted."""
     kv_heads, index = cache.kv_heads, cache.index
+    if q.requires_grad or k.requires_grad or v.requires_grad:
+        _no_gradient("rotary_append", q, k, v)
     rq, rk, rv = _new_rows(q, "q", cache), _new_rows(k, "k", cache, kv_heads), _new_rows(v, "v", cache, kv_heads)
     b, t, heads, d = q.shape
     dtype = q.dtype
@@ -352,6 +401,8 @@ def _mask(mask, cache, t):
 
 def _query(q: torch.Tensor, cache: KVCache):
     """Check queries of new tokens; their rows and shape."""
+    if q.requires_grad:
+        _no_gradient("q", q)
     rows = _new_rows(q, "q", cache)
     b, t, heads, d = q.shape
     if not 1 <= t <= MAX_NEW_TOKENS:
@@ -423,6 +474,7 @@ def tree_attention(q: torch.Tensor, cache: KVCache, mask: torch.Tensor | None = 
         at_lse = lse.data_ptr()
     else:
         at_lse = _floats(lse, "lse", (b, t, heads), cache)
+        _given(lse, "lse")
     if workspace is None:
         workspace = _workspace(cache, tree_attention_workspace_bytes(cache, t, heads))
     elif not _tensor(workspace, "workspace", torch.uint8, None, cache.device).is_contiguous():
@@ -448,12 +500,14 @@ def attention_mass(q: torch.Tensor, cache: KVCache, lse: torch.Tensor, mask: tor
     address, stride = _mask(mask, cache, t) if mask is not None else (None, 0)
     at_lse = _floats(lse, "lse", (b, t, heads), cache)
     at_weights = _floats(weights, "weights", (b, t), cache) if weights is not None else None
+    if lse.requires_grad or (weights is not None and weights.requires_grad) or (mass is not None and mass.requires_grad):
+        _no_gradient("attention_mass", lse, weights, mass)
     kv_heads = cache.kv_heads
     if out is None:
         out = torch.empty(mass.shape if mass is not None else (b, kv_heads, cache.capacity), dtype=torch.float32,
                           device=cache.device)
     else:
-        _writable(_tensor(out, "out", torch.float32, None, cache.device), "out")
+        _given(_tensor(out, "out", torch.float32, None, cache.device), "out")
     shape = out.shape
     if len(shape) != 3 or shape[0] != b or shape[1] != kv_heads or not 1 <= shape[2] <= cache.capacity:
         raise ValueError(f"out: expected [{b}, {kv_heads}, 1 to {cache.capacity}], got {tuple(shape)}")
@@ -506,6 +560,8 @@ def evict(cache: KVCache, mass: torch.Tensor, keep: int, sink: int = 0, recent: 
     sb, sh, sn = mass.stride()
     if shape[2] > 1 and sn != 1:
         raise ValueError("mass: expected contiguous rows")
+    if mass.requires_grad:
+        _no_gradient("evict", mass)
     if keep < 1 or sink < 0 or recent < 0 or sink + recent > keep:
         raise ValueError("expected keep >= 1 and 0 <= sink + recent <= keep")
     device = cache.device
@@ -516,7 +572,7 @@ def evict(cache: KVCache, mass: torch.Tensor, keep: int, sink: int = 0, recent: 
         raise ValueError("give both out_k and out_v or neither")
     else:
         for x, what in ((out_k, "out_k"), (out_v, "out_v")):
-            _writable(_tensor(x, what, cache.dtype, (b, heads, keep, d), device), what)
+            _given(_tensor(x, what, cache.dtype, (b, heads, keep, d), device), what)
         rk, rv = _rows(out_k, "out_k"), _rows(out_v, "out_v")
     kept = torch.empty((b, heads, keep), dtype=torch.int32, device=device)
     mass_out = torch.empty((b, heads, keep), dtype=torch.float32, device=device)

@@ -82,6 +82,8 @@ class Bench:
         monkeypatch.setattr(torch.cuda, "device", device)
         monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", capturing)
         monkeypatch.setattr(torch, "empty", empty)
+        self.bumped = []
+        monkeypatch.setattr(kv, "increment_version", self.bumped.append, raising=False)
 
 
 @pytest.fixture
@@ -146,3 +148,45 @@ def test_a_cache_keeps_its_tensors(bench):
     uz.evict(cache, zeros(2, 2, 32, dtype=F32), 8)
     reached = ctypes.cast(bench.calls[0][2][0], ctypes.POINTER(uz._lib.KvCache)).contents
     assert reached.d_lengths == cache.lengths.data_ptr()
+
+
+def test_a_gradient_is_not_cut_without_a_word(bench):
+    """Operators without a gradient refuse inputs whose gradient is being recorded, as does an `out`; without recording
+    they take them, and a given output counts as written."""
+    cache, pos, plan = make(), zeros(2, 3, dtype=I32), plan_on(0)
+    q, new, lse, mass = zeros(2, 3, 4, 64), zeros(2, 3, 2, 64), zeros(2, 3, 4, dtype=F32), zeros(2, 2, 32, dtype=F32)
+    weights, out, wide = zeros(2, 3, dtype=F32), zeros(2, 3, 4, 64), zeros(2, 2, 8, 64)
+    calls = {
+        "q": [lambda: uz.tree_attention(q, cache), lambda: uz.attention_mass(q, cache, lse), lambda: uz.rotary(q, pos, plan, out=out),
+              lambda: uz.rotary_append(q, new, new, pos, plan, cache), lambda: uz.rotary_backward(q, pos, plan, out=q)],
+        "new": [lambda: uz.rotary_append(q, new, new, pos, plan, cache)],
+        "lse": [lambda: uz.attention_mass(q, cache, lse), lambda: uz.tree_attention(q, cache, lse=lse)],
+        "weights": [lambda: uz.attention_mass(q, cache, lse, weights=weights)],
+        "mass": [lambda: uz.attention_mass(q, cache, lse, mass=mass), lambda: uz.evict(cache, mass, 8)],
+        "out": [lambda: uz.rotary(q, pos, plan, out=out), lambda: uz.tree_attention(q, cache, out=out),
+                lambda: uz.rotary_append(q, new, new, pos, plan, cache, out=out)],
+        "wide": [lambda: uz.evict(cache, mass, 8, out_k=wide, out_v=zeros(2, 2, 8, 64))]}
+    named = dict(q=q, new=new, lse=lse, weights=weights, mass=mass, out=out, wide=wide)
+    for name, those in calls.items():
+        for call in those:
+            named[name].host.requires_grad_(True)
+            bench.calls.clear()
+            with pytest.raises(ValueError, match="gradient"):
+                call()
+            assert not bench.calls
+            with torch.no_grad():
+                call()
+            named[name].host.requires_grad_(False)
+            call()
+            assert len(bench.calls) == 2
+    pool = zeros(4, 2, 2, 16, 64)
+    pool.host.requires_grad_(True)
+    with pytest.raises(ValueError):
+        uz.KVCache(pool[:, 0], pool[:, 1], zeros(2, 2, dtype=I32), zeros(2, dtype=I32))
+    bench.bumped.clear()
+    box = zeros(2, 2, 32, dtype=F32)
+    uz.rotary(q, pos, plan, out=out)
+    uz.rotary(q, pos, plan)
+    uz.tree_attention(q, cache, out=out, lse=lse)
+    uz.attention_mass(q, cache, lse, out=box)
+    assert bench.bumped == [out, out, lse, box]
