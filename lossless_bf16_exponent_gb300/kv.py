@@ -76,6 +76,74 @@ def _writable(x: torch.Tensor, what: str) -> torch.Tensor:
     return x
 
 
+def _bytes_of(shape, stride, size: int) -> int:
+    """Bytes from a tensor's first element to the end of its last."""
+    end = 1
+    for n, s in zip(shape, stride):
+        end += (n - 1) * s
+    return end * size
+
+
+def _overlap(x: torch.Tensor, y: torch.Tensor) -> bool:
+    """Whether two tensors share a byte: interleaved views of one buffer need not."""
+    x0, y0 = x.data_ptr(), y.data_ptr()
+    if y0 < x0:
+        x, y, x0, y0 = y, x, y0, x0
+    if y0 - x0 >= _bytes_of(x.shape, x.stride(), x.element_size()) or not x.numel() or not y.numel():
+        return False
+    # Heads side by side in one projection: what the last two dimensions span repeats at multiples of g only.
+    g = 0
+    for t in (x, y):
+        for n, s in zip(t.shape[:-2], t.stride()[:-2]):
+            if n > 1:
+                g = math.gcd(g, s * t.element_size())
+    wide, tall = (_bytes_of(t.shape[-2:], t.stride()[-2:], t.element_size()) for t in (x, y))
+    if g and wide <= (y0 - x0) % g <= g - tall:
+        return False
+    # x0 + sum of i s = y0 + sum of j t over x's and y's indexes i, j, strides s, t in bytes and the bytes of an element:
+    # one equation in bounded integers, solved from the largest stride down.
+    span: dict[int, list[int]] = {}
+    for t, sign in ((x, 1), (y, -1)):
+        size = t.element_size()
+        for n, s in [*((n, s * size) for n, s in zip(t.shape, t.stride())), (size, 1)]:
+            if n > 1 and s:
+                r = span.setdefault(s, [0, 0])
+                r[sign > 0] += sign * (n - 1)
+    strides = sorted(span, reverse=True)
+    rest = [(0, 0, 0)]  # of the strides behind: least and largest sum, greatest common divisor
+    for s in reversed(strides):
+        lo, hi, g = rest[-1]
+        rest.append((lo + s * span[s][0], hi + s * span[s][1], math.gcd(g, s)))
+    rest.reverse()
+    budget = 20000
+
+    def reach(k: int, left: int) -> bool:
+        nonlocal budget
+        budget -= 1
+        if budget < 0:
+            return True  # undecided: taken as shared
+        lo, hi, g = rest[k]
+        if not lo <= left <= hi or (left % g if g else left):
+            return False
+        if k == len(strides):
+            return True
+        s, (least, most) = strides[k], span[strides[k]]
+        lo, hi, _ = rest[k + 1]
+        return any(reach(k + 1, left - c * s) for c in range(max(least, -((hi - left) // s)), min(most, (left - lo) // s) + 1))
+
+    return reach(0, y0 - x0)
+
+
+def _apart(out: torch.Tensor, what: str, x: torch.Tensor, name: str, in_place: bool = False) -> None:
+    """Refuse an output that shares memory with something the call reads or
+    writes; ``in_place``: other than element for element."""
+    if in_place and (out is x or (out.data_ptr() == x.data_ptr() and out.shape == x.shape and out.dtype == x.dtype and all(
+            n == 1 or s == t for n, s, t in zip(x.shape, out.stride(), x.stride())))):
+        return
+    if _overlap(out, x):
+        raise ValueError(f"{what}: overlaps {name}" + (" without being it" if in_place else ""))
+
+
 def _no_gradient(what: str, *tensors) -> None:
     """Refuse tensors whose gradient would be cut without a word."""
     if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
@@ -214,6 +282,7 @@ def _rotate(x, positions, plan, out, backward):
         ro = _pack_rows(out.data_ptr(), t * heads * d, heads * d, d)
     else:
         _given(_tensor(out, "out", x.dtype, shape, x.device), "out")
+        _apart(out, "out", x, "x", in_place=True)
         ro = _rows(out, "out")
     if empty:
         return out
@@ -228,7 +297,7 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, plan: RotaryPlan,
     """Turn the pairs of each head of ``x`` ([tokens, heads, dim] or
     [sequences, tokens, heads, dim], bfloat16, float16 or float32, rows
     contiguous) by its token's position (int32). Elements past the plan's
-    rotary_dim are copied. ``out`` may be ``x``. Differentiable in ``x`` where
+    rotary_dim are copied. ``out`` may be ``x`` (or lie apart from it). Differentiable in ``x`` where
     ``out`` is not given."""
     return _rotate(x, positions, plan, out, 0)
 
@@ -324,6 +393,7 @@ def _new_out(out: torch.Tensor | None, q: torch.Tensor, b: int, t: int, heads: i
         out = torch.empty((b, t, heads, d), dtype=q.dtype, device=device)
         return out, _pack_rows(out.data_ptr(), t * heads * d, heads * d, d)
     _given(_tensor(out, "out", q.dtype, q.shape, device), "out")
+    _apart(out, "out", q, "q", in_place=True)
     return out, _rows(out, "out")
 
 
@@ -356,6 +426,9 @@ def rotary_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: 
     if plan.index != index:
         raise ValueError("plan: on another device")
     step = _positions(positions, b, t, index)
+    if out is not None:
+        _apart(out, "out", k, "k")
+        _apart(out, "out", v, "v")
     out, ro = _new_out(out, q, b, t, heads, d, cache.device)
     if t * heads == 0:
         return out
@@ -458,7 +531,7 @@ def tree_attention(q: torch.Tensor, cache: KVCache, mask: torch.Tensor | None = 
                    lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
     """Attention of new tokens over the cache that already holds their keys and
     values (:func:`rotary_append`). ``q`` [sequences, tokens, query heads, dim],
-    1 to 256 tokens; token t sees the first lengths slots and the new tokens of
+    1 to 256 tokens (``out`` may be ``q``); token t sees the first lengths slots and the new tokens of
     its mask row (:func:`tree_mask`; one tree for all when the mask has one
     sequence; None: a chain, each token and those before it). Returns ``(out,
     lse)``: the output, and the float32 log-sum-exp [sequences, tokens, heads].
@@ -508,6 +581,11 @@ def attention_mass(q: torch.Tensor, cache: KVCache, lse: torch.Tensor, mask: tor
                           device=cache.device)
     else:
         _given(_tensor(out, "out", torch.float32, None, cache.device), "out")
+        _apart(out, "out", lse, "lse")
+        if weights is not None:
+            _apart(out, "out", weights, "weights")
+        if mass is not None:
+            _apart(out, "out", mass, "mass", in_place=True)
     shape = out.shape
     if len(shape) != 3 or shape[0] != b or shape[1] != kv_heads or not 1 <= shape[2] <= cache.capacity:
         raise ValueError(f"out: expected [{b}, {kv_heads}, 1 to {cache.capacity}], got {tuple(shape)}")
@@ -573,6 +651,9 @@ def evict(cache: KVCache, mass: torch.Tensor, keep: int, sink: int = 0, recent: 
     else:
         for x, what in ((out_k, "out_k"), (out_v, "out_v")):
             _given(_tensor(x, what, cache.dtype, (b, heads, keep, d), device), what)
+            _apart(x, what, cache.k, "the cache")
+            _apart(x, what, cache.v, "the cache")
+        _apart(out_k, "out_k", out_v, "out_v")
         rk, rv = _rows(out_k, "out_k"), _rows(out_v, "out_v")
     kept = torch.empty((b, heads, keep), dtype=torch.int32, device=device)
     mass_out = torch.empty((b, heads, keep), dtype=torch.float32, device=device)

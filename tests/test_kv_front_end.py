@@ -190,3 +190,69 @@ def test_a_gradient_is_not_cut_without_a_word(bench):
     uz.tree_attention(q, cache, out=out, lse=lse)
     uz.attention_mass(q, cache, lse, out=box)
     assert bench.bumped == [out, out, lse, box]
+
+
+def test_outputs_may_not_share_memory_with_inputs(bench):
+    """An output that overlaps an input without being it is written while it is read: refused. Views side by side in one
+    buffer, and an output that is the input, go through."""
+    cache, pos, plan = make(), zeros(2, 3, dtype=I32), plan_on(0)
+    box = zeros(2, 3, 12, 64)  # heads of a projection
+    q, new = box[:, :, :4], box[:, :, 8:10]
+    lse, mass = zeros(2, 3, 4, dtype=F32), zeros(2, 2, 40, dtype=F32)
+    rows = zeros(2, 2, 24, 64)
+    flat = zeros(4 * 6 * 256 + 64)
+    shifted, plain = flat[8:8 + 6 * 256].view(2, 3, 4, 64), flat[:6 * 256].view(2, 3, 4, 64)
+    bad = [lambda: uz.rotary(q, pos, plan, out=box[:, :, 1:5]), lambda: uz.rotary_backward(plain, pos, plan, out=shifted),
+           lambda: uz.rotary_append(q, new, new, pos, plan, cache, out=box[:, :, 3:7]),
+           lambda: uz.rotary_append(q, new, box[:, :, 10:12], pos, plan, cache, out=box[:, :, 7:11]),
+           lambda: uz.rotary_append(q, new, box[:, :, 10:12], pos, plan, cache, out=box[:, :, 4:12][:, :, 4:8]),
+           lambda: uz.tree_attention(q, cache, out=box[:, :, 2:6]),
+           lambda: uz.attention_mass(q, cache, lse, mass=mass[:, :, 0:20], out=mass[:, :, 4:24]),
+           lambda: uz.attention_mass(q, cache, lse, out=OnGpu(torch.as_strided(lse.host, (2, 2, 4), (8, 4, 1)))),
+           lambda: uz.evict(cache, mass, 8, out_k=rows[:, :, :8], out_v=rows[:, :, 7:15]),
+           lambda: uz.evict(cache, mass, 8, out_k=cache.k[1:3, :, :8], out_v=rows[:, :, :8]),
+           lambda: uz.evict(cache, mass, 8, out_k=rows[:, :, :8], out_v=cache.v[:2, :, 8:])]
+    for i, call in enumerate(bad):
+        with pytest.raises(ValueError, match="overlap"):
+            call()
+        assert not bench.calls, i
+    good = [lambda: uz.rotary(q, pos, plan, out=q), lambda: uz.rotary(q, pos, plan, out=box[:, :, :4]),
+            lambda: uz.rotary(q, pos, plan, out=box[:, :, 4:8]), lambda: uz.rotary(plain, pos, plan, out=flat[6 * 256:12 * 256].view(2, 3, 4, 64)),
+            lambda: uz.rotary_append(q, new, box[:, :, 10:12], pos, plan, cache, out=box[:, :, 4:8]),
+            lambda: uz.rotary_append(q, new, new, pos, plan, cache, out=q), lambda: uz.tree_attention(q, cache, out=box[:, :, 4:8]),
+            lambda: uz.tree_attention(q, cache, out=q), lambda: uz.attention_mass(q, cache, lse, mass=mass[:, :, :20], out=mass[:, :, :20]),
+            lambda: uz.attention_mass(q, cache, lse, mass=mass[:, :, :20], out=mass[:, :, 20:]),
+            lambda: uz.evict(cache, mass, 8, out_k=rows[:, :, :8], out_v=rows[:, :, 8:16])]
+    for call in good:
+        call()
+    assert len(bench.calls) == len(good)
+
+
+def test_overlap_of_views_is_exact():
+    import random
+
+    r = random.Random(5)
+    flat = torch.zeros(400, dtype=torch.int16)
+    seen = {True: 0, False: 0}
+    for _ in range(4000):
+        views = []
+        for _ in range(2):
+            shape = [r.randint(0 if r.random() < 0.02 else 1, 4) for _ in range(r.randint(1, 4))]
+            strides = [r.choice([0, 1, 2, 3, 4, 6, 8, 12, 16, 24, 48]) for _ in shape]
+            t = flat if r.random() < 0.8 else flat.view(torch.uint8)
+            reach = sum((max(n, 1) - 1) * s for n, s in zip(shape, strides))
+            if reach >= 400:
+                strides, reach = [1] * len(shape), sum(max(n, 1) - 1 for n in shape)
+            views.append(t.as_strided(shape, strides, r.randint(0, min(399 - reach, 60))))
+        marks = []
+        for v in views:
+            base = torch.zeros(800, dtype=torch.uint8)
+            offset = v.storage_offset() * v.element_size()
+            same = base.as_strided([*v.shape, v.element_size()], [*(s * v.element_size() for s in v.stride()), 1], offset)
+            if v.numel():
+                same.fill_(1)
+            marks.append(base)
+        want = bool((marks[0] & marks[1]).any())
+        assert kv._overlap(*views) == kv._overlap(*views[::-1]) == want
+        seen[want] += 1
+    assert min(seen.values()) > 500
