@@ -567,7 +567,8 @@ def attention_mass(q: torch.Tensor, cache: KVCache, lse: torch.Tensor, mask: tor
     exp(score - lse)``; 0 for slots not in use. ``q``, ``mask``, ``counts`` and
     ``scale`` as for the :func:`tree_attention` that gave ``lse``; ``weights``
     float32 [sequences, tokens] (1 for accepted tokens, 0 for the others; None:
-    ones). ``out`` may be ``mass``; its width (default: the cache's capacity) says
+    ones). ``out`` may be ``mass``; a ``mass`` whose rows lie otherwise than
+    ``out``'s is first copied there. ``out``'s width (default: the cache's capacity) says
     how many slots are weighed."""
     rq, b, t, heads, d = _query(q, cache)
     address, stride = _mask(mask, cache, t) if mask is not None else (None, 0)
@@ -596,8 +597,8 @@ def attention_mass(q: torch.Tensor, cache: KVCache, lse: torch.Tensor, mask: tor
     if mass is not None:
         if mass.dtype != torch.float32 or mass.get_device() != cache.index or mass.shape != shape:
             raise ValueError(f"mass: expected float32 {tuple(shape)} on {cache.device}")
-        if mass.stride() != (sb, sh, sn):
-            raise ValueError("mass: expected the strides of out")
+        if mass.stride() != (sb, sh, sn) and any(n > 1 and s != t for n, s, t in zip(shape, mass.stride(), (sb, sh, sn))):
+            mass = out.copy_(mass)  # the kernel takes both with the same strides; they may be one
         at_mass = mass.data_ptr()
     _call(cache.index, load().uzkv_attention_mass, rq, at_lse, _FLOATS[q.dtype], t, heads, address, stride,
           _counts(counts, cache), at_weights, d ** -0.5 if scale is None else scale, cache._ref, at_mass, decay,

@@ -256,3 +256,27 @@ def test_overlap_of_views_is_exact():
         assert kv._overlap(*views) == kv._overlap(*views[::-1]) == want
         seen[want] += 1
     assert min(seen.values()) > 500
+
+
+def test_mass_of_any_strides(bench):
+    """A mass that is a view goes through: strides of dimensions of one element do not count, and one whose rows lie
+    otherwise than the output's is copied to the output, which may be both."""
+    cache, q, lse = make(b=1), zeros(1, 3, 4, 64), zeros(1, 3, 4, dtype=F32)
+    wide = zeros(1, 8, 2, 32, dtype=F32)[:, 0]  # one sequence of a longer buffer
+    assert wide.is_contiguous() and wide.stride(0) != 64
+    uz.attention_mass(q, cache, lse, mass=wide)
+    assert bench.calls[-1][2][11] == wide.data_ptr()
+    padded = OnGpu(torch.arange(100, dtype=F32).view(1, 2, 50))[:, :, 3:35]
+    out = uz.attention_mass(q, cache, lse, mass=padded)
+    args = bench.calls[-1][2]
+    assert args[11] == args[13] == out.data_ptr() and args[14:17] == (64, 32, 32)
+    assert torch.equal(out.host, padded.host)
+    box = zeros(1, 2, 40, dtype=F32)
+    turned = OnGpu(torch.arange(64, dtype=F32).view(1, 32, 2).transpose(1, 2))  # rows not contiguous
+    assert uz.attention_mass(q, cache, lse, mass=turned, out=box[:, :, 8:]).data_ptr() == box.data_ptr() + 32
+    assert torch.equal(box.host[:, :, 8:], turned.host) and torch.all(box.host[:, :, :8] == 0)
+    same = zeros(1, 2, 64, dtype=F32)
+    uz.attention_mass(q, cache, lse, mass=same[:, :, :32], out=same[:, :, :32])
+    assert bench.calls[-1][2][11] == bench.calls[-1][2][13] == same.data_ptr()
+    with pytest.raises(ValueError):
+        uz.attention_mass(q, cache, lse, mass=same)
