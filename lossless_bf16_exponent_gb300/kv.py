@@ -444,7 +444,9 @@ def tree_mask(parents, device="cuda") -> torch.Tensor:
     """Mask rows of drafted trees: ``parents[b][t]`` is the node that token t of
     sequence b continues, or -1 for one that continues the cache; a parent comes
     before its child. Returns int64 [sequences, tokens, ceil(tokens / 64)]: bit u
-    of row t is set where u is t or an ancestor of t."""
+    of row t is set where u is t or an ancestor of t. The host does not wait for
+    the copy to ``device``, which the current stream makes. Not under a graph's
+    capture, whose replays would copy from memory that is gone."""
     rows = [[int(u) for u in row] for row in parents]
     t = len(rows[0]) if rows else 0
     if not 1 <= t <= MAX_NEW_TOKENS or any(len(r) != t for r in rows):
@@ -459,7 +461,13 @@ def tree_mask(parents, device="cuda") -> torch.Tensor:
             seen.append((seen[u] if u >= 0 else 0) | 1 << i)
         out.append([[(w - (1 << 64) if w >= 1 << 63 else w)
                      for w in ((s >> 64 * j) & ((1 << 64) - 1) for j in range(words))] for s in seen])
-    return torch.tensor(out, dtype=torch.int64, device=device)
+    mask = torch.tensor(out, dtype=torch.int64)
+    device = torch.device(device)
+    if device.type != "cuda":
+        return mask.to(device)
+    if _capturing(codec._current_device() if device.index is None else device.index):
+        raise ValueError("tree_mask: a replay would not see the tree; make masks before the capture")
+    return mask.pin_memory().to(device, non_blocking=True)  # from pageable memory the host would wait for the stream
 
 
 def _mask(mask, cache, t):

@@ -26,3 +26,32 @@ def test_mass_of_any_strides(uz):
         box = torch.zeros(2, 3, cache.capacity, device=DEV)
         assert torch.equal(uz.attention_mass(q, cache, lse, mass=m, decay=0.5, out=box[:, 1:]), want)
         assert torch.all(box[:, 0] == 0)
+
+
+def test_tree_mask_does_not_wait_for_the_stream(uz):
+    parents = [[-1, 0, 0, 1, -1, 4]] * 3
+    want = uz.tree_mask(parents, device="cpu")
+    assert torch.equal(uz.tree_mask(parents).cpu(), want)
+    x = torch.zeros(1 << 28, device=DEV)
+    done = torch.cuda.Event()
+    torch.cuda.synchronize()
+    for _ in range(400):  # of a GB each: some 100 ms of work
+        x.add_(1.0)
+    done.record()
+    mask = uz.tree_mask(parents)
+    assert not done.query(), "the call waited for the work before it"
+    assert torch.equal(mask.cpu(), want) and mask.device == x.device
+
+
+def test_tree_mask_refuses_a_capture(uz):
+    side = torch.cuda.Stream()
+    x = torch.zeros(4, device=DEV)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        x.add_(1.0)
+        with pytest.raises(ValueError, match="capture"):
+            uz.tree_mask([[-1, 0]])
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.all(x == 1)
