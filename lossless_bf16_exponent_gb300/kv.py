@@ -429,8 +429,10 @@ def rotary_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: 
     if out is not None:
         _apart(out, "out", k, "k")
         _apart(out, "out", v, "v")
+    if heads == 0:
+        raise ValueError("q: no heads")
     out, ro = _new_out(out, q, b, t, heads, d, cache.device)
-    if t * heads == 0:
+    if b * t == 0:
         return out
     turns, rotary_dim, layout, magnitude = plan.args
     _call(index, load().uzkv_rotary_append, rq, rk, rv, ro, _FLOATS[dtype], t, heads, positions.data_ptr(), step, turns,

@@ -280,3 +280,13 @@ def test_mass_of_any_strides(bench):
     assert bench.calls[-1][2][11] == bench.calls[-1][2][13] == same.data_ptr()
     with pytest.raises(ValueError):
         uz.attention_mass(q, cache, lse, mass=same)
+
+
+def test_append_of_no_heads_is_refused_and_of_no_tokens_is_nothing(bench):
+    """Without query heads nothing was stored and nothing said; without tokens there is nothing to store."""
+    cache, pos, plan, new = make(), zeros(2, 3, dtype=I32), plan_on(0), zeros(2, 3, 2, 64)
+    with pytest.raises(ValueError, match="heads"):
+        uz.rotary_append(zeros(2, 3, 0, 64), new, new, pos, plan, cache)
+    none = zeros(2, 0, 4, 64)
+    assert uz.rotary_append(none, new[:, :0], new[:, :0], pos[:, :0], plan, cache).shape == (2, 0, 4, 64)
+    assert not bench.calls
