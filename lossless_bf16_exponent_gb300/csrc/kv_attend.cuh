@@ -175,19 +175,16 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kernel(const __grid_con
                         }
                     float up = 1.0f;
                     if (!std::is_same<QT, T>::value) {
-                        // BF16 queries of an FP16 product: a power of two out of the row brings its largest element to [1, 2).
                         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
                         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-                        const uint32_t ex = __float_as_uint(top) >> 23;
-                        const bool plain = ex > 0 && ex < 254;  // not a row of zeros or subnormals, or with an infinity
-                        const float down = plain ? __uint_as_float((254 - ex) << 23) : 1.0f;
-                        up = plain ? __uint_as_float(ex << 23) : 1.0f;
+                        const RowScale scaled(top);
+                        up = scaled.up;
 #pragma unroll
                         for (int kk = 0; kk < DP / 16; kk++)
 #pragma unroll
                             for (int y = 0; y < 2; y++) {
                                 const QT* e = reinterpret_cast<const QT*>(&q[t][kk][y]);
-                                q[t][kk][y] = pack2<__half>(to_f32(e[0]) * down, to_f32(e[1]) * down);
+                                q[t][kk][y] = pack2<__half>(to_f32(e[0]) * scaled.down, to_f32(e[1]) * scaled.down);
                             }
                     }
 #pragma unroll

@@ -323,10 +323,24 @@ constexpr float kLift = 0.0f;
 template <>
 constexpr float kLift<__half> = 6.0f;
 
+// BF16 queries of an FP16 product (an E5M2 cache): a power of two is taken out of each row and put back on its scores.
+// It brings the row's largest element `top` to [1, 2), to [2, 4) from 2^127 on, and below 1 where top is subnormal: both
+// powers are normal numbers, and neither end of BF16's range passes FP16's. BF16's eight bits fit FP16's eleven down to
+// 2^-14; smaller elements are rounded to multiples of 2^-24, so a score is off by at most 2^-24 top * sum |k|, about
+// what the product's 32-bit sums round away beside a term of the largest element.
+struct RowScale {
+    float down, up;
+    __device__ __forceinline__ explicit RowScale(float top) {
+        const uint32_t ex = top == 0.0f ? 127u : min(max(__float_as_uint(top) >> 23, 1u), 253u);  // 127: nothing to scale
+        down = __uint_as_float((254 - ex) << 23);
+        up = __uint_as_float(ex << 23);
+    }
+};
+
 // Queries of rows row0 .. row0 + rows - 1 to shared memory as T (columns past head_dim and rows past p.rows
 // zero), by THREADS threads numbered tid; at(row, c) is where 16-byte chunk c of a row goes. factor[r] is what a
 // score of row r is to be multiplied by to have it in units of log2: |scale| * log2(e), and for BF16 queries that
-// go to an FP16 product the power of two that was taken out of the row to bring its largest element to [1, 2).
+// go to an FP16 product the power of two that was taken out of the row.
 // The sign of scale goes to the queries.
 template <typename QT, typename T, int DP, int THREADS, typename At>
 __device__ __forceinline__ void load_queries(const AttParams& p, uint32_t tid, uint32_t b, uint32_t h, uint32_t row0,
@@ -362,14 +376,11 @@ __device__ __forceinline__ void load_queries(const AttParams& p, uint32_t tid, u
                     top = fmaxf(top, fabsf(v[y]));
                 }
                 for (uint32_t o = kChunks / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-                // 2^-e as a float with e the exponent of top; 1 for a row of zeros, subnormals or with an infinity
-                const uint32_t ex = __float_as_uint(top) >> 23;
-                const bool plain = ex > 0 && ex < 254;
-                const float down = plain ? __uint_as_float((254 - ex) << 23) : 1.0f;
-                f *= plain ? __uint_as_float(ex << 23) : 1.0f;
+                const RowScale row(top);
+                f *= row.up;
                 uint32_t* w = reinterpret_cast<uint32_t*>(&x);
 #pragma unroll
-                for (int y = 0; y < 4; y++) w[y] = pack2<__half>(v[2 * y] * down, v[2 * y + 1] * down);
+                for (int y = 0; y < 4; y++) w[y] = pack2<__half>(v[2 * y] * row.down, v[2 * y + 1] * row.down);
             }
             if (p.scale < 0.0f) {
                 x.x ^= 0x80008000u;

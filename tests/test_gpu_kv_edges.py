@@ -55,3 +55,34 @@ def test_tree_mask_refuses_a_capture(uz):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.all(x == 1)
+
+
+# -------------------------------------------------- bfloat16 queries over an FP8 cache
+
+@pytest.mark.parametrize("t", [1, 3, 24, 70])  # few rows, more, and the tensor-core kernel
+@pytest.mark.parametrize("gain,key,scale", [(2.0 ** 126, 2.0 ** -12, 2.0 ** -116), (2.0 ** -130, 2.0 ** 10, 2.0 ** 119)])
+def test_queries_at_the_ends_of_bfloat16_over_an_fp8_cache(uz, t, gain, key, scale):
+    """The largest and the subnormal bfloat16 numbers lie outside binary16's range, in which the products are taken: a
+    power of two out of each row brings them in."""
+    g = gen(t)
+    cache = make_cache(uz, g, [100, 9], t, 1, 64, 16, E5, scale=key)
+    x = randn(g, 2, t, 3, 64)
+    q = (x.clamp(-1.9, 1.9) * gain).to(BF)
+    q[0, 0, 0, 5] = float(torch.tensor(1.9, dtype=BF)) * gain  # a row whose largest element is 2^126 or above
+    q[1, 0, 1] = 0.0  # a row of zeros
+    assert torch.isfinite(q).all() and float(q.abs().max()) > gain
+    if gain > 1:
+        q[0, t - 1, 1, 7] = 3.0e38  # ... and 2^127 or above
+    _, lse = check_attention(uz, q, cache, None, [t, t], None, scale=scale)
+    mass = uz.attention_mass(q, cache, lse, scale=scale)
+    assert float(mass.double().sum()) == pytest.approx(2 * t * 3, rel=1e-3)
+
+
+def test_queries_with_an_infinity_over_an_fp8_cache(uz):
+    cache = make_cache(uz, gen(2), [50], 2, 1, 64, 16, E5)
+    q = randn(gen(3), 1, 2, 3, 64, dtype=BF)
+    want, _ = uz.tree_attention(q, cache)
+    q[0, 1, 2, 9] = math.inf
+    out, lse = uz.tree_attention(q, cache)
+    assert torch.equal(out[0, 0], want[0, 0]) and torch.equal(out[0, 1, :2], want[0, 1, :2])
+    assert not torch.isfinite(lse[0, 1, 2])
