@@ -181,7 +181,8 @@ class RotaryPlan:
 
 
 def rotary_rates(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
-                 original_length: int = 0, low: float = 1.0, high: float = 32.0) -> tuple[list[float], float]:
+                 original_length: int = 0, low: float = 1.0, high: float = 32.0,
+                 magnitude: float | None = None) -> tuple[list[float], float]:
     """Radians a position of each pair, and the factor on cosines and sines.
 
     ``base ** (-2 i / rotary_dim)`` for pair i, and for a context stretched by
@@ -190,7 +191,17 @@ def rotary_rates(rotary_dim: int, base: float = 10000.0, scaling: str = "none", 
     fastest pair as it is and divides the slowest by ``factor``; "ramp" divides
     the pairs that turn less than ``low`` times over ``original_length``
     positions, leaves those that turn more than ``high`` times, mixes linearly
-    between, and scales cosines and sines by ``0.1 ln(factor) + 1``."""
+    between, and scales cosines and sines by ``0.1 ln(factor) + 1``.
+    ``magnitude`` replaces the factor that the scaling gives (1 but for "ramp")."""
+    rates, given = _rates(rotary_dim, base, scaling, factor, original_length, low, high)
+    if magnitude is None:
+        return rates, given
+    if not (magnitude > 0.0 and math.isfinite(magnitude)):
+        raise ValueError("magnitude: expected a positive number")
+    return rates, float(magnitude)
+
+
+def _rates(rotary_dim, base, scaling, factor, original_length, low, high) -> tuple[list[float], float]:
     if rotary_dim < 2 or rotary_dim % 2 or rotary_dim > MAX_HEAD_DIM:
         raise ValueError(f"rotary_dim {rotary_dim}: expected an even number in [2, {MAX_HEAD_DIM}]")
     if not (base > 1.0 and math.isfinite(base) and factor >= 1.0 and math.isfinite(factor)):
@@ -218,11 +229,11 @@ def rotary_rates(rotary_dim: int, base: float = 10000.0, scaling: str = "none", 
 
 def rotary_plan(rotary_dim: int, base: float = 10000.0, layout: str = "half", scaling: str = "none",
                 factor: float = 1.0, original_length: int = 0, low: float = 1.0, high: float = 32.0,
-                device="cuda") -> RotaryPlan:
+                device="cuda", magnitude: float | None = None) -> RotaryPlan:
     """The plan of :func:`rotary` and :func:`rotary_append`; see :func:`rotary_rates`
-    for the scalings. ``layout``: "half" turns elements i and i + rotary_dim / 2
+    for the scalings and ``magnitude``. ``layout``: "half" turns elements i and i + rotary_dim / 2
     together, "interleaved" 2 i and 2 i + 1."""
-    rates, magnitude = rotary_rates(rotary_dim, base, scaling, factor, original_length, low, high)
+    rates, magnitude = rotary_rates(rotary_dim, base, scaling, factor, original_length, low, high, magnitude)
     turns = [int(round(f / (2 * math.pi) * 2.0 ** 64)) for f in rates]
     turns = torch.tensor([v - (1 << 64) if v >= 1 << 63 else v for v in turns], dtype=torch.int64, device=device)
     return RotaryPlan(turns, rotary_dim, layout, magnitude)

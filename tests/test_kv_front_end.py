@@ -290,3 +290,21 @@ def test_append_of_no_heads_is_refused_and_of_no_tokens_is_nothing(bench):
     none = zeros(2, 0, 4, 64)
     assert uz.rotary_append(none, new[:, :0], new[:, :0], pos[:, :0], plan, cache).shape == (2, 0, 4, 64)
     assert not bench.calls
+
+
+def test_the_ramp_without_its_magnitude():
+    """The ramp in turns between 1 and 4 with cosines and sines as they are: a published scaling of long contexts."""
+    kw = dict(base=500000.0, scaling="ramp", factor=8.0, original_length=8192, low=1.0, high=4.0)
+    rates, factor = uz.rotary_rates(128, **kw, magnitude=1.0)
+    assert factor == 1.0 and rates == uz.rotary_rates(128, **kw)[0]
+    for i, f in enumerate(rates):
+        plain = 500000.0 ** (-2 * i / 128)
+        length = 2 * 3.141592653589793 / plain  # positions of a turn
+        mix = min(1.0, max(0.0, (8192 / length - 1.0) / 3.0))
+        assert f == pytest.approx(plain * (mix + (1 - mix) / 8.0), rel=1e-12)
+    assert uz.rotary_plan(128, **kw, magnitude=1.0, device="cpu").magnitude == 1.0
+    assert uz.rotary_plan(128, **kw, device="cpu").magnitude == uz.rotary_rates(128, **kw)[1] > 1.2
+    assert uz.rotary_rates(8, magnitude=0.5) == (uz.rotary_rates(8)[0], 0.5)
+    for bad in (0.0, -1.0, float("nan"), float("inf")):
+        with pytest.raises(ValueError):
+            uz.rotary_rates(8, magnitude=bad)
