@@ -338,7 +338,8 @@ class KVCache:
     when a length or page number is out of range (6 if a bounded wait inside a
     kernel ran out; never cleared). A contiguous cache [sequences, heads, tokens,
     dim] is the pool of whole-sequence pages with
-    ``page_table = arange(sequences)[:, None]``."""
+    ``page_table = arange(sequences)[:, None]``. A batch of no sequences gives
+    empty results."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, lengths: torch.Tensor,
                  status: torch.Tensor | None = None):
@@ -569,6 +570,8 @@ def tree_attention(q: torch.Tensor, cache: KVCache, mask: torch.Tensor | None = 
     else:
         at_lse = _floats(lse, "lse", (b, t, heads), cache)
         _given(lse, "lse")
+    if b == 0:
+        return out, lse
     if workspace is None:
         workspace = _workspace(cache, tree_attention_workspace_bytes(cache, t, heads))
     elif not _tensor(workspace, "workspace", torch.uint8, None, cache.device).is_contiguous():
@@ -621,6 +624,8 @@ def attention_mass(q: torch.Tensor, cache: KVCache, lse: torch.Tensor, mask: tor
         if mass.stride() != (sb, sh, sn) and any(n > 1 and s != t for n, s, t in zip(shape, mass.stride(), (sb, sh, sn))):
             mass = out.copy_(mass)  # the kernel takes both with the same strides; they may be one
         at_mass = mass.data_ptr()
+    if b == 0:
+        return out
     _call(cache.index, load().uzkv_attention_mass, rq, at_lse, _FLOATS[q.dtype], t, heads, address, stride,
           _counts(counts, cache), at_weights, d ** -0.5 if scale is None else scale, cache._ref, at_mass, decay,
           out.data_ptr(), sb, sh, shape[2])
@@ -680,6 +685,8 @@ def evict(cache: KVCache, mass: torch.Tensor, keep: int, sink: int = 0, recent: 
     kept = torch.empty((b, heads, keep), dtype=torch.int32, device=device)
     mass_out = torch.empty((b, heads, keep), dtype=torch.float32, device=device)
     lengths = torch.empty((b,), dtype=torch.int32, device=device)
+    if b == 0:
+        return Packed(out_k, out_v, mass_out, kept, lengths)
     _call(cache.index, load().uzkv_evict, cache._ref, mass.data_ptr(), sb, sh, shape[2], keep, sink, recent, rk, rv,
           kept.data_ptr(), mass_out.data_ptr(), lengths.data_ptr())
     return Packed(out_k, out_v, mass_out, kept, lengths)

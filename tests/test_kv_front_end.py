@@ -308,3 +308,16 @@ def test_the_ramp_without_its_magnitude():
     for bad in (0.0, -1.0, float("nan"), float("inf")):
         with pytest.raises(ValueError):
             uz.rotary_rates(8, magnitude=bad)
+
+
+def test_a_batch_of_no_sequences_gives_empty_results(bench):
+    cache, plan = make(b=0), plan_on(0)
+    q, new, pos = zeros(0, 3, 4, 64), zeros(0, 3, 2, 64), zeros(0, 3, dtype=I32)
+    assert uz.rotary(q, pos, plan).shape == uz.rotary_append(q, new, new, pos, plan, cache).shape == (0, 3, 4, 64)
+    out, lse = uz.tree_attention(q, cache)
+    assert out.shape == (0, 3, 4, 64) and lse.shape == (0, 3, 4)
+    mass = uz.attention_mass(q, cache, lse)
+    assert mass.shape == (0, 2, 32)
+    packed = uz.evict(cache, mass, 8)
+    assert packed.k.shape == packed.v.shape == (0, 2, 8, 64) and packed.kept.shape == (0, 2, 8) and packed.lengths.shape == (0,)
+    assert not bench.calls
