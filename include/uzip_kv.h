@@ -47,7 +47,7 @@ enum uzkv_layout {
 
 typedef struct {
     void *d_k, *d_v; /* 16-byte aligned */
-    /* Strides in elements, each a multiple of 16 bytes; elements of a row are contiguous. */
+    /* Strides in elements, each a multiple of 16 bytes (any along a dimension of one); elements of a row are contiguous. */
     int64_t k_page_stride, k_head_stride, k_token_stride;
     int64_t v_page_stride, v_head_stride, v_token_stride;
     const int32_t *d_table; /* [sequences] rows of pages_per_sequence, table_stride apart */

@@ -122,7 +122,7 @@ int common(Params& p, const uzkv_rows_t* q, uint32_t dtype, uint32_t tokens, uin
     if (!rows_valid(q) || dtype > UZKV_FP16 || (cache->dtype != dtype && cache->dtype != UZKV_E5M2)) return UZIP_ERR_ARG;
     if (!tokens || tokens > UZKV_MAX_NEW_TOKENS || !q_heads || q_heads > 65535 || q_heads % cache->kv_heads) return UZIP_ERR_ARG;
     if (mask_stride_b < 0) return UZIP_ERR_ARG;
-    p.q = rows_of(q, dtype);
+    p.q = rows_of(q, dtype, cache->sequences, tokens, q_heads);
     if (!rows_aligned16(p.q)) return UZIP_ERR_ALIGN;
     if ((reinterpret_cast<uintptr_t>(d_mask) & 7) || (reinterpret_cast<uintptr_t>(d_counts) & 3)) return UZIP_ERR_ALIGN;
     p.mask = d_mask;
@@ -160,7 +160,7 @@ extern "C" UZIP_API int uzkv_tree_attention(const uzkv_rows_t* q, const uzkv_row
     Params p{};
     if (int rc = common(p, q, dtype, tokens, q_heads, d_mask, mask_stride_b, d_counts, scale, cache)) return rc;
     if (!rows_valid(out) || !d_workspace) return UZIP_ERR_ARG;
-    p.out = rows_of(out, dtype);
+    p.out = rows_of(out, dtype, cache->sequences, tokens, q_heads);
     if (!rows_aligned16(p.out) || !aligned16(d_workspace) || (reinterpret_cast<uintptr_t>(d_lse) & 3)) return UZIP_ERR_ALIGN;
     if (workspace_bytes < uzkv_tree_attention_workspace_bytes(p.cache.sequences, tokens, q_heads, p.cache.kv_heads, p.cache.head_dim))
         return UZIP_ERR_CAPACITY;

@@ -343,8 +343,8 @@ extern "C" UZIP_API int uzkv_evict(const uzkv_cache_t* cache, const float* d_mas
     if ((reinterpret_cast<uintptr_t>(d_mass) | reinterpret_cast<uintptr_t>(d_kept) |
          reinterpret_cast<uintptr_t>(d_mass_out) | reinterpret_cast<uintptr_t>(d_lengths_out)) & 3)
         return UZIP_ERR_ALIGN;
-    p.out_k = rows_of(out_k, cache->dtype);
-    p.out_v = rows_of(out_v, cache->dtype);
+    p.out_k = rows_of(out_k, cache->dtype, cache->sequences, cache->kv_heads, keep);
+    p.out_v = rows_of(out_v, cache->dtype, cache->sequences, cache->kv_heads, keep);
     if (!rows_aligned16(p.out_k) || !rows_aligned16(p.out_v)) return UZIP_ERR_ALIGN;
     p.mass = d_mass;
     p.mass_b = mass_stride_b;

@@ -116,9 +116,10 @@ __device__ __forceinline__ bool mask_bit(const int64_t* row, uint32_t t, uint32_
 
 inline uint32_t bytes_of(uint32_t dtype) { return dtype == UZKV_FP32 ? 4 : dtype == UZKV_E5M2 ? 1 : 2; }
 
-inline Rows rows_of(const uzkv_rows_t* r, uint32_t dtype) {
+// The rows of b x t x h of them. A stride along a dimension of one is nothing: no alignment is asked of it.
+inline Rows rows_of(const uzkv_rows_t* r, uint32_t dtype, uint32_t b, uint32_t t, uint32_t h) {
     const int64_t e = bytes_of(dtype);
-    return Rows{static_cast<char*>(r->d), r->stride_b * e, r->stride_t * e, r->stride_h * e};
+    return Rows{static_cast<char*>(r->d), b > 1 ? r->stride_b * e : 0, t > 1 ? r->stride_t * e : 0, h > 1 ? r->stride_h * e : 0};
 }
 
 // Host checks of a cache; fills the kernels' form. cap is the width that must fit 31 bits.
@@ -131,11 +132,14 @@ inline int cache_of(const uzkv_cache_t* c, Cache* o) {
     const uint64_t cap = (uint64_t)c->page_tokens * c->pages_per_sequence;
     if (cap > 0x7FFFFF00ull || c->pages > 0x7FFFFFFFu || c->sequences > 65535 || c->kv_heads > 65535) return UZIP_ERR_ARG;
     if (c->table_stride < 0) return UZIP_ERR_ARG;
-    const int64_t st[6] = {c->k_page_stride, c->k_head_stride, c->k_token_stride,
-                           c->v_page_stride, c->v_head_stride, c->v_token_stride};
-    for (int64_t s : st) {
-        if (s < 0) return UZIP_ERR_ARG;
-        if (s * e % 16) return UZIP_ERR_ALIGN;
+    int64_t st[6] = {c->k_page_stride, c->k_head_stride, c->k_token_stride,
+                     c->v_page_stride, c->v_head_stride, c->v_token_stride};
+    const uint32_t along[3] = {c->pages, c->kv_heads, c->page_tokens};
+    for (int i = 0; i < 6; i++) {
+        if (st[i] < 0) return UZIP_ERR_ARG;
+        st[i] *= e;
+        if (along[i % 3] == 1) st[i] = (st[i] + 15) / 16 * 16;  // along a dimension of one it only has to suit tensor maps
+        if (st[i] % 16) return UZIP_ERR_ALIGN;
     }
     if (!aligned16(c->d_k) || !aligned16(c->d_v)) return UZIP_ERR_ALIGN;
     if ((reinterpret_cast<uintptr_t>(c->d_table) | reinterpret_cast<uintptr_t>(c->d_lengths) |
@@ -143,12 +147,12 @@ inline int cache_of(const uzkv_cache_t* c, Cache* o) {
         return UZIP_ERR_ALIGN;
     o->k = static_cast<char*>(c->d_k);
     o->v = static_cast<char*>(c->d_v);
-    o->k_page = st[0] * e;
-    o->k_head = st[1] * e;
-    o->k_token = st[2] * e;
-    o->v_page = st[3] * e;
-    o->v_head = st[4] * e;
-    o->v_token = st[5] * e;
+    o->k_page = st[0];
+    o->k_head = st[1];
+    o->k_token = st[2];
+    o->v_page = st[3];
+    o->v_head = st[4];
+    o->v_token = st[5];
     o->table = c->d_table;
     o->table_stride = c->table_stride;
     o->lengths = c->d_lengths;

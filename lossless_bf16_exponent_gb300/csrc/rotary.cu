@@ -335,8 +335,8 @@ extern "C" UZIP_API int uzkv_rotary(const uzkv_rows_t* x, const uzkv_rows_t* y, 
     if (!rows_valid(x) || !rows_valid(y) || !sequences || dtype > UZKV_FP32) return UZIP_ERR_ARG;
     if (int rc = common(d_positions, position_stride, d_turns, rotary_dim, layout, head_dim, tokens, heads)) return rc;
     Params p{};
-    p.x = rows_of(x, dtype);
-    p.y = rows_of(y, dtype);
+    p.x = rows_of(x, dtype, sequences, tokens, heads);
+    p.y = rows_of(y, dtype, sequences, tokens, heads);
     if (!element_aligned(p.x, dtype) || !element_aligned(p.y, dtype)) return UZIP_ERR_ALIGN;
     p.positions = d_positions;
     p.position_stride = position_stride;
@@ -366,10 +366,10 @@ extern "C" UZIP_API int uzkv_rotary_append(const uzkv_rows_t* q, const uzkv_rows
     if (int rc = cache_of(cache, &p.cache)) return rc;
     if (cache->dtype != dtype && cache->dtype != UZKV_E5M2) return UZIP_ERR_ARG;
     if (int rc = common(d_positions, position_stride, d_turns, rotary_dim, layout, cache->head_dim, tokens, q_heads)) return rc;
-    p.x = rows_of(q, dtype);
-    p.y = rows_of(q_out, dtype);
-    p.k = rows_of(k, dtype);
-    p.v = rows_of(v, dtype);
+    p.x = rows_of(q, dtype, cache->sequences, tokens, q_heads);
+    p.y = rows_of(q_out, dtype, cache->sequences, tokens, q_heads);
+    p.k = rows_of(k, dtype, cache->sequences, tokens, cache->kv_heads);
+    p.v = rows_of(v, dtype, cache->sequences, tokens, cache->kv_heads);
     for (const Rows* r : {&p.x, &p.y, &p.k, &p.v})
         if (!element_aligned(*r, dtype)) return UZIP_ERR_ALIGN;
     if (reinterpret_cast<uintptr_t>(d_counts) & 3) return UZIP_ERR_ALIGN;

@@ -86,3 +86,36 @@ def test_queries_with_an_infinity_over_an_fp8_cache(uz):
     out, lse = uz.tree_attention(q, cache)
     assert torch.equal(out[0, 0], want[0, 0]) and torch.equal(out[0, 1, :2], want[0, 1, :2])
     assert not torch.isfinite(lse[0, 1, 2])
+
+
+# ------------------------------------------------------------ strides of nothing
+
+def test_strides_of_dimensions_of_one_do_not_count(uz):
+    """A dimension of one element may have any stride: it is never taken."""
+    g = gen(4)
+
+    def odd(x):  # the same elements; dimensions of one get a stride that no alignment allows
+        return x.as_strided(x.shape, [3 if n == 1 else s for n, s in zip(x.shape, x.stride())])
+
+    k, v = randn(g, 1, 1, 64, 128, dtype=BF), randn(g, 1, 1, 64, 128, dtype=BF)
+    table, lengths = torch.zeros(1, 1, dtype=torch.int32, device=DEV), torch.tensor([40], dtype=torch.int32, device=DEV)
+    plain = uz.KVCache(k.clone(), v.clone(), table, lengths)
+    cache = uz.KVCache(odd(k), odd(v), table, lengths)
+    plan, pos = uz.rotary_plan(128), torch.full((1, 1), 40, dtype=torch.int32, device=DEV)
+    for heads in (1, 4):
+        q, new = randn(g, 1, 1, heads, 128, dtype=BF), randn(g, 1, 1, 1, 128, dtype=BF)
+        want = uz.rotary_append(q, new, new, pos, plan, plain)
+        got = uz.rotary_append(odd(q), odd(new), odd(new), pos, plan, cache, out=odd(torch.empty_like(q)))
+        assert torch.equal(got, want) and torch.equal(cache.k, plain.k) and torch.equal(cache.v, plain.v)
+        assert torch.equal(uz.rotary(odd(q), pos, plan), want)
+        out, lse = uz.tree_attention(want, plain)
+        got, got_lse = uz.tree_attention(odd(want), cache, out=odd(torch.empty_like(q)))
+        assert torch.equal(got, out) and torch.equal(got_lse, lse)
+        mass = uz.attention_mass(want, plain, lse)
+        assert torch.equal(uz.attention_mass(odd(want), cache, lse, mass=odd(torch.zeros_like(mass))), mass)
+    many = randn(g, 1, 40, 4, 128, dtype=BF)  # many rows: pages by tensor maps
+    lengths.fill_(20)
+    assert torch.equal(uz.tree_attention(odd(many), cache)[0], uz.tree_attention(many, plain)[0])
+    assert torch.equal(uz.evict(cache, mass, 1).k, uz.evict(plain, mass, 1).k)
+    one = odd(torch.empty(1, 1, 1, 128, dtype=BF, device=DEV))
+    assert torch.equal(uz.evict(cache, mass, 1, out_k=one, out_v=odd(torch.empty_like(one))).k, uz.evict(plain, mass, 1).k)
