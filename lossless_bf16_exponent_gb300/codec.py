@@ -32,16 +32,29 @@ def _sp(device=None) -> int:
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
+def _index(t: torch.Tensor) -> int:
+    """Index of a tensor's device (of the current one for pinned host memory)."""
+    i = t.device.index
+    return _current_device() if i is None else i
+
+
+def _with_device(index: int, f, *args) -> int:
+    """``f(*args)`` with device ``index`` current."""
+    if index == _current_device():
+        return f(*args)
+    with torch.cuda.device(index):
+        return f(*args)
+
+
 def _call(index: int, f, *args) -> None:
     """Call the library's ``f(*args, stream)`` for tensors of device ``index``,
     on that device's current stream and with that device current: the library
     launches on, and asks about, the current device, and the handle of a default
     stream is the same for every device."""
-    if index == _current_device():
+    if index == _current_device():  # calls of a few microseconds: no layer more than it takes
         rc = f(*args, _sp(index))
     else:
-        with torch.cuda.device(index):
-            rc = f(*args, _sp(index))
+        rc = _with_device(index, f, *args, _sp(index))
     if rc:
         check(rc, f.__name__)
 
@@ -127,7 +140,7 @@ def calibrate(sample: torch.Tensor, codebook: torch.Tensor | None = None) -> tor
     calibration, SplitZip §3.3). Returns the 4096-byte device codebook."""
     s = _flat16(sample)
     cb = new_codebook(s.device) if codebook is None else _cb(codebook)
-    check(load().uzip_calibrate(_p(s), s.numel(), _p(cb), _sp(s.device)), "uzip_calibrate")
+    _call(_index(s), load().uzip_calibrate, _p(s), s.numel(), _p(cb))
     return cb
 
 
@@ -137,7 +150,7 @@ def codebook_from_exps(exps, device="cuda", codebook: torch.Tensor | None = None
         raise ValueError("need 16 exponents")
     arr = (ctypes.c_uint8 * 16)(*vals)
     cb = new_codebook(device) if codebook is None else _cb(codebook)
-    check(load().uzip_codebook_from_exps(arr, _p(cb), _sp(cb.device)), "uzip_codebook_from_exps")
+    _call(_index(cb), load().uzip_codebook_from_exps, arr, _p(cb))
     return cb
 
 
@@ -179,10 +192,9 @@ def encode(x: torch.Tensor, codebook: torch.Tensor, chunk: int = 1024, out: torc
     if workspace is None:
         workspace = torch.empty(max(16, workspace_bytes(n, chunk)), dtype=torch.uint8, device=v.device)
     nbytes = ctypes.c_size_t(0)
-    L = load()
     args = (_p(v), n, chunk, _p(_cb(codebook)), _p(_dev(out, "out")), _nbytes(out),
             _p(_dev(workspace, "workspace")), _nbytes(workspace), ctypes.byref(nbytes) if sync else None)
-    check(L.uzip_encode(*args, _sp(v.device)), "uzip_encode")
+    _call(_index(v), load().uzip_encode, *args)
     return out, (nbytes.value if sync else None)
 
 
@@ -200,7 +212,7 @@ def encode_dynamic(x: torch.Tensor, chunk: int = 1024, codebook: torch.Tensor | 
     nbytes = ctypes.c_size_t(0)
     args = (_p(v), n, chunk, _p(cb), _p(_dev(out, "out")), _nbytes(out), _p(_dev(workspace, "workspace")),
             _nbytes(workspace), ctypes.byref(nbytes) if sync else None)
-    check(load().uzip_encode_dynamic(*args, _sp(v.device)), "uzip_encode_dynamic")
+    _call(_index(v), load().uzip_encode_dynamic, *args)
     return out, (nbytes.value if sync else None), cb
 
 
@@ -212,8 +224,7 @@ def decode(stream: torch.Tensor, n: int, out: torch.Tensor | None = None, status
         out = torch.empty(n, dtype=dtype, device=stream.device)
     o = _out_values(out, n, _flat16) if n else out
     nb = _stream_nbytes(stream, stream_bytes)
-    check(load().uzip_decode(_p(stream), nb, _p(o) if n else None, n, _status(status), _sp(stream.device)),
-          "uzip_decode")
+    _call(_index(stream), load().uzip_decode, _p(stream), nb, _p(o) if n else None, n, _status(status))
     return out
 
 
@@ -234,14 +245,14 @@ def stream_copy(src: torch.Tensor, dst: torch.Tensor, capacity: int | None = Non
         raise ValueError("copied: expected a contiguous int64 tensor of one element")
     dev = src.device if src.is_cuda else dst.device
     s = stream if stream is not None else torch.cuda.current_stream(dev)
-    check(load().uzip_stream_copy(_p(src), _p(dst), cap, _p(copied), ctypes.c_void_p(s.cuda_stream)),
-          "uzip_stream_copy")
+    check(_with_device(s.device.index, load().uzip_stream_copy, _p(src), _p(dst), cap, _p(copied),
+                       ctypes.c_void_p(s.cuda_stream)), "uzip_stream_copy")
 
 
 def stream_info(stream: torch.Tensor, stream_bytes: int | None = None) -> dict:
     info = _lib.Info()
     nb = _stream_nbytes(stream, stream_bytes)
-    rc = load().uzip_stream_info(_p(stream), nb, ctypes.byref(info), _sp(stream.device))
+    rc = _with_device(_index(stream), load().uzip_stream_info, _p(stream), nb, ctypes.byref(info), _sp(stream.device))
     d = {f: getattr(info, f) for f, _ in _lib.Info._fields_ if f != "exps"}
     d["exps"] = list(info.exps)
     d["status"] = rc
@@ -277,7 +288,7 @@ def e5m2_calibrate(sample: torch.Tensor, codebook: torch.Tensor | None = None) -
     """Codebook from E5M2 values (SplitZip §4.2 / appendix C)."""
     s = _flat8(sample)
     cb = new_codebook(s.device) if codebook is None else _cb(codebook)
-    check(load().uzip_e5m2_calibrate(_p(s), s.numel(), _p(cb), _sp(s.device)), "uzip_e5m2_calibrate")
+    _call(_index(s), load().uzip_e5m2_calibrate, _p(s), s.numel(), _p(cb))
     return cb
 
 
@@ -297,7 +308,7 @@ def e5m2_encode(x: torch.Tensor, codebook: torch.Tensor, chunk: int = 1024, out:
     nbytes = ctypes.c_size_t(0)
     args = (_p(v), n, chunk, _p(_cb(codebook)), _p(_dev(out, "out")), _nbytes(out),
             _p(_dev(workspace, "workspace")), _nbytes(workspace), ctypes.byref(nbytes) if sync else None)
-    check(load().uzip_e5m2_encode(*args, _sp(v.device)), "uzip_e5m2_encode")
+    _call(_index(v), load().uzip_e5m2_encode, *args)
     return out, (nbytes.value if sync else None)
 
 
@@ -308,8 +319,7 @@ def e5m2_decode(stream: torch.Tensor, n: int, out: torch.Tensor | None = None, s
         out = torch.empty(max(n, 1), dtype=torch.uint8, device=stream.device)[:n]
     o = _out_values(out, n, _flat8) if n else out
     nb = _stream_nbytes(stream, stream_bytes)
-    check(load().uzip_e5m2_decode(_p(stream), nb, _p(o) if n else None, n, _status(status), _sp(stream.device)),
-          "uzip_e5m2_decode")
+    _call(_index(stream), load().uzip_e5m2_decode, _p(stream), nb, _p(o) if n else None, n, _status(status))
     return out
 
 
@@ -318,7 +328,7 @@ def e5m2_decode(stream: torch.Tensor, n: int, out: torch.Tensor | None = None, s
 def make_sentinel(codebook: torch.Tensor) -> torch.Tensor:
     """Turn a codebook into the Top-15 + sentinel codebook of its first 15
     exponents, in place (SplitZip §3.4, Table 6)."""
-    check(load().uzip_codebook_make_sentinel(_p(_cb(codebook)), _sp(codebook.device)), "uzip_codebook_make_sentinel")
+    _call(_index(codebook), load().uzip_codebook_make_sentinel, _p(_cb(codebook)))
     return codebook
 
 
@@ -338,7 +348,7 @@ def sentinel_encode(x: torch.Tensor, codebook: torch.Tensor, chunk: int = 1024, 
     nbytes = ctypes.c_size_t(0)
     args = (_p(v), n, chunk, _p(_cb(codebook)), _p(_dev(out, "out")), _nbytes(out),
             _p(_dev(workspace, "workspace")), _nbytes(workspace), ctypes.byref(nbytes) if sync else None)
-    check(load().uzip_sentinel_encode(*args, _sp(v.device)), "uzip_sentinel_encode")
+    _call(_index(v), load().uzip_sentinel_encode, *args)
     return out, (nbytes.value if sync else None)
 
 
@@ -349,7 +359,5 @@ def sentinel_decode(stream: torch.Tensor, n: int, out: torch.Tensor | None = Non
         out = torch.empty(max(n, 1), dtype=torch.bfloat16, device=stream.device)[:n]
     o = _out_values(out, n, _flat16) if n else out
     nb = _stream_nbytes(stream, stream_bytes)
-    check(load().uzip_sentinel_decode(_p(stream), nb, _p(o) if n else None, n, _status(status),
-                                      _sp(stream.device)),
-          "uzip_sentinel_decode")
+    _call(_index(stream), load().uzip_sentinel_decode, _p(stream), nb, _p(o) if n else None, n, _status(status))
     return out

@@ -82,6 +82,11 @@ def send_compressed(x: torch.Tensor, codebook: torch.Tensor, chunk: int = 1024, 
     tensor (bit-identical to ``x``) and the device-timed transfer."""
     if link not in ("host", "d2d"):
         raise ValueError("link must be 'host' or 'd2d'")
+    with torch.cuda.device(_flat16(x).device):  # the library launches on the current device
+        return _send_compressed(x, codebook, chunk, pieces, link, out)
+
+
+def _send_compressed(x, codebook, chunk, pieces, link, out) -> tuple[torch.Tensor, Transfer]:
     v = _flat16(x).reshape(-1)
     dev = v.device
     n = v.numel()
