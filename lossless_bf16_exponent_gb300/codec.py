@@ -32,31 +32,19 @@ def _sp(device=None) -> int:
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _index(t: torch.Tensor) -> int:
-    """Index of a tensor's device (of the current one for pinned host memory)."""
-    i = t.device.index
-    return _current_device() if i is None else i
+def _at(index: int | None, f):
+    """The library's ``f`` for tensors of device ``index`` (None: pinned host
+    memory): called with that device current, because the library launches on,
+    and asks about, the current device (the handle of a default stream is the
+    same for every device)."""
+    if index is None or index == _current_device():
+        return f
 
+    def there(*args):
+        with torch.cuda.device(index):
+            return f(*args)
 
-def _with_device(index: int, f, *args) -> int:
-    """``f(*args)`` with device ``index`` current."""
-    if index == _current_device():
-        return f(*args)
-    with torch.cuda.device(index):
-        return f(*args)
-
-
-def _call(index: int, f, *args) -> None:
-    """Call the library's ``f(*args, stream)`` for tensors of device ``index``,
-    on that device's current stream and with that device current: the library
-    launches on, and asks about, the current device, and the handle of a default
-    stream is the same for every device."""
-    if index == _current_device():  # calls of a few microseconds: no layer more than it takes
-        rc = f(*args, _sp(index))
-    else:
-        rc = _with_device(index, f, *args, _sp(index))
-    if rc:
-        check(rc, f.__name__)
+    return there
 
 
 def _p(t: torch.Tensor | None):
@@ -140,7 +128,7 @@ def calibrate(sample: torch.Tensor, codebook: torch.Tensor | None = None) -> tor
     calibration, SplitZip §3.3). Returns the 4096-byte device codebook."""
     s = _flat16(sample)
     cb = new_codebook(s.device) if codebook is None else _cb(codebook)
-    _call(_index(s), load().uzip_calibrate, _p(s), s.numel(), _p(cb))
+    check(_at(s.device.index, load().uzip_calibrate)(_p(s), s.numel(), _p(cb), _sp(s.device)), "uzip_calibrate")
     return cb
 
 
@@ -150,7 +138,7 @@ def codebook_from_exps(exps, device="cuda", codebook: torch.Tensor | None = None
         raise ValueError("need 16 exponents")
     arr = (ctypes.c_uint8 * 16)(*vals)
     cb = new_codebook(device) if codebook is None else _cb(codebook)
-    _call(_index(cb), load().uzip_codebook_from_exps, arr, _p(cb))
+    check(_at(cb.device.index, load().uzip_codebook_from_exps)(arr, _p(cb), _sp(cb.device)), "uzip_codebook_from_exps")
     return cb
 
 
@@ -194,7 +182,7 @@ def encode(x: torch.Tensor, codebook: torch.Tensor, chunk: int = 1024, out: torc
     nbytes = ctypes.c_size_t(0)
     args = (_p(v), n, chunk, _p(_cb(codebook)), _p(_dev(out, "out")), _nbytes(out),
             _p(_dev(workspace, "workspace")), _nbytes(workspace), ctypes.byref(nbytes) if sync else None)
-    _call(_index(v), load().uzip_encode, *args)
+    check(_at(v.device.index, load().uzip_encode)(*args, _sp(v.device)), "uzip_encode")
     return out, (nbytes.value if sync else None)
 
 
@@ -212,7 +200,7 @@ def encode_dynamic(x: torch.Tensor, chunk: int = 1024, codebook: torch.Tensor | 
     nbytes = ctypes.c_size_t(0)
     args = (_p(v), n, chunk, _p(cb), _p(_dev(out, "out")), _nbytes(out), _p(_dev(workspace, "workspace")),
             _nbytes(workspace), ctypes.byref(nbytes) if sync else None)
-    _call(_index(v), load().uzip_encode_dynamic, *args)
+    check(_at(v.device.index, load().uzip_encode_dynamic)(*args, _sp(v.device)), "uzip_encode_dynamic")
     return out, (nbytes.value if sync else None), cb
 
 
@@ -224,7 +212,8 @@ def decode(stream: torch.Tensor, n: int, out: torch.Tensor | None = None, status
         out = torch.empty(n, dtype=dtype, device=stream.device)
     o = _out_values(out, n, _flat16) if n else out
     nb = _stream_nbytes(stream, stream_bytes)
-    _call(_index(stream), load().uzip_decode, _p(stream), nb, _p(o) if n else None, n, _status(status))
+    check(_at(stream.device.index, load().uzip_decode)(_p(stream), nb, _p(o) if n else None, n, _status(status),
+                                                 _sp(stream.device)), "uzip_decode")
     return out
 
 
@@ -245,14 +234,14 @@ def stream_copy(src: torch.Tensor, dst: torch.Tensor, capacity: int | None = Non
         raise ValueError("copied: expected a contiguous int64 tensor of one element")
     dev = src.device if src.is_cuda else dst.device
     s = stream if stream is not None else torch.cuda.current_stream(dev)
-    check(_with_device(s.device.index, load().uzip_stream_copy, _p(src), _p(dst), cap, _p(copied),
-                       ctypes.c_void_p(s.cuda_stream)), "uzip_stream_copy")
+    check(_at(s.device.index, load().uzip_stream_copy)(_p(src), _p(dst), cap, _p(copied),
+                                                       ctypes.c_void_p(s.cuda_stream)), "uzip_stream_copy")
 
 
 def stream_info(stream: torch.Tensor, stream_bytes: int | None = None) -> dict:
     info = _lib.Info()
     nb = _stream_nbytes(stream, stream_bytes)
-    rc = _with_device(_index(stream), load().uzip_stream_info, _p(stream), nb, ctypes.byref(info), _sp(stream.device))
+    rc = _at(stream.device.index, load().uzip_stream_info)(_p(stream), nb, ctypes.byref(info), _sp(stream.device))
     d = {f: getattr(info, f) for f, _ in _lib.Info._fields_ if f != "exps"}
     d["exps"] = list(info.exps)
     d["status"] = rc
@@ -288,7 +277,7 @@ def e5m2_calibrate(sample: torch.Tensor, codebook: torch.Tensor | None = None) -
     """Codebook from E5M2 values (SplitZip §4.2 / appendix C)."""
     s = _flat8(sample)
     cb = new_codebook(s.device) if codebook is None else _cb(codebook)
-    _call(_index(s), load().uzip_e5m2_calibrate, _p(s), s.numel(), _p(cb))
+    check(_at(s.device.index, load().uzip_e5m2_calibrate)(_p(s), s.numel(), _p(cb), _sp(s.device)), "uzip_e5m2_calibrate")
     return cb
 
 
@@ -308,7 +297,7 @@ def e5m2_encode(x: torch.Tensor, codebook: torch.Tensor, chunk: int = 1024, out:
     nbytes = ctypes.c_size_t(0)
     args = (_p(v), n, chunk, _p(_cb(codebook)), _p(_dev(out, "out")), _nbytes(out),
             _p(_dev(workspace, "workspace")), _nbytes(workspace), ctypes.byref(nbytes) if sync else None)
-    _call(_index(v), load().uzip_e5m2_encode, *args)
+    check(_at(v.device.index, load().uzip_e5m2_encode)(*args, _sp(v.device)), "uzip_e5m2_encode")
     return out, (nbytes.value if sync else None)
 
 
@@ -319,7 +308,8 @@ def e5m2_decode(stream: torch.Tensor, n: int, out: torch.Tensor | None = None, s
         out = torch.empty(max(n, 1), dtype=torch.uint8, device=stream.device)[:n]
     o = _out_values(out, n, _flat8) if n else out
     nb = _stream_nbytes(stream, stream_bytes)
-    _call(_index(stream), load().uzip_e5m2_decode, _p(stream), nb, _p(o) if n else None, n, _status(status))
+    check(_at(stream.device.index, load().uzip_e5m2_decode)(_p(stream), nb, _p(o) if n else None, n, _status(status),
+                                                      _sp(stream.device)), "uzip_e5m2_decode")
     return out
 
 
@@ -328,7 +318,8 @@ def e5m2_decode(stream: torch.Tensor, n: int, out: torch.Tensor | None = None, s
 def make_sentinel(codebook: torch.Tensor) -> torch.Tensor:
     """Turn a codebook into the Top-15 + sentinel codebook of its first 15
     exponents, in place (SplitZip §3.4, Table 6)."""
-    _call(_index(codebook), load().uzip_codebook_make_sentinel, _p(_cb(codebook)))
+    check(_at(codebook.device.index, load().uzip_codebook_make_sentinel)(_p(_cb(codebook)), _sp(codebook.device)),
+          "uzip_codebook_make_sentinel")
     return codebook
 
 
@@ -348,7 +339,7 @@ def sentinel_encode(x: torch.Tensor, codebook: torch.Tensor, chunk: int = 1024, 
     nbytes = ctypes.c_size_t(0)
     args = (_p(v), n, chunk, _p(_cb(codebook)), _p(_dev(out, "out")), _nbytes(out),
             _p(_dev(workspace, "workspace")), _nbytes(workspace), ctypes.byref(nbytes) if sync else None)
-    _call(_index(v), load().uzip_sentinel_encode, *args)
+    check(_at(v.device.index, load().uzip_sentinel_encode)(*args, _sp(v.device)), "uzip_sentinel_encode")
     return out, (nbytes.value if sync else None)
 
 
@@ -359,5 +350,6 @@ def sentinel_decode(stream: torch.Tensor, n: int, out: torch.Tensor | None = Non
         out = torch.empty(max(n, 1), dtype=torch.bfloat16, device=stream.device)[:n]
     o = _out_values(out, n, _flat16) if n else out
     nb = _stream_nbytes(stream, stream_bytes)
-    _call(_index(stream), load().uzip_sentinel_decode, _p(stream), nb, _p(o) if n else None, n, _status(status))
+    check(_at(stream.device.index, load().uzip_sentinel_decode)(_p(stream), nb, _p(o) if n else None, n, _status(status),
+                                                          _sp(stream.device)), "uzip_sentinel_decode")
     return out

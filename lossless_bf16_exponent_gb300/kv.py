@@ -26,7 +26,8 @@ import torch
 from torch.autograd.graph import increment_version
 
 from . import _lib, codec
-from .codec import _call, _sp, load
+from ._lib import check, load
+from .codec import _at, _sp
 
 # Calls of a few microseconds on the GPU are bound by the host: each call looks
 # every attribute up once, and tensors go to the C ABI as packed structures.
@@ -65,23 +66,22 @@ def _rows(x: torch.Tensor, what: str) -> bytes:
     return _pack_rows(x.data_ptr(), sb, st, sh)
 
 
-def _writable(x: torch.Tensor, what: str) -> torch.Tensor:
-    """An output: no two of its elements in one place."""
+def _writable(x: torch.Tensor, what: str) -> None:
+    """Check an output: no two of its elements in one place."""
+    expect = 1
+    for n, s in zip(reversed(x.shape), reversed(x.stride())):  # dimensions in their usual order
+        if n > 1:
+            if s < expect:
+                break
+            expect += s * (n - 1)
+    else:
+        return
     expect = 1
     for n, s in sorted(zip(x.shape, x.stride()), key=lambda v: v[1]):
-        if n > 1 and s < expect:
-            raise ValueError(f"{what}: its elements overlap")
         if n > 1:
-            expect = s * (n - 1) + expect
-    return x
-
-
-def _bytes_of(shape, stride, size: int) -> int:
-    """Bytes from a tensor's first element to the end of its last."""
-    end = 1
-    for n, s in zip(shape, stride):
-        end += (n - 1) * s
-    return end * size
+            if s < expect:
+                raise ValueError(f"{what}: its elements overlap")
+            expect += s * (n - 1)
 
 
 def _overlap(x: torch.Tensor, y: torch.Tensor) -> bool:
@@ -89,16 +89,25 @@ def _overlap(x: torch.Tensor, y: torch.Tensor) -> bool:
     x0, y0 = x.data_ptr(), y.data_ptr()
     if y0 < x0:
         x, y, x0, y0 = y, x, y0, x0
-    if y0 - x0 >= _bytes_of(x.shape, x.stride(), x.element_size()) or not x.numel() or not y.numel():
+    end = 1
+    for n, s in zip(x.shape, x.stride()):
+        end += (n - 1) * s
+    if y0 - x0 >= end * x.element_size() or not x.numel() or not y.numel():
         return False
-    # Heads side by side in one projection: what the last two dimensions span repeats at multiples of g only.
-    g = 0
+    # What the last two dimensions span repeats at multiples of g only: heads side by side in one projection.
+    g, spans = 0, []
     for t in (x, y):
-        for n, s in zip(t.shape[:-2], t.stride()[:-2]):
+        size = t.element_size()
+        wide = size  # bytes to the end of the last two dimensions
+        behind = t.dim() - 2
+        for i, (n, s) in enumerate(zip(t.shape, t.stride())):
             if n > 1:
-                g = math.gcd(g, s * t.element_size())
-    wide, tall = (_bytes_of(t.shape[-2:], t.stride()[-2:], t.element_size()) for t in (x, y))
-    if g and wide <= (y0 - x0) % g <= g - tall:
+                if i < behind:
+                    g = math.gcd(g, s * size)
+                else:
+                    wide += (n - 1) * s * size
+        spans.append(wide)
+    if g and spans[0] <= (y0 - x0) % g <= g - spans[1]:
         return False
     # x0 + sum of i s = y0 + sum of j t over x's and y's indexes i, j, strides s, t in bytes and the bytes of an element:
     # one equation in bounded integers, solved from the largest stride down.
@@ -134,29 +143,31 @@ def _overlap(x: torch.Tensor, y: torch.Tensor) -> bool:
     return reach(0, y0 - x0)
 
 
-def _apart(out: torch.Tensor, what: str, x: torch.Tensor, name: str, in_place: bool = False) -> None:
-    """Refuse an output that shares memory with something the call reads or
-    writes; ``in_place``: other than element for element."""
-    if in_place and (out is x or (out.data_ptr() == x.data_ptr() and out.shape == x.shape and out.dtype == x.dtype and all(
-            n == 1 or s == t for n, s, t in zip(x.shape, out.stride(), x.stride())))):
-        return
-    if _overlap(out, x):
-        raise ValueError(f"{what}: overlaps {name}" + (" without being it" if in_place else ""))
-
-
 def _no_gradient(what: str, *tensors) -> None:
     """Refuse tensors whose gradient would be cut without a word."""
     if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
         raise ValueError(f"{what}: has no gradient; call it under torch.no_grad() or on detached tensors")
 
 
-def _given(out: torch.Tensor, what: str) -> torch.Tensor:
-    """Check a caller's output, which is written past autograd's knowledge: what was saved of it is no longer valid."""
+def _given(out: torch.Tensor, what: str, *apart, in_place=None) -> None:
+    """Check a caller's output, which is written past autograd's knowledge: what
+    was saved of it is no longer valid. It shares no memory with the ``apart``
+    (tensor, name), nor with the one ``in_place``, unless it is that one element
+    for element: the call reads them while it writes."""
     _writable(out, what)
     if out.requires_grad:
         _no_gradient(what, out)
-    increment_version(out)
-    return out
+    storage = out.untyped_storage().data_ptr()
+    for x, name in apart if in_place is None else (in_place, *apart):
+        if x.untyped_storage().data_ptr() != storage:
+            continue
+        if in_place is not None and x is in_place[0] and (out is x or (
+                out.data_ptr() == x.data_ptr() and out.shape == x.shape
+                and all(n == 1 or s == t for n, s, t in zip(x.shape, out.stride(), x.stride())))):
+            continue
+        if _overlap(out, x):
+            raise ValueError(f"{what}: overlaps {name}")
+    increment_version((out,))
 
 
 # ----------------------------------------------------------------- rotary
@@ -292,14 +303,15 @@ def _rotate(x, positions, plan, out, backward):
         out = torch.empty((b, t, heads, d), dtype=x.dtype, device=plan.device)
         ro = _pack_rows(out.data_ptr(), t * heads * d, heads * d, d)
     else:
-        _given(_tensor(out, "out", x.dtype, shape, x.device), "out")
-        _apart(out, "out", x, "x", in_place=True)
+        _given(_tensor(out, "out", x.dtype, shape, x.device), "out", in_place=(x, "x"))
         ro = _rows(out, "out")
     if empty:
         return out
     turns, rotary_dim, layout, magnitude = plan.args
-    _call(index, load().uzkv_rotary, rx, ro, kind, b, t, heads, d, positions.data_ptr(), step, turns, rotary_dim, layout,
-          magnitude, backward)
+    rc = _at(index, load().uzkv_rotary)(rx, ro, kind, b, t, heads, d, positions.data_ptr(), step, turns,
+        rotary_dim, layout, magnitude, backward, _sp(index))
+    if rc:
+        check(rc, "uzkv_rotary")
     return out
 
 
@@ -399,13 +411,12 @@ def _new_rows(x: torch.Tensor, what: str, cache: KVCache, heads: int | None = No
     return _pack_rows(x.data_ptr(), sb, st, sh)
 
 
-def _new_out(out: torch.Tensor | None, q: torch.Tensor, b: int, t: int, heads: int, d: int, device):
-    """The output of q's shape (a new one where None), and its rows."""
+def _new_out(out: torch.Tensor | None, q: torch.Tensor, b: int, t: int, heads: int, d: int, device, *apart):
+    """The output of q's shape (a new one where None, else q or apart from it and from ``apart``), and its rows."""
     if out is None:
         out = torch.empty((b, t, heads, d), dtype=q.dtype, device=device)
         return out, _pack_rows(out.data_ptr(), t * heads * d, heads * d, d)
-    _given(_tensor(out, "out", q.dtype, q.shape, device), "out")
-    _apart(out, "out", q, "q", in_place=True)
+    _given(_tensor(out, "out", q.dtype, q.shape, device), "out", *apart, in_place=(q, "q"))
     return out, _rows(out, "out")
 
 
@@ -438,17 +449,16 @@ def rotary_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: 
     if plan.index != index:
         raise ValueError("plan: on another device")
     step = _positions(positions, b, t, index)
-    if out is not None:
-        _apart(out, "out", k, "k")
-        _apart(out, "out", v, "v")
     if heads == 0:
         raise ValueError("q: no heads")
-    out, ro = _new_out(out, q, b, t, heads, d, cache.device)
+    out, ro = _new_out(out, q, b, t, heads, d, cache.device, (k, "k"), (v, "v"))
     if b * t == 0:
         return out
     turns, rotary_dim, layout, magnitude = plan.args
-    _call(index, load().uzkv_rotary_append, rq, rk, rv, ro, _FLOATS[dtype], t, heads, positions.data_ptr(), step, turns,
-          rotary_dim, layout, magnitude, _counts(counts, cache), cache._ref)
+    rc = _at(index, load().uzkv_rotary_append)(rq, rk, rv, ro, _FLOATS[dtype], t, heads, positions.data_ptr(),
+        step, turns, rotary_dim, layout, magnitude, _counts(counts, cache), cache._ref, _sp(index))
+    if rc:
+        check(rc, "uzkv_rotary_append")
     return out
 
 
@@ -569,15 +579,20 @@ def tree_attention(q: torch.Tensor, cache: KVCache, mask: torch.Tensor | None = 
         at_lse = lse.data_ptr()
     else:
         at_lse = _floats(lse, "lse", (b, t, heads), cache)
-        _given(lse, "lse")
+        if lse.requires_grad:
+            _no_gradient("lse", lse)
+        increment_version((lse,))
     if b == 0:
         return out, lse
     if workspace is None:
         workspace = _workspace(cache, tree_attention_workspace_bytes(cache, t, heads))
     elif not _tensor(workspace, "workspace", torch.uint8, None, cache.device).is_contiguous():
         raise ValueError("workspace: expected a contiguous tensor")
-    _call(cache.index, load().uzkv_tree_attention, rq, ro, at_lse, _FLOATS[q.dtype], t, heads, address, stride,
-          _counts(counts, cache), d ** -0.5 if scale is None else scale, cache._ref, workspace.data_ptr(), workspace.numel())
+    rc = _at(cache.index, load().uzkv_tree_attention)(rq, ro, at_lse, _FLOATS[q.dtype], t, heads, address, stride,
+        _counts(counts, cache), d ** -0.5 if scale is None else scale, cache._ref, workspace.data_ptr(),
+        workspace.numel(), _sp(cache.index))
+    if rc:
+        check(rc, "uzkv_tree_attention")
     return out, lse
 
 
@@ -605,12 +620,9 @@ def attention_mass(q: torch.Tensor, cache: KVCache, lse: torch.Tensor, mask: tor
         out = torch.empty(mass.shape if mass is not None else (b, kv_heads, cache.capacity), dtype=torch.float32,
                           device=cache.device)
     else:
-        _given(_tensor(out, "out", torch.float32, None, cache.device), "out")
-        _apart(out, "out", lse, "lse")
-        if weights is not None:
-            _apart(out, "out", weights, "weights")
-        if mass is not None:
-            _apart(out, "out", mass, "mass", in_place=True)
+        reads = [(lse, "lse")] if weights is None else [(lse, "lse"), (weights, "weights")]
+        _given(_tensor(out, "out", torch.float32, None, cache.device), "out", *reads,
+               in_place=None if mass is None else (mass, "mass"))
     shape = out.shape
     if len(shape) != 3 or shape[0] != b or shape[1] != kv_heads or not 1 <= shape[2] <= cache.capacity:
         raise ValueError(f"out: expected [{b}, {kv_heads}, 1 to {cache.capacity}], got {tuple(shape)}")
@@ -626,9 +638,11 @@ def attention_mass(q: torch.Tensor, cache: KVCache, lse: torch.Tensor, mask: tor
         at_mass = mass.data_ptr()
     if b == 0:
         return out
-    _call(cache.index, load().uzkv_attention_mass, rq, at_lse, _FLOATS[q.dtype], t, heads, address, stride,
-          _counts(counts, cache), at_weights, d ** -0.5 if scale is None else scale, cache._ref, at_mass, decay,
-          out.data_ptr(), sb, sh, shape[2])
+    rc = _at(cache.index, load().uzkv_attention_mass)(rq, at_lse, _FLOATS[q.dtype], t, heads, address, stride,
+        _counts(counts, cache), at_weights, d ** -0.5 if scale is None else scale, cache._ref, at_mass, decay,
+        out.data_ptr(), sb, sh, shape[2], _sp(cache.index))
+    if rc:
+        check(rc, "uzkv_attention_mass")
     return out
 
 
@@ -676,19 +690,21 @@ def evict(cache: KVCache, mass: torch.Tensor, keep: int, sink: int = 0, recent: 
     elif out_k is None or out_v is None:
         raise ValueError("give both out_k and out_v or neither")
     else:
+        pools = (cache.k, "the cache"), (cache.v, "the cache")
         for x, what in ((out_k, "out_k"), (out_v, "out_v")):
-            _given(_tensor(x, what, cache.dtype, (b, heads, keep, d), device), what)
-            _apart(x, what, cache.k, "the cache")
-            _apart(x, what, cache.v, "the cache")
-        _apart(out_k, "out_k", out_v, "out_v")
+            _tensor(x, what, cache.dtype, (b, heads, keep, d), device)
+        _given(out_k, "out_k", *pools, (out_v, "out_v"))
+        _given(out_v, "out_v", *pools)
         rk, rv = _rows(out_k, "out_k"), _rows(out_v, "out_v")
     kept = torch.empty((b, heads, keep), dtype=torch.int32, device=device)
     mass_out = torch.empty((b, heads, keep), dtype=torch.float32, device=device)
     lengths = torch.empty((b,), dtype=torch.int32, device=device)
     if b == 0:
         return Packed(out_k, out_v, mass_out, kept, lengths)
-    _call(cache.index, load().uzkv_evict, cache._ref, mass.data_ptr(), sb, sh, shape[2], keep, sink, recent, rk, rv,
-          kept.data_ptr(), mass_out.data_ptr(), lengths.data_ptr())
+    rc = _at(cache.index, load().uzkv_evict)(cache._ref, mass.data_ptr(), sb, sh, shape[2], keep, sink, recent,
+        rk, rv, kept.data_ptr(), mass_out.data_ptr(), lengths.data_ptr(), _sp(cache.index))
+    if rc:
+        check(rc, "uzkv_evict")
     return Packed(out_k, out_v, mass_out, kept, lengths)
 
 

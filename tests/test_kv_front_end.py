@@ -83,7 +83,7 @@ class Bench:
         monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", capturing)
         monkeypatch.setattr(torch, "empty", empty)
         self.bumped = []
-        monkeypatch.setattr(kv, "increment_version", self.bumped.append, raising=False)
+        monkeypatch.setattr(kv, "increment_version", self.bumped.extend, raising=False)
 
 
 @pytest.fixture
