@@ -5,7 +5,8 @@ import math
 import pytest
 import torch
 
-from test_gpu_kv import BF, DEV, E5, F32, HF, cached, check_attention, evict_want, gen, make_cache, randn, random_tree, raw  # noqa: F401
+import test_gpu_kv as K
+from test_gpu_kv import BF, DEV, E5, HF, check_attention, gen, make_cache, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -119,3 +120,54 @@ def test_strides_of_dimensions_of_one_do_not_count(uz):
     assert torch.equal(uz.evict(cache, mass, 1).k, uz.evict(plain, mass, 1).k)
     one = odd(torch.empty(1, 1, 1, 128, dtype=BF, device=DEV))
     assert torch.equal(uz.evict(cache, mass, 1, out_k=one, out_v=odd(torch.empty_like(one))).k, uz.evict(plain, mass, 1).k)
+
+
+# --------------------------------------- variants that the other sizes do not reach
+
+WIDE = [  # heads above 128: lengths, t, hq, hk, d, page; up to 16 rows, up to 32, more; mass in one chunk and in several
+    ([300, 5, 0], 1, 8, 2, 256, 16), ([77, 400], 3, 10, 2, 192, 48), ([129], 2, 2, 1, 144, 400), ([64, 63, 1], 1, 16, 1, 160, 7),
+    ([90, 257], 9, 8, 4, 256, 7), ([500], 4, 16, 2, 176, 64), ([33], 32, 2, 2, 144, 16), ([1000, 31], 5, 12, 2, 256, 64),
+    ([260, 3], 40, 16, 4, 256, 64), ([129], 150, 2, 1, 192, 16), ([70], 256, 2, 1, 144, 32)]
+
+
+@pytest.mark.parametrize("q_type,c_type", K.TYPES)
+@pytest.mark.parametrize("lens,t,hq,hk,d,page", WIDE)
+def test_wide_heads(uz, lens, t, hq, hk, d, page, q_type, c_type):
+    K.test_attention(uz, lens, t, hq, hk, d, page, q_type, c_type)
+    K.test_mass(uz, lens, t, hq, hk, d, page, q_type, c_type)
+
+
+@pytest.mark.parametrize("q_type,c_type", [(BF, BF), (HF, HF)])
+@pytest.mark.parametrize("lens,t,hq,hk,d,page", [([300, 17], 1, 4, 2, 136, 16), ([200], 6, 8, 2, 248, 64), ([65], 70, 2, 1, 200, 24)])
+def test_wide_heads_off_sixteen(uz, lens, t, hq, hk, d, page, q_type, c_type):
+    test_wide_heads(uz, lens, t, hq, hk, d, page, q_type, c_type)
+
+
+@pytest.mark.parametrize("kind", ["many ties", "spread", "equal", "odd values"])
+def test_evict_of_rows_longer_than_shared_memory(uz, kind):
+    """So many rows that each has one CTA, of more slots than it holds keys for: masses are read again each pass."""
+    lens = [30000, 23553, 29999, 100, 0, 24001, 26000] + [23600 + 31 * i for i in range(13)]
+    assert len(lens) * 4 * 2 > torch.cuda.get_device_properties(0).multi_processor_count
+    K.test_evict(uz, lens, 2000, 4, 100, 4, 16, 4096, kind, BF)
+
+
+# ------------------------------------------------------------ eviction and the codec
+
+@pytest.mark.parametrize("c_type", [BF, HF, E5])
+def test_packed_caches_go_through_the_codec(uz, c_type):
+    """Each type's own encoder: e5m2_encode for E5M2, encode for the 16-bit ones; every bit comes back."""
+    g = gen(6)
+    cache = make_cache(uz, g, [700, 500], 0, 2, 64, 16, c_type)
+    mass = torch.rand(2, 2, cache.capacity, generator=g, device=DEV)
+    both = torch.empty(2, 2, 2, 128, 64, dtype=c_type, device=DEV)
+    uz.evict(cache, mass, 128, sink=4, recent=32, out_k=both[0], out_v=both[1])
+    want = both.view(torch.uint8).flatten()
+    if c_type == E5:
+        stream, n = uz.e5m2_encode(both, uz.e5m2_calibrate(both))
+        got = uz.e5m2_decode(stream, both.numel(), stream_bytes=n)
+    else:
+        stream, n = uz.encode(both, uz.calibrate(both))
+        got = uz.decode(stream, both.numel(), stream_bytes=n, dtype=c_type).view(torch.uint8)
+    assert torch.equal(got.flatten(), want)
+    if c_type != HF:  # FP16's five exponent bits are not where the codebook of bfloat16's eight looks
+        assert n < want.numel()
