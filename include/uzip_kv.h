@@ -6,7 +6,7 @@
  *
  * Conventions are those of uzip.h: d_* is device memory of the caller, the
  * library allocates nothing and keeps nothing between calls, work is enqueued
- * on `stream` and is asynchronous, errors found on the host return at once
+ * on `stream`, a stream of the current device, and is asynchronous, errors found on the host return at once
  * (enum uzip_status) and enqueue nothing.
  *
  * One layer's cache is two pools of pages, K and V, of shape
@@ -23,9 +23,11 @@
  * page numbers of tokens in use below `pages`. A cache that breaks one is read
  * and written as far as it is in bounds (lengths and counts are clamped, a
  * page that does not exist reads as zeros and is not written), its outputs are
- * not trustworthy, and *d_status, if given, is set to UZIP_ERR_CORRUPT. Waits
- * inside a kernel are bounded; if one ran out, which no input brings about, it
- * is set to UZIP_ERR_TIMEOUT. No call sets it to anything else, or clears it.
+ * not trustworthy, and *d_status, if given, is set to UZIP_ERR_CORRUPT. Attention
+ * and mass wait on barriers in shared memory, each wait bounded; if one ran out,
+ * which no input brings about, it is set to UZIP_ERR_TIMEOUT. (The other kernels
+ * meet at the hardware's own barriers only.) No call sets it to anything else, or
+ * clears it.
  */
 #ifndef UZIP_KV_H
 #define UZIP_KV_H

@@ -109,11 +109,6 @@ __device__ __forceinline__ char* v_row(const Cache& c, Place p, uint32_t h) {
     return c.v + p.page * c.v_page + h * c.v_head + p.row * c.v_token;
 }
 
-// Whether new token t sees new token u.
-__device__ __forceinline__ bool mask_bit(const int64_t* row, uint32_t t, uint32_t u) {
-    return row ? (row[u >> 6] >> (u & 63)) & 1 : u <= t;
-}
-
 inline uint32_t bytes_of(uint32_t dtype) { return dtype == UZKV_FP32 ? 4 : dtype == UZKV_E5M2 ? 1 : 2; }
 
 // The rows of b x t x h of them. A stride along a dimension of one is nothing: no alignment is asked of it.

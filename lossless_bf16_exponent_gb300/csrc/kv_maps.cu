@@ -27,7 +27,7 @@ Encode encoder() {
 
 bool maps_of(const AttParams& p, const uzkv_cache_t* c, uint32_t tile, uint32_t least, Maps* m) {
     const uint32_t box = std::min(c->page_tokens & (0u - c->page_tokens), tile);  // largest power of two in both
-        const uint32_t row = c->head_dim * bytes_of(c->dtype), wide = c->dtype == UZKV_E5M2 && c->head_dim <= 64 ? 64 : 128;
+    const uint32_t row = c->head_dim * bytes_of(c->dtype), wide = c->dtype == UZKV_E5M2 && c->head_dim <= 64 ? 64 : 128;
     if (box < 8 || box * wide < least || !encoder()) return false;
     m->box = box;
     const cuuint64_t dims[4] = {row, c->page_tokens, c->kv_heads, c->pages};

@@ -30,9 +30,6 @@ struct Maps {
 // mass, rows of 128, 8 KB 90 / 96 us; E5M2 of 64, 4 KB 21.9 / 24.5, 1 KB 27.1 / 24.9 us.
 bool maps_of(const AttParams& p, const uzkv_cache_t* c, uint32_t tile, uint32_t least, Maps* m);
 
-__device__ __forceinline__ void tma_fetch_map(const CUtensorMap* m) {
-    asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
-}
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* m, uint32_t x, uint32_t row, uint32_t head, uint32_t page,
                                         uint32_t bar) {
     asm volatile(

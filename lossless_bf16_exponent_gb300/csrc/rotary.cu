@@ -13,8 +13,8 @@
 // into shared memory, then walks the tokens' rows front to back, so that the
 // grid reads and writes a few compact streams. A thread moves two vectors at
 // once: the two halves of V pairs (half layout), 2 V adjacent elements
-// (interleaved) or 2 V elements that are only copied; four such items are
-// loaded before the first is stored, the first of them before the angles are
+// (interleaved) or 2 V elements that are only copied; two such items are
+// loaded before the first is stored, the CTA's first ones before the angles are
 // computed. V is the widest of 16 bytes, 8 bytes and one element that the
 // rotary dimension, strides and addresses allow.
 // Measured: 16,388 tokens of 72 heads of 128, BF16: 98 us, 6.2 TB/s, 91 % of the measured copy rate; 4,095 new
