@@ -2,12 +2,14 @@
  * uzip_kv.h -- C ABI of libuzip's operators on a KV cache: rotary positions,
  * attention for a tree of drafted tokens, the attention weight each cached
  * token collects, and eviction by that weight into a packed buffer that the
- * codec of uzip.h then encodes.
+ * codec of uzip.h then encodes: a BF16 cache by uzip_encode, an E5M2 one by
+ * uzip_e5m2_encode. FP16 has no format of its own there: uzip_encode takes its
+ * bits and gives them back, but its codebook is for BF16's exponent field.
  *
  * Conventions are those of uzip.h: d_* is device memory of the caller, the
  * library allocates nothing and keeps nothing between calls, work is enqueued
- * on `stream`, a stream of the current device, and is asynchronous, errors found on the host return at once
- * (enum uzip_status) and enqueue nothing.
+ * on `stream`, a stream of the current device, and is asynchronous, errors found
+ * on the host return at once (enum uzip_status) and enqueue nothing.
  *
  * One layer's cache is two pools of pages, K and V, of shape
  * [pages][kv_heads][page_tokens][head_dim], a page table of page numbers

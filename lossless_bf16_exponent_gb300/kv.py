@@ -1,7 +1,7 @@
 """PyTorch front end of the KV-cache operators (``include/uzip_kv.h``): rotary
 positions, attention for a tree of drafted tokens, the attention weight that
 cached tokens collect, and eviction by that weight into a packed buffer that
-:func:`encode` then takes.
+the codec then takes (:func:`encode` for bfloat16, :func:`e5m2_encode` for E5M2).
 
 As in the codec's front end, this module marshals arguments and checks what
 the C ABI cannot see (devices, types, shapes, strides); a refusal is a
@@ -667,9 +667,10 @@ def evict(cache: KVCache, mass: torch.Tensor, keep: int, sink: int = 0, recent: 
     ``sink``, the last ``recent`` and those of the largest ``mass`` (float32
     [sequences, kv heads, slots]; equal masses: the lowest slot first). A sequence
     of at most ``keep`` tokens keeps them all. ``out_k`` and ``out_v`` default to new
-    contiguous tensors, ready for :func:`encode`; given ones may be the halves of
-    one buffer or views with room behind for tokens to come, but no part of the
-    cache."""
+    contiguous tensors, ready for :func:`encode` (bfloat16) or :func:`e5m2_encode`;
+    float16 has no format of its own, ``encode`` takes its bits but its codebook is
+    for bfloat16's exponent field. Given ones may be the halves of one buffer or
+    views with room behind for tokens to come, but no part of the cache."""
     b, heads, d = cache.sequences, cache.kv_heads, cache.head_dim
     shape = mass.shape
     if mass.dtype is not torch.float32 or mass.get_device() != cache.index or len(shape) != 3 or shape[0] != b \
