@@ -109,7 +109,7 @@ UZIP_API int uzkv_rotary_append(const uzkv_rows_t *q, const uzkv_rows_t *k, cons
  * and lse = -inf. What a row does not see, NaN and infinities among it, has no
  * part in its output.
  *   q, out         [sequences][tokens][q_heads][head_dim], dtype BF16 or FP16;
- *                  16-byte aligned rows.
+ *                  16-byte aligned rows; out may be q.
  *   d_lse          NULL or [sequences][tokens][q_heads] floats, contiguous.
  *   tokens         1 .. UZKV_MAX_NEW_TOKENS; sequences * tokens * q_heads below 2^31.
  *   d_mask         NULL or [sequences][tokens][ceil(tokens / 64)] words, a

@@ -171,3 +171,17 @@ def test_packed_caches_go_through_the_codec(uz, c_type):
     assert torch.equal(got.flatten(), want)
     if c_type != HF:  # FP16's five exponent bits are not where the codebook of bfloat16's eight looks
         assert n < want.numel()
+
+
+# ------------------------------------------------------------------ outputs in place
+
+@pytest.mark.parametrize("lens,t,hq", [([20, 300], 1, 8), ([9000], 1, 8), ([700, 33], 4, 8), ([40], 30, 8), ([5000, 3], 30, 16), ([100], 200, 16)])
+def test_attention_in_place(uz, lens, t, hq):
+    """out may be q: rows are read before they are written, whoever else works on their unit."""
+    cache = make_cache(uz, gen(t), lens, t, 2, 64, 16, BF)
+    box = randn(gen(1), len(lens), t, hq + 2, 64, dtype=BF)
+    q = box[:, :, :hq]
+    want, lse = uz.tree_attention(q, cache)
+    rest = box[:, :, hq:].clone()
+    out, got = uz.tree_attention(q, cache, out=q)
+    assert out is q and torch.equal(q, want) and torch.equal(got, lse) and torch.equal(box[:, :, hq:], rest)
