@@ -308,8 +308,9 @@ def _rotate(x, positions, plan, out, backward):
     if empty:
         return out
     turns, rotary_dim, layout, magnitude = plan.args
-    rc = _at(index, load().uzkv_rotary)(rx, ro, kind, b, t, heads, d, positions.data_ptr(), step, turns,
-        rotary_dim, layout, magnitude, backward, _sp(index))
+    rc = _at(index, load().uzkv_rotary)(
+        rx, ro, kind, b, t, heads, d, positions.data_ptr(), step, turns, rotary_dim, layout, magnitude, backward,
+        _sp(index))
     if rc:
         check(rc, "uzkv_rotary")
     return out
@@ -455,8 +456,9 @@ def rotary_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: 
     if b * t == 0:
         return out
     turns, rotary_dim, layout, magnitude = plan.args
-    rc = _at(index, load().uzkv_rotary_append)(rq, rk, rv, ro, _FLOATS[dtype], t, heads, positions.data_ptr(),
-        step, turns, rotary_dim, layout, magnitude, _counts(counts, cache), cache._ref, _sp(index))
+    rc = _at(index, load().uzkv_rotary_append)(
+        rq, rk, rv, ro, _FLOATS[dtype], t, heads, positions.data_ptr(), step, turns, rotary_dim, layout, magnitude,
+        _counts(counts, cache), cache._ref, _sp(index))
     if rc:
         check(rc, "uzkv_rotary_append")
     return out
@@ -588,9 +590,9 @@ def tree_attention(q: torch.Tensor, cache: KVCache, mask: torch.Tensor | None = 
         workspace = _workspace(cache, tree_attention_workspace_bytes(cache, t, heads))
     elif not _tensor(workspace, "workspace", torch.uint8, None, cache.device).is_contiguous():
         raise ValueError("workspace: expected a contiguous tensor")
-    rc = _at(cache.index, load().uzkv_tree_attention)(rq, ro, at_lse, _FLOATS[q.dtype], t, heads, address, stride,
-        _counts(counts, cache), d ** -0.5 if scale is None else scale, cache._ref, workspace.data_ptr(),
-        workspace.numel(), _sp(cache.index))
+    rc = _at(cache.index, load().uzkv_tree_attention)(
+        rq, ro, at_lse, _FLOATS[q.dtype], t, heads, address, stride, _counts(counts, cache),
+        d ** -0.5 if scale is None else scale, cache._ref, workspace.data_ptr(), workspace.numel(), _sp(cache.index))
     if rc:
         check(rc, "uzkv_tree_attention")
     return out, lse
@@ -638,9 +640,10 @@ def attention_mass(q: torch.Tensor, cache: KVCache, lse: torch.Tensor, mask: tor
         at_mass = mass.data_ptr()
     if b == 0:
         return out
-    rc = _at(cache.index, load().uzkv_attention_mass)(rq, at_lse, _FLOATS[q.dtype], t, heads, address, stride,
-        _counts(counts, cache), at_weights, d ** -0.5 if scale is None else scale, cache._ref, at_mass, decay,
-        out.data_ptr(), sb, sh, shape[2], _sp(cache.index))
+    rc = _at(cache.index, load().uzkv_attention_mass)(
+        rq, at_lse, _FLOATS[q.dtype], t, heads, address, stride, _counts(counts, cache), at_weights,
+        d ** -0.5 if scale is None else scale, cache._ref, at_mass, decay, out.data_ptr(), sb, sh, shape[2],
+        _sp(cache.index))
     if rc:
         check(rc, "uzkv_attention_mass")
     return out
@@ -702,8 +705,9 @@ def evict(cache: KVCache, mass: torch.Tensor, keep: int, sink: int = 0, recent: 
     lengths = torch.empty((b,), dtype=torch.int32, device=device)
     if b == 0:
         return Packed(out_k, out_v, mass_out, kept, lengths)
-    rc = _at(cache.index, load().uzkv_evict)(cache._ref, mass.data_ptr(), sb, sh, shape[2], keep, sink, recent,
-        rk, rv, kept.data_ptr(), mass_out.data_ptr(), lengths.data_ptr(), _sp(cache.index))
+    rc = _at(cache.index, load().uzkv_evict)(
+        cache._ref, mass.data_ptr(), sb, sh, shape[2], keep, sink, recent, rk, rv, kept.data_ptr(), mass_out.data_ptr(),
+        lengths.data_ptr(), _sp(cache.index))
     if rc:
         check(rc, "uzkv_evict")
     return Packed(out_k, out_v, mass_out, kept, lengths)
